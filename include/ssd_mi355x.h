@@ -94,6 +94,11 @@ enum ssd_status {
  * ReplaySSM states); inputs are SSD_F32 or SSD_BF16. */
 typedef enum { SSD_F32 = 0, SSD_BF16 = 1, SSD_F16 = 2 } ssd_dtype;
 
+/* A further dtype code, of the paged key / value cache only: 8-bit floating
+ * point with 4 exponent and 3 mantissa bits (finite values and NaN, largest
+ * 448), one power-of-two scale per row (kv_cache_store). */
+#define SSD_E4M3 3
+
 /* One packed varlen prefill (host struct). */
 typedef struct {
     int32_t total_tokens; /* T: tokens of all sequences together */
@@ -572,6 +577,236 @@ int ssd_combined_varlen_noalloc(const ssd_problem *p, const void *x, const void 
                                 const int32_t *cu_seqlens, void *state_cache,
                                 const int32_t *state_indices, const uint8_t *has_initial_state,
                                 void *y, void *checkpoints, void *stream);
+
+/*
+ * Operators of the layers around the SSD scan
+ * -------------------------------------------
+ * The conventions are those of the top of this file, with these differences:
+ * - Token rows may be strided: a *_stride field is the distance in elements
+ *   between the rows of consecutive tokens (0: the rows are contiguous), so
+ *   that a slice of a wider projection's row is taken as it lies. Inside a
+ *   row the elements are contiguous. A stride smaller than its row is
+ *   SSD_ERR_SHAPE.
+ * - Array pointers need only their element's alignment unless an entry point
+ *   says more; rows that start on 16 bytes are read in wider loads.
+ * - Parameters (weights, biases, A, D) are float32.
+ */
+
+enum ssd_activation { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1 };
+
+/* Short causal convolution (host struct). */
+typedef struct {
+    int32_t total_tokens; /* T */
+    int32_t num_seqs;     /* S (the update: requests R, each owning T / R tokens) */
+    int32_t channels;     /* C */
+    int32_t width;        /* W: taps, 2..4 */
+    int32_t num_slots;    /* rows of the convolution cache */
+    int32_t in_dtype;     /* ssd_dtype of x and y (SSD_F32 or SSD_BF16) */
+    int32_t state_dtype;  /* ssd_dtype of the cache (SSD_F32 or SSD_BF16) */
+    int32_t activation;   /* ssd_activation */
+    int64_t x_stride;
+    int32_t y_channels[3]; /* how the C results of a token are dealt to y0, y1, y2 (their sum
+                              is C; {0, 0, 0}: all to y0): x, B and C of the scan that follows
+                              leave as arrays of their own */
+    int32_t reserved;      /* 0 */
+    int64_t y_stride[3];
+} conv_problem;
+
+/*
+ * Depthwise causal convolution of packed sequences, the layer piece in front
+ * of the selective scan:
+ *   y[t,c] = act(bias[c] + sum over k < W of weight[c,k] * x[t - (W-1) + k, c])
+ * in float32, where tokens before the sequence's first are the rows of its
+ * cache slot (zeros where has_initial_state is 0). The slot is left with the
+ * last W-1 tokens of (its old rows, the sequence), in state_dtype; every read
+ * of a slot precedes its write. A zero-length sequence writes its initial
+ * rows (or zeros) back.
+ *   x [T,C]; y0, y1, y2 [T, y_channels[i]] in_dtype (y1, y2 NULL when they
+ *   get no channels); must not overlap x
+ *   weight [C,W], bias [C] float32 (bias may be NULL)
+ *   conv_cache [num_slots,W-1,C] state_dtype, oldest token first
+ *   cu_seqlens [S+1], state_indices [S], has_initial_state [S] uint8 or NULL
+ *   (no sequence reads its slot)
+ */
+int causal_conv1d_varlen(const conv_problem *p, const void *x, const float *weight,
+                         const float *bias, const int32_t *cu_seqlens, void *conv_cache,
+                         const int32_t *state_indices, const uint8_t *has_initial_state, void *y0,
+                         void *y1, void *y2, void *stream);
+
+/*
+ * The same for decode / MTP verify: request r owns rows r T/R .. (r+1) T/R - 1
+ * and always continues its slot. update_cache 0 leaves the cache as it is
+ * (a verify step whose accepted count is not known yet: causal_conv1d_commit
+ * follows), otherwise the slot takes the request's tokens in.
+ * T must be a multiple of R (SSD_ERR_SHAPE).
+ */
+int causal_conv1d_update(const conv_problem *p, const void *x, const float *weight,
+                         const float *bias, void *conv_cache, const int32_t *state_indices,
+                         void *y0, void *y1, void *y2, int32_t update_cache, void *stream);
+
+/*
+ * After a verify step that left the cache: request r's slot takes its first
+ * 1 + num_accepted[r] tokens of x in (the target token is always accepted;
+ * a count outside [0, T/R) changes nothing). x as given to the verify step.
+ */
+int causal_conv1d_commit(const conv_problem *p, const void *x, void *conv_cache,
+                         const int32_t *state_indices, const int32_t *num_accepted, void *stream);
+
+/* Channel-wise selective scan (host struct). */
+typedef struct {
+    int32_t total_tokens; /* T */
+    int32_t num_seqs;     /* S (the update: requests R, each owning T / R tokens) */
+    int32_t channels;     /* C */
+    int32_t d_state;      /* N: 16, 32 or 64 */
+    int32_t ngroups;      /* G: channel c reads B, C of group c / (C / G) */
+    int32_t num_slots;
+    int32_t in_dtype;     /* ssd_dtype of x, dt, B, C, z, y (SSD_F32 or SSD_BF16) */
+    int32_t state_dtype;  /* ssd_dtype of the state cache */
+    int64_t x_stride, dt_stride, z_stride, b_stride, c_stride, y_stride;
+} scan_problem;
+
+/*
+ * The selective scan whose decay differs by channel and state (the SSD scan
+ * above has one per head), over packed sequences with the state cache by slot:
+ *   h_t[c,n] = exp(dt_t[c] A[c,n]) h_{t-1}[c,n] + dt_t[c] x_t[c] B_t[g,n]
+ *   y_t[c]   = (sum over n of h_t[c,n] C_t[g,n] + D[c] x_t[c]) * silu(z_t[c])
+ * all in float32 (z NULL: no gate). Initial and final states are handled as
+ * in ssd_state_passing: snapshot semantics, skipped bad slots, zero-length
+ * sequences written back.
+ *   x, dt, z, y [T,C]; B, C [T,G,N]; A [C,N], D [C] float32 (D may be NULL)
+ *   dt_transform     NULL: dt as given; else dt is raw and dt_bias is [C]
+ *   state_cache      [num_slots,C,N] state_dtype (round to nearest even)
+ *   workspace        selective_scan_workspace_bytes(p) bytes, 16-byte aligned
+ *                    (NULL when that is 0)
+ * state_cache, A and workspace must be 16-byte aligned.
+ */
+size_t selective_scan_workspace_bytes(const scan_problem *p);
+int selective_scan_varlen(const scan_problem *p, const void *x, const void *dt, const float *A,
+                          const void *B, const void *C, const float *D, const void *z,
+                          const ssd_dt_transform *dt_transform, const int32_t *cu_seqlens,
+                          void *state_cache, const int32_t *state_indices,
+                          const uint8_t *has_initial_state, void *y, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/*
+ * The same for decode / MTP verify, with selective_state_update's treatment of
+ * states: request r owns rows r T/R .. and continues its slot; with
+ * intermediate_states [R,T/R,C,N] (state_dtype, 16-byte aligned) the state
+ * after every token is stored there and the cache is not written, with NULL
+ * the last state is written back. ssd_state_commit rolls back (its [H,P,N]
+ * row is [C/64,64,N] or [C/16,16,N] here; N = 16).
+ */
+int selective_scan_update(const scan_problem *p, const void *x, const void *dt, const float *A,
+                          const void *B, const void *C, const float *D, const void *z,
+                          const ssd_dt_transform *dt_transform, void *state_cache,
+                          const int32_t *state_indices, void *y, void *intermediate_states,
+                          void *stream);
+
+/* Attention over packed prompts (host struct). */
+typedef struct {
+    int32_t total_q;   /* query tokens of all sequences together */
+    int32_t total_k;   /* key tokens of all sequences together */
+    int32_t num_seqs;  /* S */
+    int32_t nheads;    /* H query heads */
+    int32_t nkv_heads; /* key heads; query head h reads key head h / (H / nkv_heads) */
+    int32_t headdim;   /* 64 or 128 */
+    int32_t dtype;     /* ssd_dtype of q, k, v, out (SSD_F32 or SSD_BF16) */
+    int32_t causal;    /* 1: query i of Lq sees keys 0 .. i + Lk - Lq; 0: all keys */
+    float scale;       /* of the scores, positive (0: 1 / sqrt(headdim)) */
+    int32_t reserved;  /* 0 */
+    int64_t q_stride, k_stride, v_stride, o_stride;
+} attn_problem;
+
+/*
+ * Softmax attention of every sequence's queries over its own keys, one pass
+ * over the keys with a running maximum and sum in float32:
+ *   out[i,h] = sum_j softmax_j(scale q[i,h] . k[j]) v[j]
+ * A continued prompt has more keys than queries (Lk > Lq): its cached prefix,
+ * read back with kv_cache_load, followed by its own. A query that sees no key
+ * (Lk < Lq, or no keys at all) gets zeros, and lse -infinity. Keys and values
+ * that a query does not see do not touch its result, whatever they hold.
+ *   q, out [total_q,H,D]; k, v [total_k,nkv_heads,D]; lse [total_q,H] float32
+ *   (log of the sum of exponentials) or NULL
+ *   cu_seqlens_q, cu_seqlens_k [S+1] int32
+ * bf16: products on bf16 MFMA with float32 accumulation; the probabilities
+ * (before their division by the sum) are rounded to bf16. q, k, v, out and
+ * their strides must keep every row 16-byte aligned (SSD_ERR_ALIGN).
+ */
+int attention_varlen(const attn_problem *p, const void *q, const void *k, const void *v,
+                     const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, void *out,
+                     float *lse, void *stream);
+
+/* Paged key / value cache of one layer (host struct). */
+typedef struct {
+    int32_t num_pages;
+    int32_t page_size;   /* tokens a page: 16, 32, 64, 128 or 256 */
+    int32_t nkv_heads;
+    int32_t headdim;     /* 64 or 128 */
+    int32_t in_dtype;    /* ssd_dtype of the k, v, q rows outside the cache */
+    int32_t cache_dtype; /* SSD_BF16 or SSD_E4M3 */
+    int64_t k_stride, v_stride;  /* token rows of k and v */
+} kv_cache_problem;
+
+/*
+ * Cache layout: k_cache, v_cache [num_pages,nkv_heads,page_size,D] cache_dtype;
+ * with SSD_E4M3 k_scale, v_scale [num_pages,nkv_heads,page_size] uint8 (else
+ * NULL). A row (token, head) of SSD_E4M3 stands for code * 2^(scale - 127),
+ * with the least power of two for which no element exceeds 448 of it (at
+ * least 2^-126; a row of zeros has scale byte 1): scaling by it is exact, so
+ * each element is rounded once, to nearest even. Infinities and NaN are
+ * stored as NaN and do not enter the scale.
+ *
+ * kv_cache_store writes token t's rows of k and v to position
+ * slot_mapping[t] = page * page_size + offset (int64 on the device; a negative
+ * or too large one is skipped). Positions of one call must be distinct.
+ *   k, v [num_tokens,nkv_heads,D] in_dtype
+ * k, v, their strides and the caches must be 16-byte aligned.
+ */
+int kv_cache_store(const kv_cache_problem *p, int32_t num_tokens, const void *k, const void *v,
+                   const int64_t *slot_mapping, void *k_cache, void *v_cache, uint8_t *k_scale,
+                   uint8_t *v_scale, void *stream);
+
+/*
+ * Reads sequences back into packed rows: token i of sequence s comes from page
+ * block_table[s, i / page_size], place i % page_size; out of a table entry
+ * outside [0, num_pages), or past the table's width, come zeros.
+ *   cu_seqlens [S+1]; block_table [S,max_pages] int32
+ *   k, v out [total_tokens,nkv_heads,D] in_dtype (rounded to nearest even)
+ */
+int kv_cache_load(const kv_cache_problem *p, int32_t total_tokens, int32_t num_seqs,
+                  int32_t max_pages, const int32_t *cu_seqlens, const int32_t *block_table,
+                  const void *k_cache, const void *v_cache, const uint8_t *k_scale,
+                  const uint8_t *v_scale, void *k, void *v, void *stream);
+
+/* Attention of single tokens over the paged cache (host struct). */
+typedef struct {
+    kv_cache_problem kv; /* in_dtype: q and out, SSD_BF16 (k_stride, v_stride unused) */
+    int32_t num_reqs;       /* R */
+    int32_t tokens_per_req; /* T: 1 for plain decode, 1 + drafts for a verify step */
+    int32_t nheads;         /* H */
+    int32_t max_pages;      /* width of the block table */
+    float scale;            /* of the scores, positive (0: 1 / sqrt(headdim)) */
+    int32_t reserved;       /* 0 */
+    int64_t q_stride, o_stride;
+} attn_decode_problem;
+
+/*
+ * Request r's T tokens are the last of its context_lens[r] cached tokens
+ * (their own keys included: kv_cache_store first); token t sees the first
+ * context_lens[r] - T + 1 + t of them. A token that sees none gets zeros (lse
+ * -infinity). A context is cut to max_pages * page_size tokens, and keys on
+ * a page whose table entry lies outside [0, num_pages) are not seen.
+ *   q, out [R,T,H,D]; block_table [R,max_pages], context_lens [R] int32
+ *   lse [R,T,H] float32 or NULL
+ *   workspace   attn_decode_workspace_bytes(p) bytes, 16-byte aligned (NULL
+ *               when that is 0): long contexts are split over blocks and
+ *               joined by a second launch
+ */
+size_t attn_decode_workspace_bytes(const attn_decode_problem *p);
+int attention_decode(const attn_decode_problem *p, const void *q, const void *k_cache,
+                     const void *v_cache, const uint8_t *k_scale, const uint8_t *v_scale,
+                     const int32_t *block_table, const int32_t *context_lens, void *out,
+                     float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -13,6 +13,9 @@ cu_seqlens [S+1] int32; state_indices [S] int32; has_initial_state [S] uint8;
 state cache [num_slots,H,P,N]; checkpoints [max_chunks,H,P,N].
 Decode: x, y [R,T,H,P]; dt [R,T,H]; B, C [R,T,G,N]; intermediate states
 [R,T,H,P,N]; num_accepted [R] int32.
+
+The operators of the layers around the scan (short convolution, channel-wise
+scan, attention, paged key / value cache) are bound in ``layer_ops``.
 """
 from __future__ import annotations
 
@@ -21,6 +24,9 @@ import os
 from typing import Optional
 
 import torch
+
+from ._layer_abi import (LAYER_SIGS, attn_decode_problem, attn_problem, conv_problem,  # noqa: F401
+                         kv_cache_problem, scan_problem)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libssd_mi355x.so")
@@ -111,6 +117,7 @@ _SIGS = {
     "ssd_noalloc_scratch_bytes": ([], ctypes.c_size_t),
     "ssd_combined_varlen_noalloc": ([_pp] + [_vp] * 13, ctypes.c_int),
 }
+_SIGS.update(LAYER_SIGS)
 for _name, (_args, _res) in _SIGS.items():
     _f = getattr(_lib, _name)
     _f.argtypes = _args
@@ -725,3 +732,14 @@ def alloc_replay_rings(p: ssu_problem, ring_len: int, device="cuda") -> dict:
                 ring_dt=torch.zeros((S, ring_len, H), dtype=ti, device=device),
                 ring_B=torch.zeros((S, ring_len, G, N), dtype=ti, device=device),
                 cursor=torch.zeros((S, 2), dtype=torch.int32, device=device))
+
+
+# ---------------------------------------------------------------------------
+# the operators of the layers around the scan
+
+from .layer_ops import (  # noqa: E402,F401
+    ACT_NONE, ACT_SILU, alloc_attn_decode_workspace, alloc_kv_cache, alloc_scan_workspace,
+    attention_decode, attention_varlen, attn_decode_workspace_bytes, causal_conv1d_commit,
+    causal_conv1d_update, causal_conv1d_varlen, kv_cache_load, kv_cache_store,
+    make_attn_decode_problem, make_attn_problem, make_conv_problem, make_kv_cache_problem,
+    make_scan_problem, selective_scan_update, selective_scan_varlen, selective_scan_workspace_bytes)

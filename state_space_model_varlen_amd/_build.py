@@ -10,8 +10,9 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libssd_mi355x.so")
 SOURCES = ["ssd_api.cpp", "ssd_prefill.hip", "ssd_decode.hip", "ssd_replay.hip",
-           "ssd_noalloc.hip"]
-HEADERS = ["ssd_device.h", "ssd_launch.h"]
+           "ssd_noalloc.hip", "ssd_layer_api.cpp", "ssd_conv.hip", "ssd_sscan.hip", "ssd_attn.hip",
+           "ssd_kv.hip"]
+HEADERS = ["ssd_device.h", "ssd_launch.h", "ssd_layer.h", "ssd_layer_device.h"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -1,0 +1,405 @@
+// Softmax attention over packed prompts: causal or full, grouped heads, more
+// keys than queries where a sequence continues a cached prefix.
+//
+// One pass over a sequence's keys per block of queries, with a running maximum
+// and sum in float32. For query row i and the keys seen so far,
+//     m = max_j s_ij,  l = sum_j exp2(s_ij - m),  o = sum_j exp2(s_ij - m) v_j
+// (scores in units of log 2), o and l being rescaled when m grows; the result
+// is o / l. 4 D operations for every visible pair, against a few bytes: bound
+// by the matrix units on any but the shortest prompts.
+#include "ssd_layer.h"
+#include "ssd_layer_device.h"
+
+namespace ssd {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
+struct AttnArgs {
+    const void *q, *k, *v;
+    const int32_t *cuq, *cuk;
+    void *out;
+    float *lse;
+    int64_t qs, ks, vs, os;
+    int Tq, Tk, S, H, Hkv, causal;
+    float scale2;   // scale log2(e)
+};
+
+// The block's queries: tile of BM queries of one sequence, head and key head,
+// the sequence's key rows, and `off`: query i sees keys up to i + off.
+struct AttnBlock {
+    int seq, q0, lq, qrow, head, kvh, krow, lk, off;
+};
+// Heads run fastest over the blocks, the key head innermost, so that the 8
+// XCDs, which take blocks in turn, each see few key heads. Within a sequence
+// the last tile, which sees the most keys, comes first.
+__device__ __forceinline__ AttnBlock attn_block(const AttnArgs &a, int BM) {
+    AttnBlock r;
+    const int hh = (int)(blockIdx.x % (unsigned)a.H), b = (int)(blockIdx.x / (unsigned)a.H);
+    const SeqTile t = find_tile(a.cuq, a.S, a.Tq, BM, 0, b);
+    r.seq = t.seq;
+    if (t.seq < 0) return r;
+    r.kvh = hh % a.Hkv;
+    r.head = r.kvh * (a.H / a.Hkv) + hh / a.Hkv;
+    r.lq = t.len;
+    r.qrow = t.start;
+    r.q0 = (t.len - 1) / BM * BM - t.t0;
+    int k0 = scalar(a.cuk[t.seq]), k1 = scalar(a.cuk[t.seq + 1]);
+    k0 = k0 < 0 ? 0 : (k0 > a.Tk ? a.Tk : k0);
+    k1 = k1 < 0 ? 0 : (k1 > a.Tk ? a.Tk : k1);
+    r.krow = k0;
+    r.lk = k1 > k0 ? k1 - k0 : 0;
+    r.off = a.causal ? r.lk - r.lq : 0x3fffffff;
+    return r;
+}
+// Keys that query i (clamped: i + off may pass 2^31 where there is no mask) sees.
+__device__ __forceinline__ int keys_seen(const AttnBlock &b, int i) {
+    const int n = b.off >= b.lk ? b.lk : i + b.off + 1;
+    return n < 0 ? 0 : (n > b.lk ? b.lk : n);
+}
+
+// A masked probability is zero, and zero times an infinity or a NaN among the
+// values is not. In a tile that hides some of its keys from some of the block's
+// queries, non-finite values are therefore taken out of the product and added
+// afterwards to the queries that do see them (any positive weight gives the
+// same infinity or NaN).
+__device__ __forceinline__ bool bad16(uint32_t w) { return (w & 0x7f80u) == 0x7f80u; }
+__device__ __forceinline__ bool take_out(u32x4 &w, bf16) {
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool lo = bad16(w[i]), hi = bad16(w[i] >> 16);
+        w[i] &= (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0x0000ffffu : 0xffffffffu);
+        any |= lo | hi;
+    }
+    return any;
+}
+__device__ __forceinline__ bool take_out(u32x4 &w, float) {
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool bad = (w[i] & 0x7f800000u) == 0x7f800000u;
+        w[i] = bad ? 0u : w[i];
+        any |= bad;
+    }
+    return any;
+}
+
+// bf16 heads of D. A block of 4 waves takes BM = 128 queries of one head, 32 a
+// wave, against tiles of 64 keys in LDS (two buffers: the next tile's rows are
+// in flight in registers while one is worked on; one barrier a tile).
+//
+// Scores are formed transposed, S^T = K Q^T (keys x queries), so that a lane
+// holds 16 of every 32 scores of one query (its partner 32 lanes away the
+// rest): the row maximum and the rescaling are per lane, and the rounded
+// probabilities are, as they stand, the operand of O^T = V^T P^T. The values'
+// transposed operand comes through the LDS transpose read. Row pitches keep
+// both kinds of reads free of bank conflicts (K: 4 dwords past a multiple of
+// 64 dwords; V: 16 past).
+template <int D>
+__global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a)
+{
+    constexpr int BM = 128, BN = 64, KP = D + 8, VP = D + 32;
+    constexpr int VEC = BN * D / 8 / 256;       // 16-byte vectors a thread stages of K, and of V
+    constexpr int RPT = D / 8;                  // threads a row
+    __shared__ __align__(16) bf16 kt[2][BN * KP];
+    __shared__ __align__(16) bf16 vt[2][BN * VP];
+    __shared__ int hidden[2];                   // a partly masked tile has non-finite values
+    const AttnBlock b = attn_block(a, BM);
+    if (b.seq < 0) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, qi = lane & 31, hf = lane >> 5;
+    const int q = b.q0 + wave * 32 + qi;                       // the lane's query
+    const int qc = q < b.lq ? q : b.lq - 1;
+    const bf16 *const Q = static_cast<const bf16 *>(a.q) + (int64_t)(b.qrow + qc) * a.qs +
+                          (int64_t)b.head * D + hf * 8;
+    bf16x8 qf[D / 16];
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) qf[s] = *reinterpret_cast<const bf16x8 *>(Q + 16 * s);
+    const int seen = q < b.lq ? keys_seen(b, q) : 0;
+    const int qlast = b.q0 + BM - 1 < b.lq - 1 ? b.q0 + BM - 1 : b.lq - 1;
+    const int kend = keys_seen(b, qlast);                      // keys the block needs
+    const int kfull = keys_seen(b, b.q0);                      // keys that all its queries see
+    const int wlast = b.q0 + wave * 32 + 31 < qlast ? b.q0 + wave * 32 + 31 : qlast;
+    const int wend = b.q0 + wave * 32 < b.lq ? keys_seen(b, wlast) : 0;   // keys the wave needs
+    const int wfull = b.q0 + wave * 32 + 31 < b.lq ? keys_seen(b, b.q0 + wave * 32) : 0;
+
+    const bf16 *const K = static_cast<const bf16 *>(a.k) + (int64_t)b.krow * a.ks + (int64_t)b.kvh * D;
+    const bf16 *const V = static_cast<const bf16 *>(a.v) + (int64_t)b.krow * a.vs + (int64_t)b.kvh * D;
+    u32x4 kr[VEC], vr[VEC];
+    // rows past the sequence's end come back as zeros
+    auto request = [&](int j0) {
+        const int rows = b.lk - j0 < BN ? b.lk - j0 : BN;
+        const rsrc_t rk = make_rsrc(K + (int64_t)j0 * a.ks, (uint32_t)((rows - 1) * (int)a.ks + D) * 2);
+        const rsrc_t rv = make_rsrc(V + (int64_t)j0 * a.vs, (uint32_t)((rows - 1) * (int)a.vs + D) * 2);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int row = (tid + 256 * i) / RPT, c = tid % RPT;
+            kr[i] = __builtin_bit_cast(u32x4, buf_ld16(rk, (uint32_t)(row * (int)a.ks + 8 * c) * 2));
+            vr[i] = __builtin_bit_cast(u32x4, buf_ld16(rv, (uint32_t)(row * (int)a.vs + 8 * c) * 2));
+        }
+    };
+    auto stage = [&](int j0, int buf) {
+        if (j0 + BN > kfull) {
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) any |= take_out(vr[i], bf16());
+            if (any) hidden[buf] = 1;
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int row = (tid + 256 * i) / RPT, c = tid % RPT;
+            *reinterpret_cast<u32x4 *>(&kt[buf][row * KP + 8 * c]) = kr[i];
+            *reinterpret_cast<u32x4 *>(&vt[buf][row * VP + 8 * c]) = vr[i];
+        }
+    };
+
+    f32x16 o[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
+    float m = -__builtin_inff(), sum = 0.0f;
+    if (tid < 2) hidden[tid] = 0;
+    __syncthreads();
+    if (kend > 0) {
+        request(0);
+        stage(0, 0);
+    }
+    __syncthreads();
+    int buf = 0;
+    for (int j0 = 0; j0 < kend; j0 += BN, buf ^= 1) {
+        const bool more = j0 + BN < kend;
+        if (more) request(j0 + BN);
+        if (j0 < wend) {
+            f32x16 s[2];
+            const bf16 *const kl = &kt[buf][qi * KP + hf * 8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[h][e] = 0.0f;
+#pragma unroll
+                for (int st = 0; st < D / 16; ++st)
+                    s[h] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        *reinterpret_cast<const bf16x8 *>(kl + h * 32 * KP + 16 * st), qf[st], s[h],
+                        0, 0, 0);
+            }
+            // element e of half h: key j0 + 32 h + 8 (e / 4) + 4 hf + e % 4
+            if (j0 + BN > wfull) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (j0 + 32 * h + 8 * (e >> 2) + 4 * hf + (e & 3) >= seen)
+                            s[h][e] = -__builtin_inff();
+            }
+            float top = s[0][0];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) top = fmaxf(top, s[h][e]);
+            top = across32(top, larger) * a.scale2;
+            if (__any(top > m)) {
+                const float was = m;
+                m = fmaxf(m, top);
+                const float f = m == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(was - m);
+                sum *= f;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[i][e] *= f;
+            }
+            // (a row that has seen nothing yet: subtract 0, its terms are exp2(-inf))
+            const float ref = m == -__builtin_inff() ? 0.0f : m;
+            bf16x8 pf[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float p = __builtin_amdgcn_exp2f(s[h][e] * a.scale2 - ref);
+                    sum += p;
+                    pf[2 * h + (e >> 3)][e & 7] = static_cast<bf16>(p);
+                }
+            // operand of dims 32 i .. and keys 16 w ..: lanes of a half hold the keys
+            // 4 hf + v and 8 + 4 hf + v that their probabilities belong to
+            const int jl = lane & 15;
+            const bf16 *const vl = &vt[buf][(4 * hf + (jl >> 2)) * VP + ((lane >> 4) & 1) * 16 + 4 * (jl & 3)];
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const v4i16 lo = lds_read_tr16(vl + 16 * w * VP + 32 * i);
+                    const v4i16 hi = lds_read_tr16(vl + (16 * w + 8) * VP + 32 * i);
+                    typedef short v8i16 __attribute__((ext_vector_type(8)));
+                    const v8i16 both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, both),
+                                                                   pf[w], o[i], 0, 0, 0);
+                }
+            if (j0 + BN > kfull && hidden[buf]) {
+                for (int j = j0; j < j0 + BN && j < b.lk; ++j)
+                    if (j < seen)
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const float v = to_f32(V[(int64_t)j * a.vs + 32 * i + 8 * (e >> 2) +
+                                                         4 * hf + (e & 3)]);
+                                if (!(fabsf(v) < __builtin_inff())) o[i][e] += v;
+                            }
+            }
+        }
+        if (more) stage(j0 + BN, buf ^ 1);
+        __syncthreads();
+    }
+
+    sum = across32(sum, added);
+    if (q < b.lq) {
+        // (a NaN sum is passed on; a row without keys gets zeros)
+        const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+        bf16 *const out = static_cast<bf16 *>(a.out) + (int64_t)(b.qrow + q) * a.os +
+                          (int64_t)b.head * D + 4 * hf;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                float r[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) r[v] = o[i][e + v] * inv;
+                store4<bf16>(out + 32 * i + 2 * e, r);
+            }
+        if (a.lse && hf == 0) {
+            const float ref = m == -__builtin_inff() ? 0.0f : m;
+            a.lse[(int64_t)(b.qrow + q) * a.H + b.head] = (ref + __builtin_amdgcn_logf(sum)) * kLn2;
+        }
+    }
+}
+
+// float heads of D: the same pass on the float32 matrix instructions (16 x 16
+// tiles, 4 keys a step), 16 queries a wave, 32 keys a tile. A lane holds the
+// scores of query lane % 16 for keys 4 (lane / 16) + v of each 16.
+template <int D>
+__global__ __launch_bounds__(256) void attn_f32_kernel(AttnArgs a)
+{
+    constexpr int BM = 64, BN = 32, P = D + 4, VEC = BN * D / 4 / 256, RPT = D / 4;
+    __shared__ __align__(16) float kt[BN * P], vt[BN * P];
+    __shared__ int hidden;
+    const AttnBlock b = attn_block(a, BM);
+    if (b.seq < 0) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, qi = lane & 15, g = lane >> 4;
+    const int q = b.q0 + wave * 16 + qi, qc = q < b.lq ? q : b.lq - 1;
+    const float *const Q = static_cast<const float *>(a.q) + (int64_t)(b.qrow + qc) * a.qs +
+                           (int64_t)b.head * D + g;
+    float qf[D / 4];
+#pragma unroll
+    for (int s = 0; s < D / 4; ++s) qf[s] = Q[4 * s];
+    const int seen = q < b.lq ? keys_seen(b, q) : 0;
+    const int qlast = b.q0 + BM - 1 < b.lq - 1 ? b.q0 + BM - 1 : b.lq - 1;
+    const int kend = keys_seen(b, qlast), kfull = keys_seen(b, b.q0);
+    const float *const K = static_cast<const float *>(a.k) + (int64_t)b.krow * a.ks + (int64_t)b.kvh * D;
+    const float *const V = static_cast<const float *>(a.v) + (int64_t)b.krow * a.vs + (int64_t)b.kvh * D;
+    f32x4 o[D / 16];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) o[i] = zero4();
+    float m = -__builtin_inff(), sum = 0.0f;
+    for (int j0 = 0; j0 < kend; j0 += BN) {
+        const int rows = b.lk - j0 < BN ? b.lk - j0 : BN;
+        const rsrc_t rk = make_rsrc(K + (int64_t)j0 * a.ks, (uint32_t)((rows - 1) * (int)a.ks + D) * 4);
+        const rsrc_t rv = make_rsrc(V + (int64_t)j0 * a.vs, (uint32_t)((rows - 1) * (int)a.vs + D) * 4);
+        u32x4 kr[VEC], vr[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int row = (tid + 256 * i) / RPT, c = tid % RPT;
+            kr[i] = __builtin_bit_cast(u32x4, buf_ld16(rk, (uint32_t)(row * (int)a.ks + 4 * c) * 4));
+            vr[i] = __builtin_bit_cast(u32x4, buf_ld16(rv, (uint32_t)(row * (int)a.vs + 4 * c) * 4));
+        }
+        __syncthreads();                       // the last tile's reads are done
+        if (tid == 0) hidden = 0;
+        __syncthreads();
+        if (j0 + BN > kfull) {
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) any |= take_out(vr[i], 0.0f);
+            if (any) hidden = 1;
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int row = (tid + 256 * i) / RPT, c = tid % RPT;
+            *reinterpret_cast<u32x4 *>(&kt[row * P + 4 * c]) = kr[i];
+            *reinterpret_cast<u32x4 *>(&vt[row * P + 4 * c]) = vr[i];
+        }
+        __syncthreads();
+        f32x4 s[2];
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            s[h] = zero4();
+#pragma unroll
+            for (int st = 0; st < D / 4; ++st)
+                s[h] = Mma<float>::run(kt[(16 * h + qi) * P + 4 * st + g], qf[st], s[h]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[h][e] = j0 + 16 * h + 4 * g + e < seen ? s[h][e] * a.scale2 : -__builtin_inff();
+                top = fmaxf(top, s[h][e]);
+            }
+        }
+        top = across32(across16(top, larger), larger);
+        const float was = m;
+        m = fmaxf(m, top);
+        const float ref = m == -__builtin_inff() ? 0.0f : m, f = __builtin_amdgcn_exp2f(was - ref);
+        sum *= f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) o[i] *= f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float p = __builtin_amdgcn_exp2f(s[h][e] - ref);
+                sum += p;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    o[i] = Mma<float>::run(vt[(16 * h + 4 * g + e) * P + 16 * i + qi], p, o[i]);
+            }
+        if (j0 + BN > kfull && hidden) {
+            for (int j = j0; j < j0 + BN && j < b.lk; ++j)
+                if (j < seen)
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float v = V[(int64_t)j * a.vs + 16 * i + 4 * g + e];
+                            if (!(fabsf(v) < __builtin_inff())) o[i][e] += v;
+                        }
+        }
+    }
+    sum = across32(across16(sum, added), added);
+    if (q < b.lq) {
+        const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+        float *const out = static_cast<float *>(a.out) + (int64_t)(b.qrow + q) * a.os +
+                           (int64_t)b.head * D + 4 * g;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) *reinterpret_cast<f32x4 *>(out + 16 * i) = o[i] * inv;
+        if (a.lse && g == 0) {
+            const float ref = m == -__builtin_inff() ? 0.0f : m;
+            a.lse[(int64_t)(b.qrow + q) * a.H + b.head] = (ref + __builtin_amdgcn_logf(sum)) * kLn2;
+        }
+    }
+}
+
+void launch_attn(const AttnDims &d, const void *q, const void *k, const void *v,
+                 const int32_t *cuq, const int32_t *cuk, void *out, float *lse, void *stream)
+{
+    if (d.S <= 0 || d.Tq <= 0) return;
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    const AttnArgs a{q, k, v, cuq, cuk, out, lse, d.qs, d.ks, d.vs, d.os, d.Tq, d.Tk, d.S, d.H,
+                     d.Hkv, d.causal ? 1 : 0, d.scale * kLog2e};
+    const int BM = d.bf16 ? 128 : 64;
+    const dim3 grid((unsigned)(((int64_t)d.Tq / BM + d.S) * d.H));
+    if (d.bf16) {
+        if (d.D == 128) hipLaunchKernelGGL(attn_kernel<128>, grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL(attn_kernel<64>, grid, dim3(256), 0, st, a);
+    } else {
+        if (d.D == 128) hipLaunchKernelGGL(attn_f32_kernel<128>, grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL(attn_f32_kernel<64>, grid, dim3(256), 0, st, a);
+    }
+}
+
+}  // namespace ssd

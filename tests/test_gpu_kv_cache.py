@@ -1,0 +1,306 @@
+"""The paged key / value cache and the attention of single tokens over it, on the GPU, against
+oracle/layers.py: stored rows and rows read back bit for bit, attention within
+attention_tolerance."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import layers as ol
+
+pytestmark = pytest.mark.gpu
+ssd = pytest.importorskip("state_space_model_varlen_amd")
+BF, F32, E4 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+DEV = "cuda"
+
+
+def values(cache, scale):
+    """What a cache's rows stand for, float64 on the CPU."""
+    if scale is None:
+        return cache.cpu().double()
+    return cache.cpu().double() * torch.exp2(scale.cpu().double() - 127)[..., None]
+
+
+def pages_for(g, page, lens, spare=2):
+    per = [-(-n // page) for n in lens]
+    order = torch.randperm(sum(per) + spare, generator=g).to(torch.int32)
+    table, at = torch.full((len(lens), max(per + [1])), -1, dtype=torch.int32), 0
+    for i, n in enumerate(per):
+        table[i, :n] = order[at:at + n]
+        at += n
+    return table, sum(per) + spare
+
+
+def wide_row(g, Hkv, D, n, ti):
+    """Rows of many magnitudes, zeros, ties and the ends of the scale among them."""
+    x = torch.randn(n, Hkv, D, generator=g) * torch.exp2(torch.randint(-40, 40, (n, Hkv, 1),
+                                                                       generator=g).float())
+    x[0] = 0
+    if n > 1:
+        x[1, 0] = 448.0
+    if n > 2:
+        x[2, 0] = torch.where(torch.arange(D) % 2 == 0, 450.0, 17.0)
+    if n > 3:
+        x[3, 0] = torch.arange(D) * 0.5
+    if n > 4:
+        x[4, 0, 0] = 1e-38
+        x[4, 0, 1:] = 1e-40
+    return x.to(ti)
+
+
+@pytest.mark.parametrize("ti", [BF, F32])
+@pytest.mark.parametrize("ct", [BF, E4])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page,Hkv", [(16, 1), (64, 3)])
+def test_store_and_load(ti, ct, D, page, Hkv):
+    g = torch.Generator().manual_seed(D + page)
+    lens = [1, 0, page, page + 1, 5]
+    T = sum(lens)
+    table, n = pages_for(g, page, lens)
+    p = ssd.make_kv_cache_problem(n, page, Hkv, D, ti, ct)
+    c = ssd.alloc_kv_cache(p, DEV)
+    k, v = wide_row(g, Hkv, D, T, ti), wide_row(g, Hkv, D, T, ti)
+    slots, at = [], []
+    for i, m in enumerate(lens):
+        for j in range(m):
+            slots.append(int(table[i, j // page]) * page + j % page)
+            at.append((int(table[i, j // page]), j % page))
+    sl = torch.tensor(slots, dtype=torch.int64)
+    ssd.kv_cache_store(p, k.to(DEV), v.to(DEV), sl.to(DEV), **c)
+    torch.cuda.synchronize()
+    for x, name in ((k, "k"), (v, "v")):
+        got = values(c[name + "_cache"], c[name + "_scale"])
+        for t, (pg, o) in enumerate(at):
+            for h in range(Hkv):
+                if ct == E4:
+                    want, b = ol.encode_row(x[t, h].double().numpy())
+                    assert int(c[name + "_scale"][pg, h, o]) == b, (name, t, h)
+                    assert np.array_equal(got[pg, h, o].numpy(), want * 2.0 ** (b - 127)), (name, t, h)
+                else:
+                    assert torch.equal(got[pg, h, o], x[t, h].to(BF).double())
+        rest = torch.ones(n, page, dtype=torch.bool)
+        for pg, o in at:
+            rest[pg, o] = False
+        assert bool((got.transpose(1, 2)[rest] == 0).all())     # nothing else was written
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32)
+    ko, vo = torch.full((T, Hkv, D), 7.0, dtype=ti, device=DEV), torch.full((T, Hkv, D), 7.0, dtype=ti,
+                                                                           device=DEV)
+    ssd.kv_cache_load(p, cu.to(DEV), table.to(DEV), c["k_cache"], c["v_cache"], c["k_scale"],
+                      c["v_scale"], ko, vo)
+    for out, name in ((ko, "k"), (vo, "v")):
+        want = values(c[name + "_cache"], c[name + "_scale"])
+        for t, (pg, o) in enumerate(at):
+            assert torch.equal(out[t].cpu(), want[pg, :, o].to(ti))
+
+
+@pytest.mark.parametrize("ct", [BF, E4])
+def test_strides_skipped_positions_and_bad_pages(ct):
+    g = torch.Generator().manual_seed(3)
+    Hkv, D, page, n = 2, 64, 16, 3
+    p = ssd.make_kv_cache_problem(n, page, Hkv, D, BF, ct)
+    c = ssd.alloc_kv_cache(p, DEV)
+    row = torch.randn(5, 2 * Hkv * D + 8, generator=g).to(BF).to(DEV)
+    k, v = row[:, :Hkv * D].unflatten(1, (Hkv, D)), row[:, Hkv * D:2 * Hkv * D].unflatten(1, (Hkv, D))
+    slots = torch.tensor([0, -1, n * page, 17, 2 ** 40], dtype=torch.int64, device=DEV)
+    ssd.kv_cache_store(p, k, v, slots, **c)
+    got = values(c["v_cache"], c["v_scale"])
+    assert bool((got[0, :, 0] != 0).any()) and bool((got[1, :, 1] != 0).any())
+    got[0, :, 0] = 0
+    got[1, :, 1] = 0
+    assert bool((got == 0).all())
+    # pages out of range, and tokens past the table's width, read back as zeros
+    table = torch.tensor([[0, -1, n, 1]], dtype=torch.int32, device=DEV)
+    T = 5 * page
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    out = torch.full((T, 2 * Hkv * D), 7.0, dtype=BF, device=DEV)
+    ko, vo = out[:, :Hkv * D].unflatten(1, (Hkv, D)), out[:, Hkv * D:].unflatten(1, (Hkv, D))
+    ssd.kv_cache_load(p, cu, table, c["k_cache"], c["v_cache"], c["k_scale"], c["v_scale"], ko, vo)
+    want = values(c["v_cache"], c["v_scale"])
+    assert torch.equal(vo[0].cpu().double(), want[0, :, 0])
+    assert torch.equal(vo[3 * page + 1].cpu().double(), want[1, :, 1])
+    vo[0] = 0
+    vo[3 * page + 1] = 0
+    assert bool((vo == 0).all())
+
+
+def test_non_finite_rows():
+    p = ssd.make_kv_cache_problem(1, 16, 1, 64, F32, E4)
+    c = ssd.alloc_kv_cache(p, DEV)
+    k = torch.linspace(-3, 3, 64).repeat(3, 1)
+    k[0, 3], k[0, 9], k[1] = float("inf"), float("nan"), float("-inf")
+    k = k[:, None].contiguous()
+    ssd.kv_cache_store(p, k.to(DEV), k.to(DEV), torch.arange(3, device=DEV), **c)
+    got = values(c["k_cache"], c["k_scale"])[0, 0].numpy()
+    for t in range(3):
+        want, b = ol.encode_row(k[t, 0].double().numpy())
+        assert np.array_equal(got[t], want * 2.0 ** (b - 127), equal_nan=True)
+
+
+def make(seed, ct, lens, T, H, Hkv, D, page):
+    g = torch.Generator().manual_seed(seed)
+    table, n = pages_for(g, page, lens)
+    p = ssd.make_kv_cache_problem(n, page, Hkv, D, BF, ct)
+    c = ssd.alloc_kv_cache(p, DEV)
+    # what no sequence owns holds NaN
+    for x in ("k", "v"):
+        c[x + "_cache"].view(torch.uint8).fill_(0xff)
+    rk, rv = [], []
+    for i, L in enumerate(lens):
+        k, v = (torch.randn(L, Hkv, D, generator=g).to(BF) for _ in range(2))
+        pos = torch.arange(L)
+        sl = table[i].long()[pos // page] * page + pos % page
+        ssd.kv_cache_store(p, k.to(DEV), v.to(DEV), sl.to(DEV), **c)
+        pick = lambda x: values(c[x + "_cache"], c[x + "_scale"])[           # noqa: E731
+            table[i].long()[pos // page], :, pos % page]
+        rk.append(pick("k"))
+        rv.append(pick("v"))
+    q = torch.randn(len(lens), T, H, D, generator=g).to(BF)
+    return p, c, table, q, rk, rv
+
+
+def decode(p, c, table, q, lens, scale=0.0, lse=True):
+    R, T, H, D = q.shape
+    d = ssd.make_attn_decode_problem(p, R, T, H, table.shape[1], scale)
+    out = torch.full(q.shape, 7.0, dtype=BF, device=DEV)
+    ls = torch.full(q.shape[:3], 7.0, device=DEV) if lse else None
+    ssd.attention_decode(d, q.to(DEV), c["k_cache"], c["v_cache"], c["k_scale"], c["v_scale"],
+                         table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV), out, ls,
+                         ssd.alloc_attn_decode_workspace(d, DEV))
+    return out, ls
+
+
+def compare(out, lse, ref, D, nk):
+    want, wl, mag, top = ref
+    got = out.cpu().double().numpy()
+    bad = ~(np.abs(got - want) <= ol.attention_tolerance(want, mag, top, D, nk, BF))
+    assert not bad.any(), (int(bad.sum()), float(np.nanmax(np.abs(got - want))))
+    if lse is None:
+        return
+    gl, f = lse.cpu().double().numpy(), np.isfinite(wl)
+    assert np.array_equal(np.isneginf(gl), ~f)
+    tl = (2 * D + 8) * 2.0 ** -24 * top + (nk + 16) * 2.0 ** -24 + 2.0 ** -22 * np.abs(np.where(f, wl, 0))
+    assert np.all(np.abs(gl - wl)[f] <= tl[f])
+
+
+@pytest.mark.parametrize("ct", [BF, E4])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H,Hkv,T", [(4, 4, 1), (8, 1, 1), (8, 2, 3), (5, 1, 4), (16, 1, 3)])
+def test_decode(ct, D, H, Hkv, T):
+    lens = [T, 31, 33, 100, 16]
+    p, c, table, q, rk, rv = make(H + T, ct, lens, T, H, Hkv, D, 16)
+    out, lse = decode(p, c, table, q, lens)
+    compare(out, lse, ol.decode_attention(q, rk, rv, lens), D, max(lens))
+
+
+@pytest.mark.parametrize("page", [16, 32, 128, 256])
+@pytest.mark.parametrize("ct", [BF, E4])
+def test_decode_pages_and_splits(page, ct):
+    # contexts long enough to be split over blocks, ending inside tiles and pages
+    lens = [1500, 1, 0, 257, 1024]
+    p, c, table, q, rk, rv = make(page, ct, lens, 2, 4, 2, 64, page)
+    out, lse = decode(p, c, table, q, lens)
+    compare(out, lse, ol.decode_attention(q, rk, rv, lens), 64, 1500)
+    out2, _ = decode(p, c, table, q, lens, lse=False)
+    assert torch.equal(out, out2)
+
+
+def test_decode_scale_and_short_contexts():
+    # fewer cached tokens than queries: the first queries see nothing
+    lens = [2, 0, 5]
+    p, c, table, q, rk, rv = make(5, E4, lens, 4, 4, 1, 128, 32)
+    out, lse = decode(p, c, table, q, lens, scale=0.7)
+    compare(out, lse, ol.decode_attention(q, rk, rv, lens, 0.7), 128, 5)
+    assert bool((out[0, :2] == 0).all()) and bool((out[1] == 0).all())
+
+
+def test_decode_lengths_and_pages_out_of_range():
+    lens = [90, 40]
+    p, c, table, q, rk, rv = make(6, E4, lens, 1, 2, 1, 64, 16)
+    # a context beyond the table is cut to it, a negative one is empty
+    out, lse = decode(p, c, table, q, [10 ** 9, -3])
+    full = table.shape[1] * 16
+    keep = [torch.cat([rk[0], values(c["k_cache"], c["k_scale"])[table[0, -1].long(), :, 90 % 16:]
+                       .transpose(0, 1)]) if 90 % 16 else rk[0]]
+    assert keep[0].shape[0] == full                 # (the cut context ends in rows of NaN)
+    assert bool((out[1] == 0).all()) and bool(torch.isneginf(lse[1]).all())
+    # keys on a page out of range are not seen
+    t2 = table.clone()
+    t2[0, 2], t2[0, 3] = -1, 10 ** 6
+    out, lse = decode(p, c, t2, q, lens)
+    drop = lambda x: torch.cat([x[:32], x[64:]])                             # noqa: E731
+    compare(out, lse, ol.decode_attention(q, [drop(rk[0]), rk[1]], [drop(rv[0]), rv[1]], lens), 64, 90)
+
+
+@pytest.mark.parametrize("ct", [BF, E4])
+def test_decode_hidden_rows_do_not_matter(ct):
+    """A draft token's key and value, non-finite, do not reach the tokens before it."""
+    lens = [70, 33]
+    p, c, table, q, rk, rv = make(7, ct, lens, 3, 4, 2, 64, 16)
+    ref = ol.decode_attention(q, rk, rv, lens)
+    for i, L in enumerate(lens):          # the last token's rows
+        pg, o = int(table[i, (L - 1) // 16]), (L - 1) % 16
+        for x in ("k", "v"):
+            if ct == E4:
+                c[x + "_cache"].view(torch.uint8)[pg, :, o] = 0x7f
+            else:
+                c[x + "_cache"][pg, :, o] = float("inf")
+    out, _ = decode(p, c, table, q, lens)
+    got = out.cpu().double().numpy()
+    tol = ol.attention_tolerance(ref[0], ref[2], ref[3], 64, 70, BF)
+    assert np.all(np.abs(got - ref[0])[:, :2] <= tol[:, :2])
+    assert not np.isfinite(got[:, 2]).any()
+
+
+def test_cache_past_4gb():
+    """Rows past 2^32 bytes of the caches are written, read back and attended to."""
+    page, Hkv, D = 64, 8, 128
+    n = (5 << 30) // (page * Hkv * D)           # 5 GB in 8 bits
+    p = ssd.make_kv_cache_problem(n, page, Hkv, D, BF, E4)
+    c = dict(k_cache=torch.empty(n, Hkv, page, D, dtype=torch.uint8, device=DEV).view(E4),
+             v_cache=torch.empty(n, Hkv, page, D, dtype=torch.uint8, device=DEV).view(E4),
+             k_scale=torch.empty(n, Hkv, page, dtype=torch.uint8, device=DEV),
+             v_scale=torch.empty(n, Hkv, page, dtype=torch.uint8, device=DEV))
+    g = torch.Generator().manual_seed(1)
+    L = 100
+    table = torch.tensor([[n - 1, n - 7]], dtype=torch.int32)
+    pos = torch.arange(L)
+    sl = table[0].long()[pos // page] * page + pos % page
+    k, v = (torch.randn(L, Hkv, D, generator=g).to(BF) for _ in range(2))
+    ssd.kv_cache_store(p, k.to(DEV), v.to(DEV), sl.to(DEV), **c)
+    ko, vo = torch.empty(L, Hkv, D, dtype=BF, device=DEV), torch.empty(L, Hkv, D, dtype=BF, device=DEV)
+    ssd.kv_cache_load(p, torch.tensor([0, L], dtype=torch.int32, device=DEV), table.to(DEV),
+                      c["k_cache"], c["v_cache"], c["k_scale"], c["v_scale"], ko, vo)
+    for x, o in ((k, ko), (v, vo)):
+        for t in (0, 63, 64, 99):
+            want, b = ol.encode_row(x[t, 3].double().numpy())
+            assert np.array_equal(o[t, 3].cpu().double().numpy(), want * 2.0 ** (b - 127))
+    q = torch.randn(1, 1, Hkv, D, generator=g).to(BF)
+    out, lse = decode(p, c, table, q, [L])
+    compare(out, lse, ol.decode_attention(q, [ko.cpu()], [vo.cpu()], [L]), D, L)
+
+
+def test_another_stream_and_a_graph():
+    lens = [300, 700]
+    p, c, table, q, rk, rv = make(9, E4, lens, 2, 8, 2, 128, 64)
+    d = ssd.make_attn_decode_problem(p, 2, 2, 8, table.shape[1])
+    ws, qd, td = ssd.alloc_attn_decode_workspace(d, DEV), q.to(DEV), table.to(DEV)
+    ld, out = torch.tensor(lens, dtype=torch.int32, device=DEV), torch.empty_like(q.to(DEV))
+    go = lambda: ssd.attention_decode(d, qd, c["k_cache"], c["v_cache"], c["k_scale"],   # noqa: E731
+                                      c["v_scale"], td, ld, out, workspace=ws)
+    go()
+    want = out.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out.zero_()
+        go()
+    side.synchronize()
+    assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go()
+    for _ in range(3):
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
