@@ -10,13 +10,12 @@ tensor, everything inside a row must be contiguous.
 """
 from __future__ import annotations
 
-import copy
 import ctypes
 import math
 
 import torch
 
-from . import _DT, _TORCH, _check, _lib, _ptr, _stream, _vp
+from . import _DT, _TORCH, _check, _lib, _stream
 from ._layer_abi import (attn_decode_problem, attn_problem, conv_problem, kv_cache_problem,
                          scan_problem)
 
@@ -27,12 +26,9 @@ _CACHE_DT = {torch.bfloat16: _DT[torch.bfloat16], torch.float8_e4m3fn: E4M3}
 _CACHE_TORCH = {v: k for k, v in _CACHE_DT.items()}
 
 
-def _rows(t, name, dtype, lead, row, optional=False):
-    """Pointer and row distance of t [*lead, *row]: the row contiguous, the rows of consecutive
-    tokens (lead flattened) evenly spaced."""
+def _refuse(t, name, dtype, shape):
+    """Says what is wrong with t, if anything is."""
     if t is None:
-        if optional:
-            return None, 0
         raise ValueError(f"{name} is required")
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
@@ -40,33 +36,75 @@ def _rows(t, name, dtype, lead, row, optional=False):
         raise ValueError(f"{name} must be on the GPU (got {t.device})")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
-    shapes = [tuple(lead) + tuple(row)]
-    if len(lead) == 2:
-        shapes.append((lead[0] * lead[1],) + tuple(row))
-    if tuple(t.shape) not in shapes:
-        raise ValueError(f"{name} must have shape {shapes[0]} (got {tuple(t.shape)})")
-    n = math.prod(row)
-    if not t.numel():
-        return _vp(t.data_ptr() or 16), n
-    want = 1
-    for d in range(t.dim() - 1, t.dim() - 1 - len(row), -1):
-        if t.shape[d] != 1 and t.stride(d) != want:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+
+
+# A verify step's kernels take a few microseconds, no more than careless checks of their arguments
+# would: pointers are passed as plain integers, and what is in order is passed with one look at
+# each property.
+
+def _arr(t, name, dtype, shape, optional=False):
+    """Pointer of a contiguous array (an empty one's may be anything)."""
+    if t is None and optional:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape):
+        _refuse(t, name, dtype, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_arr() or 16
+
+
+def _rows(t, name, dtype, shape, k, optional=False):
+    """Pointer and row distance of t: the last k dimensions of `shape` are a token's row and
+    contiguous, the rows of consecutive tokens (the dimensions before) evenly spaced. Tokens given
+    as [R,T] may also come as [R T]."""
+    if t is None and optional:
+        return None, 0
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape):
+        flat = (-1,) if len(shape) - k < 2 else (shape[0] * shape[1],) + tuple(shape[2:])
+        if not isinstance(t, torch.Tensor) or tuple(t.shape) != flat:
+            _refuse(t, name, dtype, shape)
+        _refuse(t, name, dtype, flat)
+        shape = flat
+    n = math.prod(shape[-k:])
+    if t.is_contiguous():
+        return t.data_arr() or 16, n
+    st, nl, want = t.stride(), len(shape) - k, 1
+    for d in range(len(shape) - 1, nl - 1, -1):
+        if shape[d] != 1 and st[d] != want:
             raise ValueError(f"{name}: the elements of a token's row must be contiguous")
-        want *= t.shape[d]
-    nl = t.dim() - len(row)
-    stride = n if t.shape[nl - 1] == 1 else t.stride(nl - 1)
-    if nl == 2:
-        if t.shape[1] == 1:
-            stride = n if t.shape[0] == 1 else t.stride(0)
-        elif t.shape[0] != 1 and t.stride(0) != t.shape[1] * stride:
+        want *= shape[d]
+    if nl == 1:
+        stride = st[0] if shape[0] > 1 else n
+    elif shape[1] == 1:
+        stride = st[0] if shape[0] > 1 else n
+    else:
+        stride = st[1]
+        if shape[0] > 1 and st[0] != shape[1] * stride:
             raise ValueError(f"{name}: token rows must be evenly spaced")
     if stride < n:
         raise ValueError(f"{name}: token rows overlap")
-    return _vp(t.data_ptr()), stride
+    return t.data_arr() or 16, stride
+
+
+def _on(stream):
+    """The stream's handle; None: the current one of the current device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return _stream(stream)
+
+
+def _workspace(w):
+    if w is None:
+        return None, 0
+    n = w.numel() if isinstance(w, torch.Tensor) else 0
+    return _arr(w, "workspace", torch.uint8, (n,)), n
 
 
 def _with(p, **strides):
-    q = copy.copy(p)
+    """A copy of the problem with these row distances."""
+    q = type(p).from_buffer_copy(p)
     for k, v in strides.items():
         setattr(q, k, v)
     return q
@@ -86,37 +124,26 @@ def make_conv_problem(total_tokens: int, num_seqs: int, channels: int, width: in
     return p
 
 
-def _conv_y(p, y):
-    """The problem with the outputs' channels and row distances, and their pointers."""
-    ys = tuple(y) if isinstance(y, (tuple, list)) else (y,)
+def _conv_args(p, x, weight, bias, conv_cache, state_indices, y):
+    """The problem with its row distances and the outputs' shares of the channels, and the
+    pointers that the prompt form and the update have in common."""
+    q, ti, T, C = type(p).from_buffer_copy(p), _TORCH[p.in_dtype], p.total_tokens, p.channels
+    ys = (y,) if isinstance(y, torch.Tensor) else tuple(y)
     if not 1 <= len(ys) <= 3:
         raise ValueError("y must be one tensor, or two or three that share the channels")
-    q, ptrs = copy.copy(p), []
-    q.y_channels, q.y_stride = (ctypes.c_int32 * 3)(), (ctypes.c_int64 * 3)()
+    out, total = [None, None, None], 0
     for i, t in enumerate(ys):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("y must be a torch tensor")
-        c = int(t.shape[-1]) if t.dim() else 0
-        ptr, stride = _rows(t, f"y[{i}]", _TORCH[p.in_dtype], (p.total_tokens,), (c,))
-        q.y_channels[i], q.y_stride[i] = c, stride
-        ptrs.append(ptr)
-    if sum(q.y_channels) != p.channels:
-        raise ValueError(f"y must have {p.channels} channels together (got {sum(q.y_channels)})")
-    return q, ptrs + [None] * (3 - len(ptrs))
-
-
-def _conv_common(p, x, weight, bias, conv_cache, state_indices, y):
-    q, ys = _conv_y(p, y)
-    xp, q.x_stride = _rows(x, "x", _TORCH[p.in_dtype], (p.total_tokens,), (p.channels,))
-    return (q, xp, _ptr(weight, "weight", torch.float32, (p.channels, p.width)),
-            _ptr(bias, "bias", torch.float32, (p.channels,), optional=True),
-            _conv_cache(p, conv_cache),
-            _ptr(state_indices, "state_indices", torch.int32, (p.num_seqs,)), ys)
-
-
-def _conv_cache(p, conv_cache):
-    return _ptr(conv_cache, "conv_cache", _TORCH[p.state_dtype],
-                (p.num_slots, p.width - 1, p.channels))
+        c = t.shape[-1] if isinstance(t, torch.Tensor) and t.dim() else 0
+        out[i], q.y_stride[i] = _rows(t, "y", ti, (T, c), 1)
+        q.y_channels[i] = c
+        total += c
+    if total != C:
+        raise ValueError(f"y must have {C} channels together (got {total})")
+    xp, q.x_stride = _rows(x, "x", ti, (T, C), 1)
+    return (q, xp, _arr(weight, "weight", torch.float32, (C, p.width)),
+            _arr(bias, "bias", torch.float32, (C,), True),
+            _arr(conv_cache, "conv_cache", _TORCH[p.state_dtype], (p.num_slots, p.width - 1, C)),
+            _arr(state_indices, "state_indices", torch.int32, (p.num_seqs,)), out)
 
 
 def causal_conv1d_varlen(p: conv_problem, x, weight, bias, cu_seqlens, conv_cache, state_indices,
@@ -124,12 +151,12 @@ def causal_conv1d_varlen(p: conv_problem, x, weight, bias, cu_seqlens, conv_cach
     """y = act(conv(x)) over packed sequences; y: [T,C], or a tuple of up to three tensors that
     share the channels. The cache slots [num_slots,W-1,C] are read where has_initial_state is
     set, and left with each sequence's last W-1 tokens."""
-    q, xp, w, b, cache, idx, ys = _conv_common(p, x, weight, bias, conv_cache, state_indices, y)
+    q, xp, w, b, cache, idx, ys = _conv_args(p, x, weight, bias, conv_cache, state_indices, y)
     rc = _lib.causal_conv1d_varlen(
         ctypes.byref(q), xp, w, b,
-        _ptr(cu_seqlens, "cu_seqlens", torch.int32, (p.num_seqs + 1,)), cache, idx,
-        _ptr(has_initial_state, "has_initial_state", torch.uint8, (p.num_seqs,), optional=True),
-        *ys, _stream(stream))
+        _arr(cu_seqlens, "cu_seqlens", torch.int32, (p.num_seqs + 1,)), cache, idx,
+        _arr(has_initial_state, "has_initial_state", torch.uint8, (p.num_seqs,), True),
+        *ys, _on(stream))
     _check("causal_conv1d_varlen", rc)
 
 
@@ -137,19 +164,21 @@ def causal_conv1d_update(p: conv_problem, x, weight, bias, conv_cache, state_ind
                          update_cache: bool = True, stream=None):
     """Decode / MTP verify: x [T,C], request r owning rows r T/R .. (r+1) T/R - 1 and continuing
     its slot. update_cache=False leaves the cache for causal_conv1d_commit."""
-    q, xp, w, b, cache, idx, ys = _conv_common(p, x, weight, bias, conv_cache, state_indices, y)
+    q, xp, w, b, cache, idx, ys = _conv_args(p, x, weight, bias, conv_cache, state_indices, y)
     rc = _lib.causal_conv1d_update(ctypes.byref(q), xp, w, b, cache, idx, *ys,
-                                   int(bool(update_cache)), _stream(stream))
+                                   int(bool(update_cache)), _on(stream))
     _check("causal_conv1d_update", rc)
 
 
 def causal_conv1d_commit(p: conv_problem, x, conv_cache, state_indices, num_accepted, stream=None):
     """After a verify step with update_cache=False: slot r takes 1 + num_accepted[r] tokens in."""
-    xp, xs = _rows(x, "x", _TORCH[p.in_dtype], (p.total_tokens,), (p.channels,))
+    xp, xs = _rows(x, "x", _TORCH[p.in_dtype], (p.total_tokens, p.channels), 1)
     rc = _lib.causal_conv1d_commit(
-        ctypes.byref(_with(p, x_stride=xs)), xp, _conv_cache(p, conv_cache),
-        _ptr(state_indices, "state_indices", torch.int32, (p.num_seqs,)),
-        _ptr(num_accepted, "num_accepted", torch.int32, (p.num_seqs,)), _stream(stream))
+        ctypes.byref(_with(p, x_stride=xs)), xp,
+        _arr(conv_cache, "conv_cache", _TORCH[p.state_dtype],
+             (p.num_slots, p.width - 1, p.channels)),
+        _arr(state_indices, "state_indices", torch.int32, (p.num_seqs,)),
+        _arr(num_accepted, "num_accepted", torch.int32, (p.num_seqs,)), _on(stream))
     _check("causal_conv1d_commit", rc)
 
 
@@ -177,16 +206,16 @@ def alloc_scan_workspace(p: scan_problem, device="cuda"):
 
 
 def _scan_common(p, x, dt, A, B, C, D, z, y):
-    ti, T, ch, gn = _TORCH[p.in_dtype], (p.total_tokens,), (p.channels,), (p.ngroups, p.d_state)
-    xp, xs = _rows(x, "x", ti, T, ch)
-    dp, ds = _rows(dt, "dt", ti, T, ch)
-    bp, bs = _rows(B, "B", ti, T, gn)
-    cp, cs = _rows(C, "C", ti, T, gn)
-    zp, zs = _rows(z, "z", ti, T, ch, optional=True)
-    yp, ys = _rows(y, "y", ti, T, ch)
-    q = _with(p, x_stride=xs, dt_stride=ds, b_stride=bs, c_stride=cs, z_stride=zs, y_stride=ys)
-    return (q, yp, xp, dp, _ptr(A, "A", torch.float32, (p.channels, p.d_state)), bp, cp,
-            _ptr(D, "D", torch.float32, ch, optional=True), zp)
+    ti, T, ch, N = _TORCH[p.in_dtype], p.total_tokens, p.channels, p.d_state
+    q, row, bc = type(p).from_buffer_copy(p), (T, ch), (T, p.ngroups, N)
+    xp, q.x_stride = _rows(x, "x", ti, row, 1)
+    dp, q.dt_stride = _rows(dt, "dt", ti, row, 1)
+    bp, q.b_stride = _rows(B, "B", ti, bc, 2)
+    cp, q.c_stride = _rows(C, "C", ti, bc, 2)
+    zp, q.z_stride = _rows(z, "z", ti, row, 1, True)
+    yp, q.y_stride = _rows(y, "y", ti, row, 1)
+    return (q, yp, xp, dp, _arr(A, "A", torch.float32, (ch, N)), bp, cp,
+            _arr(D, "D", torch.float32, (ch,), True), zp)
 
 
 def _scan_transform(p, tf):
@@ -206,13 +235,12 @@ def selective_scan_varlen(p: scan_problem, x, dt, A, B, C, D, z, dt_transform, c
     q, yp, *a = _scan_common(p, x, dt, A, B, C, D, z, y)
     rc = _lib.selective_scan_varlen(
         ctypes.byref(q), *a, _scan_transform(p, dt_transform),
-        _ptr(cu_seqlens, "cu_seqlens", torch.int32, (p.num_seqs + 1,)),
-        _ptr(state_cache, "state_cache", _TORCH[p.state_dtype],
+        _arr(cu_seqlens, "cu_seqlens", torch.int32, (p.num_seqs + 1,)),
+        _arr(state_cache, "state_cache", _TORCH[p.state_dtype],
              (p.num_slots, p.channels, p.d_state)),
-        _ptr(state_indices, "state_indices", torch.int32, (p.num_seqs,)),
-        _ptr(has_initial_state, "has_initial_state", torch.uint8, (p.num_seqs,), optional=True),
-        yp, _ptr(workspace, "workspace", torch.uint8, optional=True),
-        ctypes.c_size_t(0 if workspace is None else workspace.numel()), _stream(stream))
+        _arr(state_indices, "state_indices", torch.int32, (p.num_seqs,)),
+        _arr(has_initial_state, "has_initial_state", torch.uint8, (p.num_seqs,), True),
+        yp, *_workspace(workspace), _on(stream))
     _check("selective_scan_varlen", rc)
 
 
@@ -225,10 +253,10 @@ def selective_scan_update(p: scan_problem, x, dt, A, B, C, D, z, dt_transform, s
     ts, cn = _TORCH[p.state_dtype], (p.channels, p.d_state)
     rc = _lib.selective_scan_update(
         ctypes.byref(q), *a, _scan_transform(p, dt_transform),
-        _ptr(state_cache, "state_cache", ts, (p.num_slots,) + cn),
-        _ptr(state_indices, "state_indices", torch.int32, (p.num_seqs,)), yp,
-        _ptr(intermediate_states, "intermediate_states", ts, (p.total_tokens,) + cn,
-             optional=True), _stream(stream))
+        _arr(state_cache, "state_cache", ts, (p.num_slots,) + cn),
+        _arr(state_indices, "state_indices", torch.int32, (p.num_seqs,)), yp,
+        _arr(intermediate_states, "intermediate_states", ts, (p.total_tokens,) + cn,
+             True), _on(stream))
     _check("selective_scan_update", rc)
 
 
@@ -251,15 +279,16 @@ def attention_varlen(p: attn_problem, q, k, v, cu_seqlens_q, cu_seqlens_k, out, 
     """q, out [total_q,H,D]; k, v [total_k,Hkv,D]; lse [total_q,H] float32 or None. Causal
     queries are the last ones of their sequence's keys."""
     t = _TORCH[p.dtype]
-    qp, qs = _rows(q, "q", t, (p.total_q,), (p.nheads, p.headdim))
-    kp, ks = _rows(k, "k", t, (p.total_k,), (p.nkv_heads, p.headdim))
-    vp, vs = _rows(v, "v", t, (p.total_k,), (p.nkv_heads, p.headdim))
-    op, os_ = _rows(out, "out", t, (p.total_q,), (p.nheads, p.headdim))
+    qrow, krow = (p.total_q, p.nheads, p.headdim), (p.total_k, p.nkv_heads, p.headdim)
+    qp, qs = _rows(q, "q", t, qrow, 2)
+    kp, ks = _rows(k, "k", t, krow, 2)
+    vp, vs = _rows(v, "v", t, krow, 2)
+    op, os_ = _rows(out, "out", t, qrow, 2)
     rc = _lib.attention_varlen(
         ctypes.byref(_with(p, q_stride=qs, k_stride=ks, v_stride=vs, o_stride=os_)), qp, kp, vp,
-        _ptr(cu_seqlens_q, "cu_seqlens_q", torch.int32, (p.num_seqs + 1,)),
-        _ptr(cu_seqlens_k, "cu_seqlens_k", torch.int32, (p.num_seqs + 1,)), op,
-        _ptr(lse, "lse", torch.float32, (p.total_q, p.nheads), optional=True), _stream(stream))
+        _arr(cu_seqlens_q, "cu_seqlens_q", torch.int32, (p.num_seqs + 1,)),
+        _arr(cu_seqlens_k, "cu_seqlens_k", torch.int32, (p.num_seqs + 1,)), op,
+        _arr(lse, "lse", torch.float32, (p.total_q, p.nheads), True), _on(stream))
     _check("attention_varlen", rc)
 
 
@@ -293,10 +322,10 @@ def _kv_ptrs(p, k_cache, v_cache, k_scale, v_scale):
     none = p.cache_dtype != E4M3
     if none and (k_scale is not None or v_scale is not None):
         raise ValueError("a bfloat16 cache has no scales")
-    return (_ptr(k_cache, "k_cache", t, shape + (p.headdim,)),
-            _ptr(v_cache, "v_cache", t, shape + (p.headdim,)),
-            _ptr(k_scale, "k_scale", torch.uint8, shape, optional=none),
-            _ptr(v_scale, "v_scale", torch.uint8, shape, optional=none))
+    return (_arr(k_cache, "k_cache", t, shape + (p.headdim,)),
+            _arr(v_cache, "v_cache", t, shape + (p.headdim,)),
+            _arr(k_scale, "k_scale", torch.uint8, shape, none),
+            _arr(v_scale, "v_scale", torch.uint8, shape, none))
 
 
 def kv_cache_store(p: kv_cache_problem, k, v, slot_mapping, k_cache, v_cache, k_scale=None,
@@ -305,13 +334,14 @@ def kv_cache_store(p: kv_cache_problem, k, v, slot_mapping, k_cache, v_cache, k_
     negative: skipped), in the cache's type."""
     if not isinstance(k, torch.Tensor):
         raise TypeError("k must be a torch tensor")
-    n, row, t = int(k.shape[0]), (p.nkv_heads, p.headdim), _TORCH[p.in_dtype]
-    kp, ks = _rows(k, "k", t, (n,), row)
-    vp, vs = _rows(v, "v", t, (n,), row)
+    n, t = (k.shape[0] if k.dim() else 0), _TORCH[p.in_dtype]
+    row = (n, p.nkv_heads, p.headdim)
+    kp, ks = _rows(k, "k", t, row, 2)
+    vp, vs = _rows(v, "v", t, row, 2)
     rc = _lib.kv_cache_store(
         ctypes.byref(_with(p, k_stride=ks, v_stride=vs)), n, kp, vp,
-        _ptr(slot_mapping, "slot_mapping", torch.int64, (n,)),
-        *_kv_ptrs(p, k_cache, v_cache, k_scale, v_scale), _stream(stream))
+        _arr(slot_mapping, "slot_mapping", torch.int64, (n,)),
+        *_kv_ptrs(p, k_cache, v_cache, k_scale, v_scale), _on(stream))
     _check("kv_cache_store", rc)
 
 
@@ -323,15 +353,15 @@ def kv_cache_load(p: kv_cache_problem, cu_seqlens, block_table, k_cache, v_cache
         raise TypeError("k and block_table must be torch tensors")
     if block_table.dim() != 2:
         raise ValueError("block_table must have shape (num_seqs, max_pages)")
-    n, row, t = int(k.shape[0]), (p.nkv_heads, p.headdim), _TORCH[p.in_dtype]
-    S, mp = (int(d) for d in block_table.shape)
-    kp, ks = _rows(k, "k", t, (n,), row)
-    vp, vs = _rows(v, "v", t, (n,), row)
+    n, t = (k.shape[0] if k.dim() else 0), _TORCH[p.in_dtype]
+    row, (S, mp) = (n, p.nkv_heads, p.headdim), block_table.shape
+    kp, ks = _rows(k, "k", t, row, 2)
+    vp, vs = _rows(v, "v", t, row, 2)
     rc = _lib.kv_cache_load(
         ctypes.byref(_with(p, k_stride=ks, v_stride=vs)), n, S, mp,
-        _ptr(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,)),
-        _ptr(block_table, "block_table", torch.int32),
-        *_kv_ptrs(p, k_cache, v_cache, k_scale, v_scale), kp, vp, _stream(stream))
+        _arr(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,)),
+        _arr(block_table, "block_table", torch.int32, (S, mp)),
+        *_kv_ptrs(p, k_cache, v_cache, k_scale, v_scale), kp, vp, _on(stream))
     _check("kv_cache_load", rc)
 
 
@@ -362,15 +392,15 @@ def attention_decode(p: attn_decode_problem, q, k_cache, v_cache, k_scale, v_sca
     """q, out [R,T,H,D]: the last T of each request's context_lens [R] cached tokens (their own
     keys included); block_table [R,max_pages]; lse [R,T,H] float32 or None; workspace:
     alloc_attn_decode_workspace(p)."""
-    R, T, row, t = p.num_reqs, p.tokens_per_req, (p.nheads, p.kv.headdim), _TORCH[p.kv.in_dtype]
-    qp, qs = _rows(q, "q", t, (R, T), row)
-    op, os_ = _rows(out, "out", t, (R, T), row)
+    R, T, t = p.num_reqs, p.tokens_per_req, _TORCH[p.kv.in_dtype]
+    row = (R, T, p.nheads, p.kv.headdim)
+    qp, qs = _rows(q, "q", t, row, 2)
+    op, os_ = _rows(out, "out", t, row, 2)
     rc = _lib.attention_decode(
         ctypes.byref(_with(p, q_stride=qs, o_stride=os_)), qp,
         *_kv_ptrs(p.kv, k_cache, v_cache, k_scale, v_scale),
-        _ptr(block_table, "block_table", torch.int32, (R, p.max_pages)),
-        _ptr(context_lens, "context_lens", torch.int32, (R,)), op,
-        _ptr(lse, "lse", torch.float32, (R, T, p.nheads), optional=True),
-        _ptr(workspace, "workspace", torch.uint8, optional=True),
-        ctypes.c_size_t(0 if workspace is None else workspace.numel()), _stream(stream))
+        _arr(block_table, "block_table", torch.int32, (R, p.max_pages)),
+        _arr(context_lens, "context_lens", torch.int32, (R,)), op,
+        _arr(lse, "lse", torch.float32, (R, T, p.nheads), True),
+        *_workspace(workspace), _on(stream))
     _check("attention_decode", rc)
