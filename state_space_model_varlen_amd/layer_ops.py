@@ -52,7 +52,7 @@ def _arr(t, name, dtype, shape, optional=False):
         _refuse(t, name, dtype, shape)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.data_arr() or 16
+    return t.data_ptr() or 16
 
 
 def _rows(t, name, dtype, shape, k, optional=False):
@@ -69,7 +69,7 @@ def _rows(t, name, dtype, shape, k, optional=False):
         shape = flat
     n = math.prod(shape[-k:])
     if t.is_contiguous():
-        return t.data_arr() or 16, n
+        return t.data_ptr() or 16, n
     st, nl, want = t.stride(), len(shape) - k, 1
     for d in range(len(shape) - 1, nl - 1, -1):
         if shape[d] != 1 and st[d] != want:
@@ -85,7 +85,7 @@ def _rows(t, name, dtype, shape, k, optional=False):
             raise ValueError(f"{name}: token rows must be evenly spaced")
     if stride < n:
         raise ValueError(f"{name}: token rows overlap")
-    return t.data_arr() or 16, stride
+    return t.data_ptr() or 16, stride
 
 
 def _on(stream):
