@@ -107,6 +107,9 @@ int scan_dims(const scan_problem *p, bool uniform, const ssd_dt_transform *tf, s
         !stride_of(p->z_stride, p->channels, &d->zs) || !stride_of(p->b_stride, gn, &d->bs) ||
         !stride_of(p->c_stride, gn, &d->cs) || !stride_of(p->y_stride, p->channels, &d->ys))
         return SSD_ERR_SHAPE;
+    // a stage of up to 64 rows is addressed by 32-bit byte offsets
+    for (int64_t v : {d->xs, d->dts, d->zs, d->bs, d->cs, d->ys})
+        if (v > (1 << 21)) return SSD_ERR_UNSUPPORTED;
     d->tf = ssd::DtTf();
     if (tf) {
         if (!(tf->dt_min <= tf->dt_max)) return SSD_ERR_SHAPE;   // (NaN bounds fail too)

@@ -113,6 +113,31 @@ __device__ __forceinline__ SeqTile find_tile(const int32_t *__restrict__ cu, int
     return SeqTile{-1, 0, 0, 0};
 }
 
+// The b-th longest of up to 64 sequences, whole (of equal ones the first): blocks
+// are started in order, so the longest chains start first. Every lane of the
+// wave takes part: a lane's sequence counts those in front of it.
+__device__ __forceinline__ SeqTile longest_first(const int32_t *__restrict__ cu, int S, int total,
+                                                 int b) {
+    const int s = threadIdx.x & (kWave - 1);
+    int a = 0, len = -1;
+    if (s < S) {
+        a = cu[s];
+        const int e = cu[s + 1];
+        a = a < 0 ? 0 : (a > total ? total : a);
+        const int ec = e < 0 ? 0 : (e > total ? total : e);
+        len = ec > a ? ec - a : 0;
+    }
+    int rank = 0;
+    for (int j = 0; j < S; ++j) {
+        const int o = __builtin_amdgcn_readlane(len, j);
+        rank += o > len || (o == len && j < s) ? 1 : 0;
+    }
+    const uint64_t mine = __ballot(s < S && rank == b);
+    if (!mine) return SeqTile{-1, 0, 0, 0};
+    const int src = __ffsll((unsigned long long)mine) - 1;
+    return SeqTile{src, __builtin_amdgcn_readlane(a, src), __builtin_amdgcn_readlane(len, src), 0};
+}
+
 // The same for a batch whose sequences all have `len` tokens.
 __device__ __forceinline__ SeqTile uniform_tile(int S, int len, int tile, int b) {
     const int per = len > 0 ? (len - 1) / tile + 1 : 1;

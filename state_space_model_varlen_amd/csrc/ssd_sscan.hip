@@ -10,31 +10,28 @@
 // prompt form. The single-token form is bound by the states it reads and writes.
 #include "ssd_layer.h"
 #include "ssd_layer_device.h"
+#include <cmath>
 
 namespace ssd {
 
 // softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|) <= 1, with
-// log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, summed to s^13 (the next
-// term is under 2^-25 of the sum): accurate relative to the result also where
-// e is small, which a logarithm of the rounded 1 + e is not.
+// log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3: s times a polynomial in s^2,
+// fitted on [0, 1/9] at Chebyshev's points to 4e-9 relative. Accurate relative
+// to the result also where e is small, which a logarithm of the rounded 1 + e
+// is not, and half the operations of the library's log1p.
 __device__ __forceinline__ float softplus(float v) {
     const float e = __expf(-fabsf(v));
     const float s = e * __builtin_amdgcn_rcpf(2.0f + e);
     const float q = s * s;
-    float p = 2.0f / 13.0f;
-    p = p * q + 2.0f / 11.0f;
-    p = p * q + 2.0f / 9.0f;
-    p = p * q + 2.0f / 7.0f;
-    p = p * q + 2.0f / 5.0f;
-    p = p * q + 2.0f / 3.0f;
+    float p = 0.28174657f;
+    p = p * q + 0.27961418f;
+    p = p * q + 0.40024853f;
+    p = p * q + 0.66666317f;
     p = p * q + 2.0f;
     return fmaxf(v, 0.0f) + p * s;
 }
-// (NaN steps stay NaN: fminf and fmaxf would drop them)
 __device__ __forceinline__ float step_size(const DtTf &tf, float raw, float bias) {
-    if (!tf.on) return raw;
-    const float sp = softplus(raw + bias);
-    return sp != sp ? sp : fminf(fmaxf(sp, tf.lo), tf.hi);
+    return tf.on ? __builtin_amdgcn_fmed3f(softplus(raw + bias), tf.lo, tf.hi) : raw;
 }
 __device__ __forceinline__ float silu(float z) {
     return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
@@ -99,128 +96,308 @@ template <typename T, int M> __device__ __forceinline__ void store_state(T *p, c
 }
 
 // Prompt form. L lanes per channel hold SPL = N / L states each, in registers
-// for the whole sequence; a block of 4 waves takes 256 / L channels of one
-// group and one sequence. The tokens are taken in groups of L: lane j of a
-// channel reads x, dt and z of the group's token j, prepares its step size and
-// gate once, and the group's L tokens are then run through one after the
-// other, each lane taking token j's values from lane j. B and C of a stage of
-// ST tokens are widened to float in LDS by the whole block (two buffers, one
-// barrier a stage); the next stage's loads are in flight meanwhile.
+// for as long as the block runs; a block of 4 waves takes 256 / L channels of
+// one group and one sequence, or one segment of it. The tokens are taken in
+// groups of L: lane j of a channel reads x, dt and z of the group's token j,
+// prepares its step size and gate once, and the group's L tokens are then run
+// through one after the other, each lane taking token j's values from lane j.
+// B and C of a stage of ST tokens are widened to float in LDS by the whole
+// block (two buffers, one barrier a stage); the next stage's loads are in
+// flight meanwhile. Rows are read through buffer resources that end with the
+// sequence, so tokens past it come as zeros and are dropped on the way out.
+//
+// Segments. One sequence is a chain, and few channels leave most of the chip
+// idle; then sequences are cut into segments of `seg` tokens. The recurrence
+// is linear in its starting state: a first launch runs every segment but the
+// last from zero (the first one from its cached state, finished at once) and
+// keeps its final state and the sum of its steps; a second one chains those in
+// front of it, exp(A sum dt) state + final, and runs each later segment again,
+// with outputs. `cur` says which launch this is: 0 the only one, 1 and 2.
+struct ScanSegs {
+    int seg, cur;
+    float *fin, *sum;   // [segments][C][N] final states, [segments][C] sums of steps
+};
+
+// One element through a resource, `row` bytes (a scalar, counted by the range check) and `off`
+// into it; a register of its own until it is widened.
+template <typename TX> __device__ __forceinline__ uint32_t buf_one(rsrc_t r, int off, int row) {
+    if constexpr (sizeof(TX) == 2)
+        return (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(r, off, row, 0);
+    else
+        return __builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0);
+}
+template <typename TX> __device__ __forceinline__ float widen_one(uint32_t w) {
+    return __uint_as_float(sizeof(TX) == 2 ? w << 16 : w);
+}
+template <typename TX> __device__ __forceinline__ void buf_put(rsrc_t r, float v, int off, int row) {
+    const TX t = from_f32<TX>(v);
+    if constexpr (sizeof(TX) == 2)
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, t), r, off, row, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(t), r, off, row, 0);
+}
+
 template <typename TX, typename TS, int N, int L>
 __global__ __launch_bounds__(256) void scan_kernel(
     int T, int S, int C, int G, int num_slots, int chb, ScanArgs a, int64_t xs, int64_t dts,
-    int64_t zs, int64_t bs, int64_t cs, int64_t ys, DtTf tf)
+    int64_t zs, int64_t bs, int64_t cs, int64_t ys, DtTf tf, ScanSegs sg)
 {
     constexpr int SPL = N / L, CB = 256 / L;
     constexpr int GROUPS = L == 16 ? 4 : 8;      // groups of L tokens in a stage
     constexpr int ST = L * GROUPS;
     constexpr int BCV = ST * N * 2 / 256;        // B, C values a thread stages
+    constexpr int E = (int)sizeof(TX);
     __shared__ __align__(16) float bc[2][2][ST][N];
     const int tid = threadIdx.x, lane = tid & (kWave - 1), j0 = tid % L;
+    // Blocks go to the 8 XCDs in turn; the 4 blocks of L = 16 that share a row's 128
+    // bytes are dealt to one XCD, whose L2 then fetches the line once.
+    unsigned id = blockIdx.x;
+    if (L == 16 && (id | 31u) < gridDim.x) id = (id & ~31u) | (id & 7u) << 2 | (id >> 3 & 3u);
+    const int b = (int)(id / (unsigned)chb), cb = (int)(id % (unsigned)chb);
+    const SeqTile tile = sg.cur == 0 && S > 1 && S <= kWave ? longest_first(a.cu, S, T, b)
+                                                           : find_tile(a.cu, S, T, sg.seg, 1, b);
+    if (tile.seq < 0) return;
+    const bool first = tile.t0 == 0, last = tile.t0 >= tile.len - sg.seg;
+    if (sg.cur == 1 ? !first && last : sg.cur == 2 && first) return;
     const int per = C / G, gblocks = chb / G;
-    const int s = (int)(blockIdx.x / (unsigned)chb), cb = (int)(blockIdx.x % (unsigned)chb);
-    const int g = cb / gblocks;
-    const int in_g = (cb % gblocks) * CB + tid / L;
-    const bool live = in_g < per;
-    const int c = g * per + (live ? in_g : per - 1);
-
-    int start = a.cu[s], end = a.cu[s + 1];
-    start = start < 0 ? 0 : (start > T ? T : start);
-    end = end < 0 ? 0 : (end > T ? T : end);
-    const int len = end > start ? end - start : 0;
-    const int slot = a.idx[s];
+    const int g = cb / gblocks, c_first = (cb % gblocks) * CB;
+    const bool live = c_first + tid / L < per;
+    const int c = g * per + (live ? c_first + tid / L : per - 1);
+    const int len = tile.len - tile.t0 < sg.seg ? tile.len - tile.t0 : sg.seg;
+    const int64_t row0 = tile.start + tile.t0;
+    const int slot = scalar(a.idx[tile.seq]);
     const bool slot_ok = slot >= 0 && slot < num_slots;
-    const int64_t so = ((int64_t)(slot_ok ? slot : 0) * C + c) * N + j0 * SPL;
-    TS *const cache = static_cast<TS *>(a.cache) + so;
+    const int64_t so = (int64_t)c * N + j0 * SPL;
+    TS *const cache = static_cast<TS *>(a.cache) + (int64_t)(slot_ok ? slot : 0) * C * N + so;
 
     float A2[SPL], h[SPL];
 #pragma unroll
     for (int i = 0; i < SPL; ++i) {
-        A2[i] = a.A[(int64_t)c * N + j0 * SPL + i] * kLog2e;
+        A2[i] = a.A[so + i] * kLog2e;
         h[i] = 0.0f;
     }
-    if (slot_ok && a.has && a.has[s]) load_state<TS, SPL>(cache, h);
+    if (first) {
+        if (slot_ok && a.has && a.has[tile.seq]) load_state<TS, SPL>(cache, h);
+    } else if (sg.cur == 2) {
+        const int f = b - tile.t0 / sg.seg;
+        load_state<float, SPL>(sg.fin + (int64_t)f * C * N + so, h);
+        constexpr int AT = 32 / SPL;          // segments requested at once
+        for (int k = f + 1; k < b; k += AT) {
+            float add[AT][SPL], d[AT];
+#pragma unroll
+            for (int u = 0; u < AT; ++u) {
+                const int64_t at = k + u < b ? k + u : b - 1;
+                load_state<float, SPL>(sg.fin + at * C * N + so, add[u]);
+                d[u] = sg.sum[at * C + c];
+            }
+#pragma unroll
+            for (int u = 0; u < AT; ++u)
+                if (k + u < b)
+#pragma unroll
+                    for (int i = 0; i < SPL; ++i)
+                        h[i] = fmaf(__builtin_amdgcn_exp2f(d[u] * A2[i]), h[i], add[u][i]);
+        }
+    }
+    const bool out = sg.cur != 1 || first;       // outputs wanted, not the final state alone
     const float Dc = a.D ? a.D[c] : 0.0f, bias = tf.bias ? tf.bias[c] : 0.0f;
-    const TX *const xp = static_cast<const TX *>(a.x) + (int64_t)start * xs + c;
-    const TX *const dp = static_cast<const TX *>(a.dt) + (int64_t)start * dts + c;
-    const TX *const zp = a.z ? static_cast<const TX *>(a.z) + (int64_t)start * zs + c : nullptr;
-    TX *const yp = static_cast<TX *>(a.y) + (int64_t)start * ys + c;
-    const TX *const Bp = static_cast<const TX *>(a.B) + (int64_t)start * bs + (int64_t)g * N;
-    const TX *const Cp = static_cast<const TX *>(a.C) + (int64_t)start * cs + (int64_t)g * N;
+    const bool gated = a.z != nullptr;
+    const TX *const xb = static_cast<const TX *>(a.x) + row0 * xs;
+    const TX *const db = static_cast<const TX *>(a.dt) + row0 * dts;
+    const TX *const zb = static_cast<const TX *>(gated ? a.z : a.x) + row0 * zs;
+    TX *const yb = static_cast<TX *>(a.y) + row0 * ys;
+    const TX *const Bb = static_cast<const TX *>(a.B) + row0 * bs + (int64_t)g * N;
+    const TX *const Cb = static_cast<const TX *>(a.C) + row0 * cs + (int64_t)g * N;
+    // a lane's place in a stage's rows: its token of the first group, its channel
+    const int xo = (j0 * (int)xs + c) * E, dto = (j0 * (int)dts + c) * E;
+    const int zo = (j0 * (int)zs + c) * E;
+    // (a lane without a channel writes past the end: dropped)
+    const int yo = live ? (j0 * (int)ys + c) * E : 0x40000000;
 
-    TX xv[GROUPS], dv[GROUPS], zv[GROUPS], bv[BCV];
+    uint32_t xv[GROUPS], dv[GROUPS], zv[GROUPS], bv[BCV];
     auto request = [&](int t0) {
+        const int n = len - t0 < ST ? len - t0 : ST;
+        const rsrc_t rx = make_rsrc(xb + t0 * xs, (uint32_t)((n - 1) * (int)xs + C) * E);
+        const rsrc_t rd = make_rsrc(db + t0 * dts, (uint32_t)((n - 1) * (int)dts + C) * E);
+        const rsrc_t rz = make_rsrc(zb + t0 * zs, gated ? (uint32_t)((n - 1) * (int)zs + C) * E : 0);
+        const rsrc_t rb = make_rsrc(Bb + t0 * bs, (uint32_t)((n - 1) * (int)bs + N) * E);
+        const rsrc_t rc = make_rsrc(Cb + t0 * cs, (uint32_t)((n - 1) * (int)cs + N) * E);
 #pragma unroll
         for (int m = 0; m < GROUPS; ++m) {
-            const int t = t0 + m * L + j0;
-            const int64_t r = t < len ? t : len - 1;
-            xv[m] = xp[r * xs];
-            dv[m] = dp[r * dts];
-            if (zp) zv[m] = zp[r * zs];
+            xv[m] = buf_one<TX>(rx, xo, m * L * (int)xs * E);
+            dv[m] = buf_one<TX>(rd, dto, m * L * (int)dts * E);
+            zv[m] = buf_one<TX>(rz, zo, m * L * (int)zs * E);   // (no gate: an empty resource)
         }
         // value e of the stage: state e % N of token (e / N) % ST, of B then C
 #pragma unroll
         for (int k = 0; k < BCV; ++k) {
-            const int e = tid + 256 * k, n = e % N, t = t0 + (e / N) % ST;
-            const int64_t r = t < len ? t : len - 1;
-            bv[k] = e < ST * N ? Bp[r * bs + n] : Cp[r * cs + n];
+            const int e = tid + 256 * k, n_ = e % N, t = (e / N) % ST;
+            if (256 * k < ST * N) bv[k] = buf_one<TX>(rb, (t * (int)bs + n_) * E, 0);
+            else bv[k] = buf_one<TX>(rc, (t * (int)cs + n_) * E, 0);
         }
     };
+    float steps = 0.0f;       // of the lane's own tokens
     if (len > 0) request(0);
     int buf = 0;
     for (int t0 = 0; t0 < len; t0 += ST, buf ^= 1) {
-        // tokens past the end: B, C zero here and a step of zero below
 #pragma unroll
-        for (int k = 0; k < BCV; ++k) {
-            const int e = tid + 256 * k, t = (e / N) % ST;
-            (&bc[buf][0][0][0])[e] = t0 + t < len ? to_f32(bv[k]) : 0.0f;
-        }
+        for (int k = 0; k < BCV; ++k) (&bc[buf][0][0][0])[tid + 256 * k] = widen_one<TX>(bv[k]);
         float x[GROUPS], dt[GROUPS], gate[GROUPS];
 #pragma unroll
         for (int m = 0; m < GROUPS; ++m) {
-            const bool in = t0 + m * L + j0 < len;
-            x[m] = in ? to_f32(xv[m]) : 0.0f;
-            dt[m] = in ? step_size(tf, to_f32(dv[m]), bias) : 0.0f;
-            gate[m] = zp ? silu(to_f32(zv[m])) : 1.0f;
+            x[m] = widen_one<TX>(xv[m]);
+            dt[m] = step_size(tf, widen_one<TX>(dv[m]), bias);
+            gate[m] = gated ? silu(widen_one<TX>(zv[m])) : 1.0f;
+        }
+        if (t0 + ST > len) {          // tokens past the end take no step: the state stays
+#pragma unroll
+            for (int m = 0; m < GROUPS; ++m)
+                if (t0 + m * L + j0 >= len) dt[m] = 0.0f;
         }
         __syncthreads();
         if (t0 + ST < len) request(t0 + ST);
+        if (sg.cur == 1) {
 #pragma unroll
-        for (int m = 0; m < GROUPS; ++m) {
-            if (t0 + m * L >= len) break;
-            const float dtx = dt[m] * x[m];
-            float part[L];
-            unrolled<L>([&](auto J) {
-                constexpr int j = decltype(J)::value;
-                const float d = from_lane<L, j>(dt[m]), u = from_lane<L, j>(dtx);
-                const float *const Bt = &bc[buf][0][m * L + j][j0 * SPL];
-                const float *const Ct = &bc[buf][1][m * L + j][j0 * SPL];
-                float p = 0.0f;
+            for (int m = 0; m < GROUPS; ++m) steps += dt[m];
+        }
+        if (out) {
+            const int n = len - t0 < ST ? len - t0 : ST;
+            const rsrc_t ry = make_rsrc(yb + t0 * ys, (uint32_t)((n - 1) * (int)ys + C) * E);
+            // With few states a lane, B and C of a group are read from LDS while the group
+            // before is worked on
+            constexpr int AHEAD = L == 16 && SPL <= 2 ? 1 : 0;
+            float Bn[2][L][SPL], Cn[2][L][SPL];
+            auto fetch = [&](int m) {
 #pragma unroll
-                for (int i = 0; i < SPL; ++i) {
-                    h[i] = __builtin_amdgcn_exp2f(d * A2[i]) * h[i] + u * Bt[i];
-                    p = i == 0 ? h[i] * Ct[i] : p + h[i] * Ct[i];
-                }
-                part[j] = p;
-            });
-            const float y = (sum_own<L>(part, lane) + Dc * x[m]) * gate[m];
-            const int t = t0 + m * L + j0;
-            if (live && t < len) yp[(int64_t)t * ys] = from_f32<TX>(y);
+                for (int j = 0; j < L; ++j)
+#pragma unroll
+                    for (int i = 0; i < SPL; ++i) {
+                        Bn[m & 1][j][i] = bc[buf][0][m * L + j][j0 * SPL + i];
+                        Cn[m & 1][j][i] = bc[buf][1][m * L + j][j0 * SPL + i];
+                    }
+            };
+            if (AHEAD) fetch(0);
+#pragma unroll
+            for (int m = 0; m < GROUPS; ++m) {
+                if (m + AHEAD < GROUPS) fetch(m + AHEAD);
+                const float dtx = dt[m] * x[m];
+                float part[L];
+                unrolled<L>([&](auto J) {
+                    constexpr int j = decltype(J)::value;
+                    const float d = from_lane<L, j>(dt[m]), u = from_lane<L, j>(dtx);
+                    float p = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < SPL; ++i) {
+                        h[i] = fmaf(__builtin_amdgcn_exp2f(d * A2[i]), h[i], u * Bn[m & 1][j][i]);
+                        p = i == 0 ? h[i] * Cn[m & 1][j][i] : fmaf(h[i], Cn[m & 1][j][i], p);
+                    }
+                    part[j] = p;
+                });
+                const float y = (sum_own<L>(part, lane) + Dc * x[m]) * gate[m];
+                buf_put<TX>(ry, y, yo, m * L * (int)ys * E);
+            }
+        } else {
+#pragma unroll
+            for (int m = 0; m < GROUPS; ++m) {
+                const float dtx = dt[m] * x[m];
+                unrolled<L>([&](auto J) {
+                    constexpr int j = decltype(J)::value;
+                    const float d = from_lane<L, j>(dt[m]), u = from_lane<L, j>(dtx);
+                    const float *const Bt = &bc[buf][0][m * L + j][j0 * SPL];
+#pragma unroll
+                    for (int i = 0; i < SPL; ++i)
+                        h[i] = fmaf(__builtin_amdgcn_exp2f(d * A2[i]), h[i], u * Bt[i]);
+                });
+            }
         }
     }
-    if (slot_ok && live) store_state<TS, SPL>(cache, h);
+    if (!live) return;
+    if (last) {
+        if (slot_ok) store_state<TS, SPL>(cache, h);
+    } else if (sg.cur == 1) {
+        store_state<float, SPL>(sg.fin + (int64_t)b * C * N + so, h);
+        // the channel's lanes hold the steps of their own tokens
+        steps += dpp<0xb1>(steps);
+        steps += dpp<0x4e>(steps);
+        if constexpr (L == 16) {
+            steps += dpp<0x141>(steps);
+            steps += dpp<0x140>(steps);
+        }
+        if (j0 == 0) sg.sum[(int64_t)b * C + c] = steps;
+    }
 }
 
-size_t scan_workspace(const ScanDims &) { return 0; }
+// Lanes a channel (4 or 16) and tokens a segment (0: whole sequences), from an
+// estimate of each way's time in cycles of a SIMD (1024 of them). Measured with
+// N = 16: a wave alone on its SIMD takes 280 cycles a token with 4 lanes a
+// channel (16 channels a wave) and 117 with 16 (4 channels); waves that share
+// a SIMD 175 and 90 each; both launches of the segmented form together 325.
+//   2 prompts of 100 and 156 tokens, 64 channels: 16 lanes 24 us, 4 lanes 34 us
+//   1 of 8192, 4096 channels: 857 us with 4 lanes, 446 us with 16, 267 us in
+//   segments of 256 (279 us of 128, 285 us of 512)
+//   8 of 1 to 1600, 5120 channels: 187 us with 4 lanes, the longest first (274 us
+//   in the order given), 223 us with 16, 207 us in segments of 256
+// The longest sequence is not known here: 2.5 times the mean stands for it.
+struct ScanPlan {
+    int lanes, seg;
+};
+static ScanPlan scan_plan(const ScanDims &d)
+{
+    ScanPlan best{4, 0};
+    if (d.S <= 0) return best;
+    const double T = d.T, waves = (double)d.C * d.N / 16 / 16;
+    const double longest = d.S == 1 ? T : fmin(T, 2.5 * T / d.S), share = T * waves / 1024;
+    double least = fmax(longest * 280, share * 175);
+    const double e16 = fmax(longest * 117, share * 4 * 90);
+    if (e16 < least) {
+        least = e16;
+        best = ScanPlan{16, 0};
+    }
+    for (int seg = 128; seg <= 512; seg *= 2) {
+        const double e = fmax(2.0 * seg * 280, share * 325) + 12000 + longest / seg * 250 + seg * 50.0;
+        if (longest > seg && e < least) {
+            least = e;
+            best = ScanPlan{4, seg};
+        }
+    }
+    return best;
+}
+static int64_t scan_segments(const ScanDims &d, const ScanPlan &p)
+{
+    return p.seg ? (int64_t)d.T / p.seg + d.S : 0;
+}
+
+size_t scan_workspace(const ScanDims &d)
+{
+    return (size_t)scan_segments(d, scan_plan(d)) * d.C * (d.N + 1) * sizeof(float);
+}
+
+template <typename TX, typename TS, int N, int L>
+static void launch_scan_l(const ScanDims &d, const ScanArgs &a, int seg, void *workspace,
+                          hipStream_t st)
+{
+    const int per = d.C / d.G, chb = d.G * ((per + 256 / L - 1) / (256 / L));
+    ScanSegs sg{0x7fffffff, 0, nullptr, nullptr};
+    const int64_t n = seg ? (int64_t)d.T / seg + d.S : d.S;
+    if (seg) {
+        sg.seg = seg;
+        sg.cur = 1;
+        sg.fin = static_cast<float *>(workspace);
+        sg.sum = sg.fin + n * d.C * d.N;
+    }
+    for (; sg.cur <= 2; ++sg.cur) {
+        hipLaunchKernelGGL((scan_kernel<TX, TS, N, L>), dim3((unsigned)(n * chb)), dim3(256), 0, st,
+                           d.T, d.S, d.C, d.G, d.num_slots, chb, a, d.xs, d.dts, d.zs, d.bs, d.cs,
+                           d.ys, d.tf, sg);
+        if (!seg) break;
+    }
+}
 
 template <typename TX, typename TS, int N>
-static void launch_scan_n(const ScanDims &d, const ScanArgs &a, hipStream_t st)
+static void launch_scan_n(const ScanDims &d, const ScanArgs &a, void *workspace, hipStream_t st)
 {
-    constexpr int L = 4;
-    const int per = d.C / d.G, chb = d.G * ((per + 256 / L - 1) / (256 / L));
-    hipLaunchKernelGGL((scan_kernel<TX, TS, N, L>), dim3((unsigned)((int64_t)chb * d.S)), dim3(256),
-                       0, st, d.T, d.S, d.C, d.G, d.num_slots, chb, a, d.xs, d.dts, d.zs, d.bs,
-                       d.cs, d.ys, d.tf);
+    const ScanPlan p = scan_plan(d);
+    if (p.lanes == 16) launch_scan_l<TX, TS, N, 16>(d, a, p.seg, workspace, st);
+    else launch_scan_l<TX, TS, N, 4>(d, a, p.seg, workspace, st);
 }
 
 // Verify-step form: L = 4 lanes per channel, N / 4 states each; a block takes 64
@@ -330,11 +507,11 @@ static void launch_update_n(const ScanDims &d, const ScanArgs &a, void *inter, h
         }                                                                \
     } while (0)
 
-void launch_scan(const ScanDims &d, const ScanArgs &a, void *, void *stream)
+void launch_scan(const ScanDims &d, const ScanArgs &a, void *workspace, void *stream)
 {
     if (d.S <= 0) return;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-    SSD_BY_TYPE(launch_scan_n, st);
+    SSD_BY_TYPE(launch_scan_n, workspace, st);
 }
 
 void launch_scan_update(const ScanDims &d, const ScanArgs &a, void *inter, void *stream)

@@ -113,6 +113,14 @@ def test_long_prompts(lens, C, ti, ts):
     run(make(13, lens, C, 16, 1, ti, ts), lens)
 
 
+@pytest.mark.parametrize("N,G", [(16, 1), (32, 2), (64, 1)])
+@pytest.mark.parametrize("ti,ts", [(F32, F32), (BF, BF)])
+def test_many_channels_and_sequences(N, G, ti, ts):
+    # enough to fill the chip without segments, and with few lanes a channel
+    lens = [3 + (7 * i) % 11 for i in range(40)] + [37]
+    run(make(19, lens, 900, N, G, ti, ts), lens)
+
+
 def test_many_sequences():
     lens = [(5 * i) % 9 for i in range(150)]
     run(make(14, lens, 20, 16, 1, BF, F32), lens)
