@@ -31,12 +31,20 @@ struct AttnBlock {
     int seq, q0, lq, qrow, head, kvh, krow, lk, off;
 };
 // Heads run fastest over the blocks, the key head innermost, so that the 8
-// XCDs, which take blocks in turn, each see few key heads. Within a sequence
-// the last tile, which sees the most keys, comes first.
+// XCDs, which take blocks in turn, each see few key heads. The sequences with
+// the most keys come first (up to 64 of them), and within a sequence the last
+// tile, which sees the most.
 __device__ __forceinline__ AttnBlock attn_block(const AttnArgs &a, int BM) {
     AttnBlock r;
     const int hh = (int)(blockIdx.x % (unsigned)a.H), b = (int)(blockIdx.x / (unsigned)a.H);
-    const SeqTile t = find_tile(a.cuq, a.S, a.Tq, BM, 0, b);
+    SeqTile t;
+    if (a.S > 1 && a.S <= kWave) {
+        LaneSeqs l = lane_seqs(a.cuq, a.S, a.Tq, BM, 0);
+        const int s = threadIdx.x & (kWave - 1);
+        if (s < a.S) l.weight = a.cuk[s + 1] - a.cuk[s];
+        t = heaviest_first(l, a.S, BM, b);
+    } else
+        t = find_tile(a.cuq, a.S, a.Tq, BM, 0, b);
     r.seq = t.seq;
     if (t.seq < 0) return r;
     r.kvh = hh % a.Hkv;
@@ -86,8 +94,7 @@ __device__ __forceinline__ bool take_out(u32x4 &w, float) {
 }
 
 // bf16 heads of D. A block of 4 waves takes BM = 128 queries of one head, 32 a
-// wave, against tiles of 64 keys in LDS (two buffers: the next tile's rows are
-// in flight in registers while one is worked on; one barrier a tile).
+// wave, against tiles of 64 keys in LDS, worked on in two steps of 32 keys.
 //
 // Scores are formed transposed, S^T = K Q^T (keys x queries), so that a lane
 // holds 16 of every 32 scores of one query (its partner 32 lanes away the
@@ -96,15 +103,31 @@ __device__ __forceinline__ bool take_out(u32x4 &w, float) {
 // transposed operand comes through the LDS transpose read. Row pitches keep
 // both kinds of reads free of bank conflicts (K: 4 dwords past a multiple of
 // 64 dwords; V: 16 past).
+//
+// The matrix and the vector work of a step are about equally long (D = 128: 512
+// cycles of MFMA, 360 of exponentials, maxima and sums), and a wave that takes
+// one after the other leaves each unit idle half the time. So a step forms the
+// scores of the step after it, adds the values of the step before it, and does
+// the softmax of its own: three pieces that do not depend on one another and
+// are issued interleaved. Keys are therefore needed a step early and values a
+// step late; with two buffers of each, one barrier a tile, between its steps,
+// lets K of the next tile and V of this one be written before it and used
+// after it.
+template <int D> struct AttnSmem {
+    static constexpr int BN = 64, KP = D + 8, VP = D + 32;
+    __align__(16) bf16 k[2][BN * KP];
+    __align__(16) bf16 v[2][BN * VP];
+    int hidden;                      // a partly masked tile has non-finite values
+};
+
 template <int D>
 __global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a)
 {
-    constexpr int BM = 128, BN = 64, KP = D + 8, VP = D + 32;
+    typedef AttnSmem<D> SM;
+    constexpr int BM = 128, BN = SM::BN, KP = SM::KP, VP = SM::VP;
     constexpr int VEC = BN * D / 8 / 256;       // 16-byte vectors a thread stages of K, and of V
     constexpr int RPT = D / 8;                  // threads a row
-    __shared__ __align__(16) bf16 kt[2][BN * KP];
-    __shared__ __align__(16) bf16 vt[2][BN * VP];
-    __shared__ int hidden[2];                   // a partly masked tile has non-finite values
+    __shared__ SM sm;
     const AttnBlock b = attn_block(a, BM);
     if (b.seq < 0) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, qi = lane & 31, hf = lane >> 5;
@@ -119,38 +142,35 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a)
     const int qlast = b.q0 + BM - 1 < b.lq - 1 ? b.q0 + BM - 1 : b.lq - 1;
     const int kend = keys_seen(b, qlast);                      // keys the block needs
     const int kfull = keys_seen(b, b.q0);                      // keys that all its queries see
-    const int wlast = b.q0 + wave * 32 + 31 < qlast ? b.q0 + wave * 32 + 31 : qlast;
-    const int wend = b.q0 + wave * 32 < b.lq ? keys_seen(b, wlast) : 0;   // keys the wave needs
-    const int wfull = b.q0 + wave * 32 + 31 < b.lq ? keys_seen(b, b.q0 + wave * 32) : 0;
 
     const bf16 *const K = static_cast<const bf16 *>(a.k) + (int64_t)b.krow * a.ks + (int64_t)b.kvh * D;
     const bf16 *const V = static_cast<const bf16 *>(a.v) + (int64_t)b.krow * a.vs + (int64_t)b.kvh * D;
     u32x4 kr[VEC], vr[VEC];
-    // rows past the sequence's end come back as zeros
-    auto request = [&](int j0) {
+    // a tile's rows from key j0 on; rows past the sequence's end come back as zeros
+    auto request = [&](u32x4 (&r)[VEC], const bf16 *base, int stride, int j0) __attribute__((always_inline)) {
         const int rows = b.lk - j0 < BN ? b.lk - j0 : BN;
-        const rsrc_t rk = make_rsrc(K + (int64_t)j0 * a.ks, (uint32_t)((rows - 1) * (int)a.ks + D) * 2);
-        const rsrc_t rv = make_rsrc(V + (int64_t)j0 * a.vs, (uint32_t)((rows - 1) * (int)a.vs + D) * 2);
+        const rsrc_t rs = make_rsrc(base + (int64_t)j0 * stride,
+                                    rows > 0 ? (uint32_t)((rows - 1) * stride + D) * 2 : 0u);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const int row = (tid + 256 * i) / RPT, c = tid % RPT;
-            kr[i] = __builtin_bit_cast(u32x4, buf_ld16(rk, (uint32_t)(row * (int)a.ks + 8 * c) * 2));
-            vr[i] = __builtin_bit_cast(u32x4, buf_ld16(rv, (uint32_t)(row * (int)a.vs + 8 * c) * 2));
-        }
+        for (int i = 0; i < VEC; ++i)
+            r[i] = __builtin_bit_cast(u32x4, buf_ld16(rs, (uint32_t)((tid + 256 * i) / RPT * stride +
+                                                                     8 * (tid % RPT)) * 2));
     };
-    auto stage = [&](int j0, int buf) {
-        if (j0 + BN > kfull) {
+    auto stage_k = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            *reinterpret_cast<u32x4 *>(&sm.k[t & 1][(tid + 256 * i) / RPT * KP + 8 * (tid % RPT)]) = kr[i];
+    };
+    auto stage_v = [&](int t) __attribute__((always_inline)) {
+        if ((t + 1) * BN > kfull) {
             bool any = false;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) any |= take_out(vr[i], bf16());
-            if (any) hidden[buf] = 1;
+            if (any) sm.hidden = 1;
         }
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const int row = (tid + 256 * i) / RPT, c = tid % RPT;
-            *reinterpret_cast<u32x4 *>(&kt[buf][row * KP + 8 * c]) = kr[i];
-            *reinterpret_cast<u32x4 *>(&vt[buf][row * VP + 8 * c]) = vr[i];
-        }
+        for (int i = 0; i < VEC; ++i)
+            *reinterpret_cast<u32x4 *>(&sm.v[t & 1][(tid + 256 * i) / RPT * VP + 8 * (tid % RPT)]) = vr[i];
     };
 
     f32x16 o[D / 32];
@@ -159,96 +179,128 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a)
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
     float m = -__builtin_inff(), sum = 0.0f;
-    if (tid < 2) hidden[tid] = 0;
-    __syncthreads();
-    if (kend > 0) {
-        request(0);
-        stage(0, 0);
+
+    // scores of 32 keys: element e is key 8 (e / 4) + 4 hf + e % 4 of them
+    auto scores = [&](int buf, int sub) __attribute__((always_inline)) {
+        f32x16 s;
+        const bf16 *const kl = &sm.k[buf][(sub * 32 + qi) * KP + hf * 8];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = 0.0f;
+#pragma unroll
+        for (int st = 0; st < D / 16; ++st)
+            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                *reinterpret_cast<const bf16x8 *>(kl + 16 * st), qf[st], s, 0, 0, 0);
+        return s;
+    };
+    // adds 32 keys' values: the operand of dims 32 i .. and keys 16 w .., of which the
+    // lanes of a half hold the keys 4 hf + v and 8 + 4 hf + v that their weights belong to
+    const int jl = lane & 15;
+    const int vo = (4 * hf + (jl >> 2)) * VP + ((lane >> 4) & 1) * 16 + 4 * (jl & 3);
+    auto add_values = [&](int buf, int sub, const bf16x8 (&p)[2]) __attribute__((always_inline)) {
+        const bf16 *const vl = &sm.v[buf][sub * 32 * VP + vo];
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const v4i16 lo = lds_read_tr16(vl + 16 * w * VP + 32 * i);
+                const v4i16 hi = lds_read_tr16(vl + (16 * w + 8) * VP + 32 * i);
+                typedef short v8i16 __attribute__((ext_vector_type(8)));
+                const v8i16 both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, both), p[w],
+                                                               o[i], 0, 0, 0);
+            }
+    };
+    // softmax weights of the 32 keys from key j on; returns what the result so far has
+    // to be scaled by, and whether any lane's maximum rose
+    auto weights = [&](f32x16 &s, int j, bool masked, bf16x8 (&p)[2], bool &rose) __attribute__((always_inline)) {
+        if (masked) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (j + 8 * (e >> 2) + 4 * hf + (e & 3) >= seen) s[e] = -__builtin_inff();
+        }
+        float top = s[0];
+#pragma unroll
+        for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e]);
+        top = across32(top, larger) * a.scale2;
+        const float was = m;
+        m = fmaxf(m, top);
+        // (a row that has seen nothing yet: subtract 0, its terms are exp2(-inf))
+        const float ref = m == -__builtin_inff() ? 0.0f : m;
+        const float f = __builtin_amdgcn_exp2f(was - ref);
+        sum *= f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float w = __builtin_amdgcn_exp2f(s[e] * a.scale2 - ref);
+            sum += w;
+            p[e >> 3][e & 7] = static_cast<bf16>(w);
+        }
+        rose = top > was;
+        return f;
+    };
+    // (the empty statements keep the weights in front of the branch, where the matrix
+    // products they run beside are, and the products with f behind it)
+    auto rescale = [&](float f, bool rose, bf16x8 (&p)[2]) __attribute__((always_inline)) {
+        asm volatile("" : "+v"(p[0]), "+v"(p[1]), "+v"(sum));
+        if (__any(rose)) {
+            asm volatile("" : "+v"(f));
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) o[i] *= f;
+        }
+    };
+    const int tiles = (kend + BN - 1) / BN;
+    f32x16 s0, s1;
+    bf16x8 p0[2], p1[2];
+    if (tid == 0) sm.hidden = 0;
+    // (the values "before the first tile": zeros with zero weights)
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p1[w][e] = static_cast<bf16>(0.0f);
+    for (int i = tid; i < BN * VP / 8; i += 256) reinterpret_cast<u32x4 *>(sm.v[1])[i] = u32x4{0, 0, 0, 0};
+    if (tiles > 0) {
+        request(kr, K, (int)a.ks, 0);
+        stage_k(0);
+        request(kr, K, (int)a.ks, BN);
+        request(vr, V, (int)a.vs, 0);
     }
     __syncthreads();
-    int buf = 0;
-    for (int j0 = 0; j0 < kend; j0 += BN, buf ^= 1) {
-        const bool more = j0 + BN < kend;
-        if (more) request(j0 + BN);
-        if (j0 < wend) {
-            f32x16 s[2];
-            const bf16 *const kl = &kt[buf][qi * KP + hf * 8];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) s[h][e] = 0.0f;
-#pragma unroll
-                for (int st = 0; st < D / 16; ++st)
-                    s[h] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                        *reinterpret_cast<const bf16x8 *>(kl + h * 32 * KP + 16 * st), qf[st], s[h],
-                        0, 0, 0);
-            }
-            // element e of half h: key j0 + 32 h + 8 (e / 4) + 4 hf + e % 4
-            if (j0 + BN > wfull) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (j0 + 32 * h + 8 * (e >> 2) + 4 * hf + (e & 3) >= seen)
-                            s[h][e] = -__builtin_inff();
-            }
-            float top = s[0][0];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) top = fmaxf(top, s[h][e]);
-            top = across32(top, larger) * a.scale2;
-            if (__any(top > m)) {
-                const float was = m;
-                m = fmaxf(m, top);
-                const float f = m == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(was - m);
-                sum *= f;
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[i][e] *= f;
-            }
-            // (a row that has seen nothing yet: subtract 0, its terms are exp2(-inf))
-            const float ref = m == -__builtin_inff() ? 0.0f : m;
-            bf16x8 pf[4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float p = __builtin_amdgcn_exp2f(s[h][e] * a.scale2 - ref);
-                    sum += p;
-                    pf[2 * h + (e >> 3)][e & 7] = static_cast<bf16>(p);
-                }
-            // operand of dims 32 i .. and keys 16 w ..: lanes of a half hold the keys
-            // 4 hf + v and 8 + 4 hf + v that their probabilities belong to
-            const int jl = lane & 15;
-            const bf16 *const vl = &vt[buf][(4 * hf + (jl >> 2)) * VP + ((lane >> 4) & 1) * 16 + 4 * (jl & 3)];
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const v4i16 lo = lds_read_tr16(vl + 16 * w * VP + 32 * i);
-                    const v4i16 hi = lds_read_tr16(vl + (16 * w + 8) * VP + 32 * i);
-                    typedef short v8i16 __attribute__((ext_vector_type(8)));
-                    const v8i16 both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, both),
-                                                                   pf[w], o[i], 0, 0, 0);
-                }
-            if (j0 + BN > kfull && hidden[buf]) {
-                for (int j = j0; j < j0 + BN && j < b.lk; ++j)
-                    if (j < seen)
-#pragma unroll
-                        for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const float v = to_f32(V[(int64_t)j * a.vs + 32 * i + 8 * (e >> 2) +
-                                                         4 * hf + (e & 3)]);
-                                if (!(fabsf(v) < __builtin_inff())) o[i][e] += v;
-                            }
-            }
-        }
-        if (more) stage(j0 + BN, buf ^ 1);
+    if (tiles > 0) s0 = scores(0, 0);
+    auto tile = [&](int t, auto with_mask) __attribute__((always_inline)) {
+        constexpr bool masked = decltype(with_mask)::value;
+        const int j = t * BN, buf = t & 1;
+        bool rose;
+        s1 = scores(buf, 1);
+        add_values(buf ^ 1, 1, p1);
+        float f = weights(s0, j, masked, p0, rose);
+        rescale(f, rose, p0);
+        stage_k(t + 1);
+        stage_v(t);
         __syncthreads();
+        request(kr, K, (int)a.ks, j + 2 * BN);
+        request(vr, V, (int)a.vs, j + BN);
+        s0 = scores(buf ^ 1, 0);
+        add_values(buf, 0, p0);
+        f = weights(s1, j + 32, masked, p1, rose);
+        rescale(f, rose, p1);
+    };
+    const int open = kfull / BN < tiles ? kfull / BN : tiles;     // tiles without a mask
+    for (int t = 0; t < open; ++t) tile(t, std::false_type());
+    for (int t = open; t < tiles; ++t) tile(t, std::true_type());
+    if (tiles > 0) {
+        const int t = tiles - 1;
+        add_values(t & 1, 1, p1);
+        // the values taken out, for the queries that see them
+        if (sm.hidden)
+            for (int k = open * BN; k < kend; ++k)
+                if (k < seen)
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float v = to_f32(V[(int64_t)k * a.vs + 32 * i + 8 * (e >> 2) +
+                                                     4 * hf + (e & 3)]);
+                            if (!(fabsf(v) < __builtin_inff())) o[i][e] += v;
+                        }
     }
 
     sum = across32(sum, added);
@@ -300,6 +352,8 @@ __global__ __launch_bounds__(256) void attn_f32_kernel(AttnArgs a)
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) o[i] = zero4();
     float m = -__builtin_inff(), sum = 0.0f;
+    if (tid == 0) hidden = 0;
+    __syncthreads();
     for (int j0 = 0; j0 < kend; j0 += BN) {
         const int rows = b.lk - j0 < BN ? b.lk - j0 : BN;
         const rsrc_t rk = make_rsrc(K + (int64_t)j0 * a.ks, (uint32_t)((rows - 1) * (int)a.ks + D) * 4);
@@ -312,8 +366,6 @@ __global__ __launch_bounds__(256) void attn_f32_kernel(AttnArgs a)
             vr[i] = __builtin_bit_cast(u32x4, buf_ld16(rv, (uint32_t)(row * (int)a.vs + 4 * c) * 4));
         }
         __syncthreads();                       // the last tile's reads are done
-        if (tid == 0) hidden = 0;
-        __syncthreads();
         if (j0 + BN > kfull) {
             bool any = false;
 #pragma unroll
@@ -358,18 +410,17 @@ __global__ __launch_bounds__(256) void attn_f32_kernel(AttnArgs a)
                 for (int i = 0; i < D / 16; ++i)
                     o[i] = Mma<float>::run(vt[(16 * h + 4 * g + e) * P + 16 * i + qi], p, o[i]);
             }
-        if (j0 + BN > kfull && hidden) {
-            for (int j = j0; j < j0 + BN && j < b.lk; ++j)
-                if (j < seen)
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float v = V[(int64_t)j * a.vs + 16 * i + 4 * g + e];
-                            if (!(fabsf(v) < __builtin_inff())) o[i][e] += v;
-                        }
-        }
     }
+    if (hidden)                                // the values taken out, for the queries that see them
+        for (int j = kfull / BN * BN; j < kend; ++j)
+            if (j < seen)
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float v = V[(int64_t)j * a.vs + 16 * i + 4 * g + e];
+                        if (!(fabsf(v) < __builtin_inff())) o[i][e] += v;
+                    }
     sum = across32(across16(sum, added), added);
     if (q < b.lq) {
         const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;

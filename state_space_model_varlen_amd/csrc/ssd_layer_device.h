@@ -113,29 +113,39 @@ __device__ __forceinline__ SeqTile find_tile(const int32_t *__restrict__ cu, int
     return SeqTile{-1, 0, 0, 0};
 }
 
-// The b-th longest of up to 64 sequences, whole (of equal ones the first): blocks
-// are started in order, so the longest chains start first. Every lane of the
-// wave takes part: a lane's sequence counts those in front of it.
-__device__ __forceinline__ SeqTile longest_first(const int32_t *__restrict__ cu, int S, int total,
-                                                 int b) {
+// A lane's sequence of up to 64: its rows, its tiles and what orders it.
+struct LaneSeqs {
+    int start, len, tiles, weight;
+};
+__device__ __forceinline__ LaneSeqs lane_seqs(const int32_t *__restrict__ cu, int S, int total,
+                                              int tile, int of_empty) {
     const int s = threadIdx.x & (kWave - 1);
-    int a = 0, len = -1;
+    LaneSeqs r{0, 0, 0, -1};
     if (s < S) {
-        a = cu[s];
-        const int e = cu[s + 1];
-        a = a < 0 ? 0 : (a > total ? total : a);
+        const int a = cu[s], e = cu[s + 1];
+        r.start = a < 0 ? 0 : (a > total ? total : a);
         const int ec = e < 0 ? 0 : (e > total ? total : e);
-        len = ec > a ? ec - a : 0;
+        r.len = ec > r.start ? ec - r.start : 0;
+        r.tiles = r.len > 0 ? (r.len - 1) / tile + 1 : of_empty;
+        r.weight = r.len;
     }
-    int rank = 0;
+    return r;
+}
+// Tile b of them when the sequences are taken by falling weight (of equal ones
+// the first): blocks start in order, so the longest work starts first and the
+// short ends fill the gaps. Every lane of the wave takes part.
+__device__ __forceinline__ SeqTile heaviest_first(const LaneSeqs &r, int S, int tile, int b) {
+    const int s = threadIdx.x & (kWave - 1);
+    int before = 0;
     for (int j = 0; j < S; ++j) {
-        const int o = __builtin_amdgcn_readlane(len, j);
-        rank += o > len || (o == len && j < s) ? 1 : 0;
+        const int w = __builtin_amdgcn_readlane(r.weight, j), n = __builtin_amdgcn_readlane(r.tiles, j);
+        before += w > r.weight || (w == r.weight && j < s) ? n : 0;
     }
-    const uint64_t mine = __ballot(s < S && rank == b);
+    const uint64_t mine = __ballot(b >= before && b < before + r.tiles);
     if (!mine) return SeqTile{-1, 0, 0, 0};
     const int src = __ffsll((unsigned long long)mine) - 1;
-    return SeqTile{src, __builtin_amdgcn_readlane(a, src), __builtin_amdgcn_readlane(len, src), 0};
+    return SeqTile{src, __builtin_amdgcn_readlane(r.start, src), __builtin_amdgcn_readlane(r.len, src),
+                   (b - __builtin_amdgcn_readlane(before, src)) * tile};
 }
 
 // The same for a batch whose sequences all have `len` tokens.

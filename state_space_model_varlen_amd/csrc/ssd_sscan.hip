@@ -154,8 +154,9 @@ __global__ __launch_bounds__(256) void scan_kernel(
     unsigned id = blockIdx.x;
     if (L == 16 && (id | 31u) < gridDim.x) id = (id & ~31u) | (id & 7u) << 2 | (id >> 3 & 3u);
     const int b = (int)(id / (unsigned)chb), cb = (int)(id % (unsigned)chb);
-    const SeqTile tile = sg.cur == 0 && S > 1 && S <= kWave ? longest_first(a.cu, S, T, b)
-                                                           : find_tile(a.cu, S, T, sg.seg, 1, b);
+    const SeqTile tile = sg.cur == 0 && S > 1 && S <= kWave
+                             ? heaviest_first(lane_seqs(a.cu, S, T, sg.seg, 1), S, sg.seg, b)
+                             : find_tile(a.cu, S, T, sg.seg, 1, b);
     if (tile.seq < 0) return;
     const bool first = tile.t0 == 0, last = tile.t0 >= tile.len - sg.seg;
     if (sg.cur == 1 ? !first && last : sg.cur == 2 && first) return;
