@@ -39,7 +39,7 @@ __device__ __forceinline__ u32x2 codes8(const float *v) {
 // bytes.
 template <typename T, bool E4M3, int D>
 __global__ __launch_bounds__(256) void kv_store_kernel(
-    int rows, int Hkv, int page, int64_t positions, const T *__restrict__ k,
+    int rows, int Hkv, int log_page, int64_t positions, const T *__restrict__ k,
     const T *__restrict__ v, int64_t ks, int64_t vs, const int64_t *__restrict__ slots, KvCache c)
 {
     constexpr int LPR = D / 8;
@@ -53,7 +53,7 @@ __global__ __launch_bounds__(256) void kv_store_kernel(
     RawV<T, 8> raw;
     raw.load((is_v ? v + (int64_t)t * vs : k + (int64_t)t * ks) + (int64_t)h * D + d0);
     raw.get(f);
-    const int64_t to = (pos / page * Hkv + h) * page + pos % page;
+    const int64_t to = (((pos >> log_page) * Hkv + h) << log_page) + (pos & ((1 << log_page) - 1));
     if constexpr (E4M3) {
         float top = 0.0f;
 #pragma unroll
@@ -104,7 +104,7 @@ template <bool E4M3> __device__ __forceinline__ void cache16(const void *cache, 
 constexpr int kLoadTile = 16;
 template <typename T, bool E4M3, int D>
 __global__ __launch_bounds__(256) void kv_load_kernel(
-    int T_, int S, int max_pages, int pages, int page, int Hkv, const int32_t *__restrict__ cu,
+    int T_, int S, int max_pages, int pages, int log_page, int Hkv, const int32_t *__restrict__ cu,
     const int32_t *__restrict__ table, KvCache c, T *__restrict__ k, T *__restrict__ v, int64_t ks,
     int64_t vs)
 {
@@ -115,11 +115,11 @@ __global__ __launch_bounds__(256) void kv_load_kernel(
     const int chunks = Hkv * (D / 16);
     for (int e = (int)threadIdx.x; e < n * chunks; e += 256) {
         const int j = e / chunks, o = (e - j * chunks) * 16, h = o / D, pos = t.t0 + j;
-        const int pi = pos / page;
+        const int pi = pos >> log_page;
         const int pg = pi < max_pages ? table[(int64_t)t.seq * max_pages + pi] : -1;
         float f[16] = {};
         if (pg >= 0 && pg < pages) {
-            const int64_t row = ((int64_t)pg * Hkv + h) * page + pos % page;
+            const int64_t row = (((int64_t)pg * Hkv + h) << log_page) + (pos & ((1 << log_page) - 1));
             const float sc = E4M3 ? pow2_of_byte((is_v ? c.vsc : c.ksc)[row]) : 1.0f;
             cache16<E4M3>(is_v ? c.v : c.k, row * D + o % D, sc, f);
         }
@@ -135,7 +135,7 @@ static void store_t(const KvDims &d, int n, const void *k, const void *v, const 
     const int64_t rows = (int64_t)n * d.Hkv;
     const int per = 256 / (D / 8);
     hipLaunchKernelGGL((kv_store_kernel<T, E4M3, D>), dim3((unsigned)((rows + per - 1) / per), 2),
-                       dim3(256), 0, st, (int)rows, d.Hkv, d.page, (int64_t)d.pages * d.page,
+                       dim3(256), 0, st, (int)rows, d.Hkv, __builtin_ctz(d.page), (int64_t)d.pages * d.page,
                        static_cast<const T *>(k), static_cast<const T *>(v), d.ks, d.vs, slots, c);
 }
 template <typename T, bool E4M3, int D>
@@ -143,7 +143,7 @@ static void load_t(const KvDims &d, int n, int S, int max_pages, const int32_t *
                    const int32_t *table, const KvCache &c, void *k, void *v, hipStream_t st)
 {
     hipLaunchKernelGGL((kv_load_kernel<T, E4M3, D>), dim3((unsigned)(n / kLoadTile + S), 2),
-                       dim3(256), 0, st, n, S, max_pages, d.pages, d.page, d.Hkv, cu, table, c,
+                       dim3(256), 0, st, n, S, max_pages, d.pages, __builtin_ctz(d.page), d.Hkv, cu, table, c,
                        static_cast<T *>(k), static_cast<T *>(v), d.ks, d.vs);
 }
 
@@ -252,8 +252,8 @@ struct DecodePart {
 };
 
 template <bool E4M3, int D, int NRT>
-__global__ __launch_bounds__(256) void decode_attn_kernel(
-    int T, int H, int Hkv, int pages, int page, int max_pages, float scale2,
+__global__ __launch_bounds__(256, 2) void decode_attn_kernel(
+    int T, int H, int Hkv, int pages, int log_page, int max_pages, float scale2,
     const bf16 *__restrict__ q, int64_t qs, KvCache c, const int32_t *__restrict__ table,
     const int32_t *__restrict__ lens, bf16 *__restrict__ out, int64_t os, float *__restrict__ lse,
     DecodePart part)
@@ -264,12 +264,12 @@ __global__ __launch_bounds__(256) void decode_attn_kernel(
     static_assert(16 * OP * 4 <= 32 * VP * 2, "a row tile's result fits the value tile");
     __shared__ __align__(16) bf16 vt[4][32 * VP];
     __shared__ float ml[4][2][NRT * 16];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n16 = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = scalar(tid >> 6), n16 = lane & 15, g = lane >> 4;
     const int split = (int)blockIdx.x % part.splits, r0 = (int)blockIdx.x / part.splits * NRT * 16;
     const int kvh = blockIdx.y, r = blockIdx.z;
     const int group = H / Hkv, rows = T * group;
-    int L = lens[r];
-    const int most = max_pages * page;
+    int L = scalar(lens[r]);
+    const int most = max_pages << log_page;
     L = L < 0 ? 0 : (L > most ? most : L);
     const int k0 = split * part.span;
     const int k1 = L - k0 < part.span ? L : k0 + part.span;
@@ -294,29 +294,35 @@ __global__ __launch_bounds__(256) void decode_attn_kernel(
     // the first row in the cache of 16 keys from `key` on (a multiple of 16), or -1
     auto base_of = [&](int key) -> int64_t {
         if (key >= k1) return -1;
-        const int pg = tab[key / page];
-        return pg >= 0 && pg < pages ? ((int64_t)pg * Hkv + kvh) * page + key % page : -1;
+        const int pg = scalar(tab[key >> log_page]);
+        return pg >= 0 && pg < pages
+                   ? (((int64_t)pg * Hkv + kvh) << log_page) + (key & ((1 << log_page) - 1)) : -1;
     };
     auto request = [&](TL &t, int key, int64_t b0, int64_t b1) {
+        // (scalar bases, one offset a lane; a load of the values stays in one half)
         const int64_t base[2] = {b0 < 0 ? 0 : b0, b1 < 0 ? 0 : b1};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const char *const p = kc + (base[i] + n16) * (D * TL::EB) + g * 16;
+            const char *const p = kc + base[i] * (D * TL::EB);
 #pragma unroll
-            for (int l = 0; l < TL::KL; ++l) t.k[i][l] = *reinterpret_cast<const u32x4 *>(p + 64 * l);
-            if (E4M3) t.ksc[i] = c.ksc[base[i] + n16];
+            for (int l = 0; l < TL::KL; ++l)
+                t.k[i][l] = *reinterpret_cast<const u32x4 *>(p + (n16 * (D * TL::EB) + g * 16 + 64 * l));
+            if (E4M3) t.ksc[i] = (c.ksc + base[i])[n16];
         }
+        constexpr int RV = 64 / TL::LPV;          // value rows a load covers: 4, 8 or 16
 #pragma unroll
         for (int l = 0; l < TL::VL; ++l) {
-            const int vr = l * (64 / TL::LPV) + lane / TL::LPV;
-            const int64_t row = base[vr >> 4] + (vr & 15);
-            t.v[l] = *reinterpret_cast<const u32x4 *>(vc + row * (D * TL::EB) + lane % TL::LPV * 16);
-            if (E4M3) t.vsc[l] = c.vsc[row];
+            const int64_t half = base[l * RV / 16];
+            const int vr = l * RV % 16 + lane / TL::LPV;
+            t.v[l] = *reinterpret_cast<const u32x4 *>(
+                vc + half * (D * TL::EB) + (vr * (D * TL::EB) + lane % TL::LPV * 16));
+            if (E4M3) t.vsc[l] = (c.vsc + half)[vr];
         }
     };
 
     f32x4 o[NRT][DT];
     float mx[NRT], sum[NRT];
+    bool odd = false;                          // values were taken out
 #pragma unroll
     for (int m = 0; m < NRT; ++m) {
         mx[m] = -__builtin_inff();
@@ -356,11 +362,10 @@ __global__ __launch_bounds__(256) void decode_attn_kernel(
         // zero but zero times an infinity is not: non-finite values stay out of the
         // product and are added below to the rows that see them.
         const bool partial = key + 32 > L - T + 1;
-        bool odd = false;
 #pragma unroll
         for (int l = 0; l < TL::VL; ++l) {
             const int vr = l * (64 / TL::LPV) + lane / TL::LPV;
-            const bool in = key + vr < k1 && (vr < 16 ? b0 : b1) >= 0;
+            const bool in = key + vr < k1 && (l * (64 / TL::LPV) < 16 ? b0 : b1) >= 0;
             const uint32_t keep = in ? 0xffffffffu : 0u;
             u32x4 w = cur.v[l] & keep;
             if (partial) odd |= take_out<E4M3>(w);
@@ -408,32 +413,36 @@ __global__ __launch_bounds__(256) void decode_attn_kernel(
 #pragma unroll
             for (int m = 0; m < NRT; ++m) o[m][i] = Mma<bf16>::run(vf, pf[m], o[m][i]);
         }
-        if (partial && __any(odd)) {
-            for (int j = 0; j < 32 && key + j < k1; ++j) {
-                const int64_t b = j < 16 ? b0 : b1;
-                if (b < 0) continue;
-                const int64_t at = (b + (j & 15)) * D + 4 * g;
-#pragma unroll
-                for (int i = 0; i < DT; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float v;
-                        if constexpr (E4M3)
-                            v = (static_cast<const uint8_t *>(c.v)[at + 16 * i + e] & 0x7f) == 0x7f
-                                    ? __builtin_nanf("") : 0.0f;
-                        else
-                            v = to_f32(static_cast<const bf16 *>(c.v)[at + 16 * i + e]);
-                        if (!(fabsf(v) < __builtin_inff()))
-#pragma unroll
-                            for (int m = 0; m < NRT; ++m)
-                                if (key + j < sees[m]) o[m][i][e] += v;
-                    }
-            }
-        }
         wave_lds_sync();
         cur = next;
         b0 = n0;
         b1 = n1;
+    }
+
+    if (__any(odd)) {
+        // back to the rows that see them, from the wave that had their tile
+        for (int j = L - T + 1 > k0 ? L - T + 1 : k0; j < k1; ++j) {
+            if (((j - k0) >> 5 & 3) != wave) continue;
+            const int64_t b = base_of(j & ~15);
+            if (b < 0) continue;
+            const int64_t at = (b + (j & 15)) * D + 4 * g;
+            for (int i = 0; i < DT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float v;
+                    if constexpr (E4M3)
+                        v = (static_cast<const uint8_t *>(c.v)[at + 16 * i + e] & 0x7f) == 0x7f
+                                ? __builtin_nanf("") : 0.0f;
+                    else
+                        v = to_f32(static_cast<const bf16 *>(c.v)[at + 16 * i + e]);
+                    v = fabsf(v) < __builtin_inff() ? 0.0f : v;
+#pragma unroll
+                    for (int k = 0; k < DT; ++k)
+#pragma unroll
+                        for (int m = 0; m < NRT; ++m)
+                            if (k == i && j < sees[m]) o[m][k][e] += v;
+                }
+        }
     }
 
     // join the waves: common maximum, then the four results summed through LDS
@@ -503,66 +512,100 @@ __global__ __launch_bounds__(256) void decode_attn_kernel(
     }
 }
 
-// Joins the splits of a (token, head): one wave each, D / 64 elements a lane.
+// Joins the splits of a (token, head): one block, its threads in groups of D / 4
+// lanes that take the splits in turn, 4 elements a lane and the loads of 4
+// splits at once, and are summed through LDS. (One wave that walked 86 splits
+// took 28 us, this takes 5.)
 template <int D>
-__global__ __launch_bounds__(256) void decode_join_kernel(int64_t n, int T, int H, int most,
+__global__ __launch_bounds__(256) void decode_join_kernel(int T, int H, int most,
                                                           const int32_t *__restrict__ lens,
                                                           DecodePart part, bf16 *__restrict__ out,
                                                           int64_t os, float *__restrict__ lse)
 {
-    constexpr int PER = D / 64;
-    const int lane = threadIdx.x & 63;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= n) return;
-    const int64_t qr = row / H;
+    constexpr int LANES = D / 4, GRP = 256 / LANES;
+    __shared__ __align__(16) float acc_l[GRP][D];
+    __shared__ float red[2][4];
+    const int tid = threadIdx.x, grp = tid / LANES, d0 = tid % LANES * 4;
+    const int64_t row = blockIdx.x, qr = row / H;
     int L = lens[qr / T];
     L = L < 0 ? 0 : (L > most ? most : L);
     int ns = (L + part.span - 1) / part.span;
     ns = ns < 1 ? 1 : ns;
     const float *const ml = part.ml + row * part.splits * 2;
-    const float *const o = part.o + row * part.splits * D;
+    const float *const o = part.o + row * part.splits * D + d0;
     float top = -__builtin_inff();
-    for (int s = lane; s < ns; s += 64) top = fmaxf(top, ml[2 * s]);
+    for (int s = tid; s < ns; s += 256) top = fmaxf(top, ml[2 * s]);
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+    if ((tid & 63) == 0) red[0][tid >> 6] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
     const float ref = top == -__builtin_inff() ? 0.0f : top;
-    float all = 0.0f, acc[PER] = {};
-    for (int s = 0; s < ns; ++s) {
-        const float f = __builtin_amdgcn_exp2f(ml[2 * s] - ref);
-        all += f * ml[2 * s + 1];
+    float all = 0.0f;
+    for (int s = tid; s < ns; s += 256) all += __builtin_amdgcn_exp2f(ml[2 * s] - ref) * ml[2 * s + 1];
 #pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] += f * o[(int64_t)s * D + lane * PER + e];
+    for (int off = 32; off > 0; off >>= 1) all += __shfl_xor(all, off, 64);
+    if ((tid & 63) == 0) red[1][tid >> 6] = all;
+    f32x4 acc = zero4();
+    for (int s0 = grp; s0 < ns; s0 += 4 * GRP) {
+        f32x4 v[4];
+        float f[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int s = s0 + u * GRP < ns ? s0 + u * GRP : ns - 1;
+            v[u] = *reinterpret_cast<const f32x4 *>(o + (int64_t)s * D);
+            f[u] = ml[2 * s];
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (s0 + u * GRP < ns) acc += v[u] * __builtin_amdgcn_exp2f(f[u] - ref);
     }
+    *reinterpret_cast<f32x4 *>(&acc_l[grp][d0]) = acc;
+    __syncthreads();
+    all = red[1][0] + red[1][1] + red[1][2] + red[1][3];
     const float inv = all > 0.0f || all != all ? 1.0f / all : 0.0f;
     const int h = (int)(row - qr * H);
+    if (tid < D) {
+        float v = 0.0f;
 #pragma unroll
-    for (int e = 0; e < PER; ++e)
-        out[qr * os + (int64_t)h * D + lane * PER + e] = static_cast<bf16>(acc[e] * inv);
-    if (lse && lane == 0) lse[row] = (ref + __builtin_amdgcn_logf(all)) * kLn2;
+        for (int g = 0; g < GRP; ++g) v += acc_l[g][tid];
+        out[qr * os + (int64_t)h * D + tid] = static_cast<bf16>(v * inv);
+    }
+    if (lse && tid == 0) lse[row] = (ref + __builtin_amdgcn_logf(all)) * kLn2;
 }
 
-// Row tiles a block holds, and how the contexts are split: enough blocks to
-// fill the chip, spans of whole 128-key rounds.
+// Row tiles a block holds: all of a head group's rows where they fit in two.
 static int row_tiles(const DecodeAttnDims &d)
 {
-    const int rows = d.T * (d.H / d.kv.Hkv);
-    return rows <= 16 ? 1 : 2;
+    return d.T * (d.H / d.kv.Hkv) <= 16 ? 1 : 2;
 }
+// How the contexts are split over blocks. Splits cost their partial results
+// (twice, written and read) and the join's launch, so there are no more than
+// bring 1024 blocks, of at least 512 keys; but with few requests a block's
+// chain of key tiles is what takes time, and up to 512 blocks of at least 128
+// keys are made. (128 requests of 1 K to 4 K keys, 8 key heads, 8 bits: 173 us
+// unsplit, 199 us in two, 206 us in four. One request of 32769 keys in bf16: 35
+// us in 65 splits of 512, 41 us in 128 of 256.)
 static DecodePart plan(const DecodeAttnDims &d)
 {
     DecodePart p{nullptr, nullptr, 1, 128};
     const int64_t most = (int64_t)d.max_pages * d.kv.page;
-    const int nrt = row_tiles(d), rows = d.T * (d.H / d.kv.Hkv);
-    const int64_t blocks = (int64_t)d.R * d.kv.Hkv * ((rows + 16 * nrt - 1) / (16 * nrt));
-    int64_t splits = blocks > 0 ? 1024 / blocks : 1;
-    const int64_t longest = (most + 255) / 256;      // spans of at least 256 keys
-    splits = splits > longest ? longest : splits;
-    splits = splits < 1 ? 1 : splits;
-    int64_t span = ((most + splits - 1) / splits + 127) / 128 * 128;
-    if (span < 128) span = 128;
+    const int rows = d.T * (d.H / d.kv.Hkv), in_block = 16 * row_tiles(d);
+    const int64_t blocks = (int64_t)d.R * d.kv.Hkv * ((rows + in_block - 1) / in_block);
+    if (blocks <= 0 || most <= 128) {
+        p.span = most > 128 ? (int)((most + 127) / 128 * 128) : 128;
+        return p;
+    }
+    auto most_splits = [&](int64_t target, int64_t keys) {
+        const int64_t n = (most + keys - 1) / keys;
+        return target / blocks < n ? target / blocks : n;
+    };
+    int64_t splits = most_splits(1024, 512);
+    if (splits * blocks < 512) splits = most_splits(512, 128);
+    if (splits < 1) splits = 1;
+    const int64_t span = ((most + splits - 1) / splits + 127) / 128 * 128;
     p.span = (int)span;
     p.splits = (int)((most + span - 1) / span);
-    if (p.splits < 1) p.splits = 1;
     return p;
 }
 
@@ -580,14 +623,13 @@ static void decode_t(const DecodeAttnDims &d, const void *q, const KvCache &c, c
     const int rows = d.T * (d.H / d.kv.Hkv);
     const dim3 grid((unsigned)(p.splits * ((rows + 16 * NRT - 1) / (16 * NRT))), d.kv.Hkv, d.R);
     hipLaunchKernelGGL((decode_attn_kernel<E4M3, D, NRT>), grid, dim3(256), 0, st, d.T, d.H,
-                       d.kv.Hkv, d.kv.pages, d.kv.page, d.max_pages, d.scale * kLog2e,
+                       d.kv.Hkv, d.kv.pages, __builtin_ctz(d.kv.page), d.max_pages, d.scale * kLog2e,
                        static_cast<const bf16 *>(q), d.qs, c, table, lens, static_cast<bf16 *>(out),
                        d.os, lse, p);
     if (p.splits > 1) {
         const int64_t n = (int64_t)d.R * d.T * d.H;
-        hipLaunchKernelGGL((decode_join_kernel<D>), dim3((unsigned)((n + 3) / 4)), dim3(256), 0, st,
-                           n, d.T, d.H, d.max_pages * d.kv.page, lens, p, static_cast<bf16 *>(out),
-                           d.os, lse);
+        hipLaunchKernelGGL((decode_join_kernel<D>), dim3((unsigned)n), dim3(256), 0, st, d.T, d.H,
+                           d.max_pages * d.kv.page, lens, p, static_cast<bf16 *>(out), d.os, lse);
     }
 }
 

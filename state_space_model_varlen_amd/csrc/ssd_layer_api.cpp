@@ -198,7 +198,7 @@ int decode_dims(const attn_decode_problem *p, ssd::DecodeAttnDims *d)
     if (p->nheads % p->kv.nkv_heads != 0) return SSD_ERR_SHAPE;
     if (p->kv.in_dtype != SSD_BF16) return SSD_ERR_UNSUPPORTED;
     if (p->num_reqs > 65535 || (int64_t)p->tokens_per_req * p->nheads > 65535 ||
-        (int64_t)p->max_pages * p->kv.page_size > 0x7fffffffLL)
+        (int64_t)p->max_pages * p->kv.page_size > 0x7fffff00LL)
         return SSD_ERR_UNSUPPORTED;
     if (!scale_of(p->scale, p->kv.headdim, &d->scale)) return SSD_ERR_SHAPE;
     const int64_t row = (int64_t)p->nheads * p->kv.headdim;
