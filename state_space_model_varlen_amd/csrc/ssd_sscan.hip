@@ -401,58 +401,84 @@ static void launch_scan_n(const ScanDims &d, const ScanArgs &a, void *workspace,
     else launch_scan_l<TX, TS, N, 4>(d, a, p.seg, workspace, st);
 }
 
-// Verify-step form: L = 4 lanes per channel, N / 4 states each; a block takes 64
-// channels of one request. The state and the tokens' inputs, TM tokens at a
-// time, are all requested before the first wait.
+// Verify-step form, bound by the states: a lane holds 16 bytes of them (4 float
+// or 8 two-byte states), N of them a channel's L lanes, a block 256 / L channels
+// of one group and one request. The state and the inputs of TM tokens are all
+// requested before the first wait; B and C go through LDS, widened once for all
+// of the block's channels. States after a token leave past the caches: a
+// rollback reads one of them, later.
+template <typename TS, int M> __device__ __forceinline__ void store_state_nt(TS *p, const float *v) {
+    RawV<TS, M> r;
+    r.set(v);
+    typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+    static_assert(sizeof(r.v) == 16, "16 bytes a lane");
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, r.v), reinterpret_cast<u32x4 *>(p));
+}
+
 template <typename TX, typename TS, int N, int TM>
 __global__ __launch_bounds__(256) void scan_update_kernel(
     int Tr, int C, int G, int num_slots, int chb, ScanArgs a, int64_t xs, int64_t dts, int64_t zs,
     int64_t bs, int64_t cs, int64_t ys, DtTf tf, TS *__restrict__ inter)
 {
-    constexpr int L = 4, SPL = N / L, CB = 256 / L;
+    constexpr int SPL = 16 / (int)sizeof(TS), L = N / SPL, CB = 256 / L;
+    constexpr int BCV = (TM * N * 2 + 255) / 256;
+    __shared__ __align__(16) float bc[2][TM][N];
     const int tid = threadIdx.x, j0 = tid % L;
-    const int r = (int)(blockIdx.x / (unsigned)chb);
-    const int c = (int)(blockIdx.x % (unsigned)chb) * CB + tid / L;
-    if (c >= C) return;      // (whole quads)
-    const int g = c / (C / G);
-    const int slot = a.idx[r];
-    const bool slot_ok = slot >= 0 && slot < num_slots;
-    TS *const cache = static_cast<TS *>(a.cache) +
-                      ((int64_t)(slot_ok ? slot : 0) * C + c) * N + j0 * SPL;
-    const TX *const xp = static_cast<const TX *>(a.x) + (int64_t)r * Tr * xs + c;
-    const TX *const dp = static_cast<const TX *>(a.dt) + (int64_t)r * Tr * dts + c;
-    const TX *const zp = a.z ? static_cast<const TX *>(a.z) + (int64_t)r * Tr * zs + c : nullptr;
-    TX *const yp = static_cast<TX *>(a.y) + (int64_t)r * Tr * ys + c;
-    const TX *const Bp = static_cast<const TX *>(a.B) + (int64_t)r * Tr * bs + g * N + j0 * SPL;
-    const TX *const Cp = static_cast<const TX *>(a.C) + (int64_t)r * Tr * cs + g * N + j0 * SPL;
+    const int r = (int)(blockIdx.x / (unsigned)chb), cb = (int)(blockIdx.x % (unsigned)chb);
+    const int per = C / G, gblocks = chb / G, g = cb / gblocks;
+    const int in_g = cb % gblocks * CB + tid / L;
+    const bool live = in_g < per;
+    const int c = g * per + (live ? in_g : per - 1);
+    const int64_t row0 = (int64_t)r * Tr;
+    const TX *const xp = static_cast<const TX *>(a.x) + row0 * xs + c;
+    const TX *const dp = static_cast<const TX *>(a.dt) + row0 * dts + c;
+    const TX *const zp = a.z ? static_cast<const TX *>(a.z) + row0 * zs + c : nullptr;
+    TX *const yp = static_cast<TX *>(a.y) + row0 * ys + c;
+    const TX *const Bp = static_cast<const TX *>(a.B) + row0 * bs + (int64_t)g * N;
+    const TX *const Cp = static_cast<const TX *>(a.C) + row0 * cs + (int64_t)g * N;
 
-    TX xv[TM], dv[TM], zv[TM], Bv[TM][SPL], Cv[TM][SPL];
+    TX xv[TM], dv[TM], zv[TM], bv[BCV];
     auto request = [&](int t0) {
+        // value e: state e % N of token e / N, of B and then of C
+#pragma unroll
+        for (int k = 0; k < BCV; ++k) {
+            const int e = tid + 256 * k, t = t0 + e / N % TM;
+            const int64_t tr = t < Tr ? t : Tr - 1;
+            if (e < 2 * TM * N) bv[k] = e < TM * N ? Bp[tr * bs + e % N] : Cp[tr * cs + e % N];
+        }
 #pragma unroll
         for (int m = 0; m < TM; ++m) {
             const int64_t t = t0 + m < Tr ? t0 + m : Tr - 1;
             xv[m] = xp[t * xs];
             dv[m] = dp[t * dts];
-            if (zp) zv[m] = zp[t * zs];
-#pragma unroll
-            for (int i = 0; i < SPL; ++i) {
-                Bv[m][i] = Bp[t * bs + i];
-                Cv[m][i] = Cp[t * cs + i];
-            }
+            zv[m] = zp ? zp[t * zs] : xv[m];
         }
     };
-    float h[SPL], A2[SPL];
     if (Tr > 0) request(0);
-    load_state<TS, SPL>(cache, h);
+    const int slot = a.idx[r];
+    const bool slot_ok = slot >= 0 && slot < num_slots;
+    const int64_t so = (int64_t)c * N + j0 * SPL;
+    TS *const cache = static_cast<TS *>(a.cache) + (int64_t)(slot_ok ? slot : 0) * C * N + so;
+    RawV<TS, SPL> raw;
+    raw.load(cache);
+    float h[SPL], A2[SPL];
 #pragma unroll
-    for (int i = 0; i < SPL; ++i) A2[i] = a.A[(int64_t)c * N + j0 * SPL + i] * kLog2e;
+    for (int i = 0; i < SPL; ++i) A2[i] = a.A[so + i] * kLog2e;
     const float Dc = a.D ? a.D[c] : 0.0f, bias = tf.bias ? tf.bias[c] : 0.0f;
+    raw.get(h);
     if (!slot_ok) {
 #pragma unroll
         for (int i = 0; i < SPL; ++i) h[i] = 0.0f;
     }
     for (int t0 = 0; t0 < Tr; t0 += TM) {
-        if (t0 > 0) request(t0);
+        if (t0 > 0) {
+            __syncthreads();       // the last tokens' B and C are done with
+            request(t0);
+        }
+#pragma unroll
+        for (int k = 0; k < BCV; ++k)
+            if (tid + 256 * k < 2 * TM * N) (&bc[0][0][0])[tid + 256 * k] = to_f32(bv[k]);
+        __syncthreads();
 #pragma unroll
         for (int m = 0; m < TM; ++m) {
             const int t = t0 + m;
@@ -461,30 +487,36 @@ __global__ __launch_bounds__(256) void scan_update_kernel(
             float p = 0.0f;
 #pragma unroll
             for (int i = 0; i < SPL; ++i) {
-                h[i] = __builtin_amdgcn_exp2f(dt * A2[i]) * h[i] + u * to_f32(Bv[m][i]);
-                p += h[i] * to_f32(Cv[m][i]);
+                h[i] = fmaf(__builtin_amdgcn_exp2f(dt * A2[i]), h[i], u * bc[0][m][j0 * SPL + i]);
+                p = fmaf(h[i], bc[1][m][j0 * SPL + i], p);
             }
+            // the sum over the channel's L = 2, 4, 8 or 16 lanes
             p += dpp<0xb1>(p);
-            p += dpp<0x4e>(p);
+            if constexpr (L >= 4) p += dpp<0x4e>(p);
+            if constexpr (L >= 8) p += dpp<0x141>(p);
+            if constexpr (L >= 16) p += dpp<0x140>(p);
             const float y = (p + Dc * x) * (zp ? silu(to_f32(zv[m])) : 1.0f);
-            if (j0 == 0) yp[(int64_t)t * ys] = from_f32<TX>(y);
-            if (inter)
-                store_state<TS, SPL>(inter + (((int64_t)r * Tr + t) * C + c) * N + j0 * SPL, h);
+            if (live && j0 == 0) yp[(int64_t)t * ys] = from_f32<TX>(y);
+            if (inter && live) store_state_nt<TS, SPL>(inter + (row0 + t) * C * N + so, h);
         }
     }
-    if (!inter && slot_ok) store_state<TS, SPL>(cache, h);
+    if (!inter && slot_ok && live) store_state<TS, SPL>(cache, h);
 }
 
 template <typename TX, typename TS, int N>
 static void launch_update_n(const ScanDims &d, const ScanArgs &a, void *inter, hipStream_t st)
 {
-    const int Tr = d.T / d.S, chb = (d.C + 63) / 64;
+    constexpr int CB = 256 * 16 / (int)sizeof(TS) / N;
+    const int Tr = d.T / d.S, per = d.C / d.G, chb = d.G * ((per + CB - 1) / CB);
     const dim3 grid((unsigned)((int64_t)chb * d.S));
 #define SSD_UPD(TM)                                                                              \
     hipLaunchKernelGGL((scan_update_kernel<TX, TS, N, TM>), grid, dim3(256), 0, st, Tr, d.C, d.G, \
                        d.num_slots, chb, a, d.xs, d.dts, d.zs, d.bs, d.cs, d.ys, d.tf,           \
                        static_cast<TS *>(inter))
+    // tokens requested at once: the whole request when it has up to 4
     if (Tr <= 1) SSD_UPD(1);
+    else if (Tr <= 2) SSD_UPD(2);
+    else if (Tr <= 3) SSD_UPD(3);
     else SSD_UPD(4);
 #undef SSD_UPD
 }
