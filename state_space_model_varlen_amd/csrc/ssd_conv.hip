@@ -33,36 +33,61 @@ __global__ __launch_bounds__(64) void conv_kernel(
     const int b = (int)(blockIdx.x / (unsigned)chb);
     const int c0 = ((int)(blockIdx.x % (unsigned)chb) * kWave + (int)threadIdx.x) * VEC;
     const SeqTile t = cu ? find_tile(cu, S, T, TT, 1, b) : uniform_tile(S, T / S, TT, b);
-    if (t.seq < 0 || c0 >= C) return;
-    const int slot = idx[t.seq];
-    const bool slot_ok = slot >= 0 && slot < num_slots;
-    const bool init = slot_ok && (all_init || (has && has[t.seq]));
-    TS *const cs = cache + (int64_t)(slot_ok ? slot : 0) * (W - 1) * C + c0;
+    if (t.seq < 0) return;
+    // A lane's 8 channels x 4 taps are 128 bytes; read as they lie, every load of
+    // theirs would touch 64 lines, more than all the rows together. They come in
+    // whole lines and change lanes through LDS (the channel's place turned by the
+    // lane, so that neither side meets bank conflicts).
+    const int lane = threadIdx.x;
+    __shared__ f32x4 wl[VEC == 8 && W == 4 ? 512 : 1];
+    if constexpr (VEC == 8 && W == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int q = i * kWave + lane, ch = c0 - lane * 8 + q;
+            if (ch < C) wl[(q & ~7) | ((q ^ (q >> 3)) & 7)] = *reinterpret_cast<const f32x4 *>(weight + (int64_t)ch * 4);
+        }
+    }
+    if (c0 >= C) return;
     const TX *const xr = x + (int64_t)t.start * xs + c0;
     const bool first = t.t0 == 0;
     const int n = t.len - t.t0 < TT ? t.len - t.t0 : TT;
 
-    RawV<TS, VEC> old[W - 1];     // the slot's rows (the first tile)
-    RawV<TX, VEC> hist[W - 1];    // the rows before the tile (later tiles: places t0 - (W-1) ..)
-    RawV<TX, VEC> row[TT];
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k) {
-        old[k].zero();
-        hist[k].zero();
-        if (first && init) old[k].load(cs + (int64_t)k * C);
-        if (!first) hist[k].load(xr + (int64_t)(t.t0 - (W - 1) + k) * xs);
-    }
+    // requested in this order: the tile's rows, those before it (a later tile: places
+    // t0 - (W-1) ..; the first tile: the slot's rows, once its number is there)
+    RawV<TX, VEC> row[TT], hist[W - 1];
+    RawV<TS, VEC> old[W - 1];
     if (n > 0) {
 #pragma unroll
-        for (int j = 0; j < TT; ++j) {
-            const int place = t.t0 + (j < n ? j : n - 1);
-            row[j].load(xr + (int64_t)place * xs);
-        }
+        for (int j = 0; j < TT; ++j) row[j].load(xr + (int64_t)(t.t0 + (j < n ? j : n - 1)) * xs);
+    }
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+        hist[k].zero();
+        old[k].zero();
+    }
+    const int slot = idx[t.seq];
+    const bool slot_ok = slot >= 0 && slot < num_slots;
+    TS *const cs = cache + (int64_t)(slot_ok ? slot : 0) * (W - 1) * C + c0;
+    if (!first) {
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) hist[k].load(xr + (int64_t)(t.t0 - (W - 1) + k) * xs);
+    } else if (slot_ok && (all_init || (has && has[t.seq]))) {
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) old[k].load(cs + (int64_t)k * C);
+    }
+    if (n > 0) {
         float w[VEC][W], bs[VEC];
+        if constexpr (VEC == 8 && W == 4) wave_lds_sync();
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
+            if constexpr (VEC == 8 && W == 4) {
+                const f32x4 v = wl[lane * 8 + (i ^ (lane & 7))];
 #pragma unroll
-            for (int k = 0; k < W; ++k) w[i][k] = weight[(int64_t)(c0 + i) * W + k];
+                for (int k = 0; k < 4; ++k) w[i][k] = v[k];
+            } else {
+#pragma unroll
+                for (int k = 0; k < W; ++k) w[i][k] = weight[(int64_t)(c0 + i) * W + k];
+            }
             bs[i] = bias ? bias[c0 + i] : 0.0f;
         }
         const int seg = c0 < out.end0 ? 0 : (c0 < out.end1 ? 1 : 2);
@@ -169,7 +194,7 @@ static void launch_conv_w(const ConvDims &d, const void *x, const float *w, cons
         return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (uint64_t)stride * e % 16 == 0;
     };
     bool wide = d.C % 8 == 0 && o.end0 % 8 == 0 && o.end1 % 8 == 0 && on16(x, d.xs, sizeof(TX)) &&
-                on16(cache, d.C, sizeof(TS));
+                on16(cache, d.C, sizeof(TS)) && on16(w, 0, 4);
     for (int i = 0; i < 3; ++i)
         if (d.yc[i] > 0) wide = wide && on16(o.p[i], o.s[i], sizeof(TX));
     // a verify step's few tokens need no 16-row tile (and its registers)
