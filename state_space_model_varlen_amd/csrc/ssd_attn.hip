@@ -25,18 +25,20 @@ struct AttnArgs {
     float scale2;   // scale log2(e)
 };
 
-// The block's queries: tile of BM queries of one sequence, head and key head,
-// the sequence's key rows, and `off`: query i sees keys up to i + off.
+// The block's queries: tile of BM queries of one sequence, the first of its
+// heads (HPB of one key head's group) and the head past them, the key head, the
+// sequence's key rows, and `off`: query i sees keys up to i + off.
 struct AttnBlock {
-    int seq, q0, lq, qrow, head, kvh, krow, lk, off;
+    int seq, q0, lq, qrow, head, head_end, kvh, krow, lk, off;
 };
 // Heads run fastest over the blocks, the key head innermost, so that the 8
 // XCDs, which take blocks in turn, each see few key heads. The sequences with
 // the most keys come first (up to 64 of them), and within a sequence the last
 // tile, which sees the most.
-__device__ __forceinline__ AttnBlock attn_block(const AttnArgs &a, int BM) {
+__device__ __forceinline__ AttnBlock attn_block(const AttnArgs &a, int BM, int HPB = 1) {
     AttnBlock r;
-    const int hh = (int)(blockIdx.x % (unsigned)a.H), b = (int)(blockIdx.x / (unsigned)a.H);
+    const int group = a.H / a.Hkv, hb = a.Hkv * ((group + HPB - 1) / HPB);
+    const int hh = (int)(blockIdx.x % (unsigned)hb), b = (int)(blockIdx.x / (unsigned)hb);
     SeqTile t;
     if (a.S > 1 && a.S <= kWave) {
         LaneSeqs l = lane_seqs(a.cuq, a.S, a.Tq, BM, 0);
@@ -48,7 +50,8 @@ __device__ __forceinline__ AttnBlock attn_block(const AttnArgs &a, int BM) {
     r.seq = t.seq;
     if (t.seq < 0) return r;
     r.kvh = hh % a.Hkv;
-    r.head = r.kvh * (a.H / a.Hkv) + hh / a.Hkv;
+    r.head = r.kvh * group + hh / a.Hkv * HPB;
+    r.head_end = (r.kvh + 1) * group;
     r.lq = t.len;
     r.qrow = t.start;
     r.q0 = (t.len - 1) / BM * BM - t.t0;
@@ -82,19 +85,10 @@ __device__ __forceinline__ bool take_out(u32x4 &w, bf16) {
     }
     return any;
 }
-__device__ __forceinline__ bool take_out(u32x4 &w, float) {
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool bad = (w[i] & 0x7f800000u) == 0x7f800000u;
-        w[i] = bad ? 0u : w[i];
-        any |= bad;
-    }
-    return any;
-}
-
-// bf16 heads of D. A block of 4 waves takes BM = 128 queries of one head, 32 a
-// wave, against tiles of 64 keys in LDS, worked on in two steps of 32 keys.
+// bf16 heads of D. A block of 4 waves takes 32 queries of one head a wave: of HPB
+// heads that share a key head, BM = 128 / HPB queries of each (fewer queries
+// mean less work beyond the diagonal, and short sequences fill the block),
+// against tiles of 64 keys in LDS, worked on in two steps of 32 keys.
 //
 // Scores are formed transposed, S^T = K Q^T (keys x queries), so that a lane
 // holds 16 of every 32 scores of one query (its partner 32 lanes away the
@@ -120,21 +114,22 @@ template <int D> struct AttnSmem {
     int hidden;                      // a partly masked tile has non-finite values
 };
 
-template <int D>
+template <int D, int HPB>
 __global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a)
 {
     typedef AttnSmem<D> SM;
-    constexpr int BM = 128, BN = SM::BN, KP = SM::KP, VP = SM::VP;
+    constexpr int BM = 128 / HPB, BN = SM::BN, KP = SM::KP, VP = SM::VP;
     constexpr int VEC = BN * D / 8 / 256;       // 16-byte vectors a thread stages of K, and of V
     constexpr int RPT = D / 8;                  // threads a row
     __shared__ SM sm;
-    const AttnBlock b = attn_block(a, BM);
+    const AttnBlock b = attn_block(a, BM, HPB);
     if (b.seq < 0) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, qi = lane & 31, hf = lane >> 5;
-    const int q = b.q0 + wave * 32 + qi;                       // the lane's query
+    const int tid = threadIdx.x, lane = tid & 63, wave = scalar(tid >> 6), qi = lane & 31, hf = lane >> 5;
+    const int q = b.q0 + wave / HPB * 32 + qi;                 // the lane's query
     const int qc = q < b.lq ? q : b.lq - 1;
+    const int head = b.head + wave % HPB, hc = head < b.head_end ? head : b.head;
     const bf16 *const Q = static_cast<const bf16 *>(a.q) + (int64_t)(b.qrow + qc) * a.qs +
-                          (int64_t)b.head * D + hf * 8;
+                          (int64_t)hc * D + hf * 8;
     bf16x8 qf[D / 16];
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) qf[s] = *reinterpret_cast<const bf16x8 *>(Q + 16 * s);
@@ -304,11 +299,11 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a)
     }
 
     sum = across32(sum, added);
-    if (q < b.lq) {
+    if (q < b.lq && head < b.head_end) {
         // (a NaN sum is passed on; a row without keys gets zeros)
         const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
         bf16 *const out = static_cast<bf16 *>(a.out) + (int64_t)(b.qrow + q) * a.os +
-                          (int64_t)b.head * D + 4 * hf;
+                          (int64_t)head * D + 4 * hf;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -320,119 +315,351 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a)
             }
         if (a.lse && hf == 0) {
             const float ref = m == -__builtin_inff() ? 0.0f : m;
-            a.lse[(int64_t)(b.qrow + q) * a.H + b.head] = (ref + __builtin_amdgcn_logf(sum)) * kLn2;
+            a.lse[(int64_t)(b.qrow + q) * a.H + head] = (ref + __builtin_amdgcn_logf(sum)) * kLn2;
         }
     }
 }
 
-// float heads of D: the same pass on the float32 matrix instructions (16 x 16
-// tiles, 4 keys a step), 16 queries a wave, 32 keys a tile. A lane holds the
-// scores of query lane % 16 for keys 4 (lane / 16) + v of each 16.
+// Few queries, or few heads: a block of NW waves takes one tile of queries (32 in
+// bf16, 16 QT in float), and its waves the key tiles in turn, each with a running
+// maximum and sum of its own; they are joined in LDS at the end. The chain of
+// tiles that a wave walks is NW times shorter, and no matrix row is spent on
+// queries that are not there; but every tile of keys is read for fewer queries.
+// Keys go from memory to the operand's registers (any order of the head's
+// dimensions will do, as long as q's registers follow it), the next tile's
+// requested as soon as the scores are formed.
+//
+// join_waves: the waves' results (o scaled to the common maximum, in rows of
+// D + 4 floats a query) and statistics, one thread per PER elements.
+template <int D, int NQ, int NW> struct JoinSmem {
+    __align__(16) float o[NW][NQ * (D + 4)];
+};
+template <typename T, int D, int NQ, int NW>
+__device__ __forceinline__ void join_waves(const AttnArgs &a, const AttnBlock &b,
+                                           const float (&o)[NW][NQ * (D + 4)],
+                                           const float (&ml)[NW][2][NQ]) {
+    constexpr int PER = NQ * D / (NW * 64), TPR = D / PER;
+    static_assert(PER % 4 == 0, "whole vectors");
+    const int row = (int)threadIdx.x / TPR, d0 = (int)threadIdx.x % TPR * PER, q = b.q0 + row;
+    if (q >= b.lq) return;
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int w = 0; w < NW; ++w) top = fmaxf(top, ml[w][0][row]);
+    const float ref = top == -__builtin_inff() ? 0.0f : top;
+    float sum = 0.0f, acc[PER] = {};
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        sum += ml[w][1][row] * __builtin_amdgcn_exp2f(ml[w][0][row] - ref);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] += o[w][row * (D + 4) + d0 + e];
+    }
+    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    T *const out = static_cast<T *>(a.out) + (int64_t)(b.qrow + q) * a.os + (int64_t)b.head * D + d0;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] *= inv;
+#pragma unroll
+    for (int e = 0; e < PER; e += 4) store4<T>(out + e, acc + e);
+    if (a.lse && d0 == 0)
+        a.lse[(int64_t)(b.qrow + q) * a.H + b.head] = (ref + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
 template <int D>
-__global__ __launch_bounds__(256) void attn_f32_kernel(AttnArgs a)
+__global__ __launch_bounds__(512, 1) void attn_split_kernel(AttnArgs a)
 {
-    constexpr int BM = 64, BN = 32, P = D + 4, VEC = BN * D / 4 / 256, RPT = D / 4;
-    __shared__ __align__(16) float kt[BN * P], vt[BN * P];
-    __shared__ int hidden;
-    const AttnBlock b = attn_block(a, BM);
+    constexpr int NW = 8, BN = 32, VP = D + 32;
+    constexpr int VL = BN * D / 512, LPV = D / 8, RV = 64 / LPV;   // value loads, lanes a row, rows a load
+    typedef JoinSmem<D, 32, NW> JS;
+    __shared__ __align__(16) char raw[sizeof(JS) > NW * BN * VP * 2 ? sizeof(JS) : NW * BN * VP * 2];
+    __shared__ float ml[NW][2][32];
+    const AttnBlock b = attn_block(a, 32);
     if (b.seq < 0) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, qi = lane & 15, g = lane >> 4;
-    const int q = b.q0 + wave * 16 + qi, qc = q < b.lq ? q : b.lq - 1;
-    const float *const Q = static_cast<const float *>(a.q) + (int64_t)(b.qrow + qc) * a.qs +
-                           (int64_t)b.head * D + g;
-    float qf[D / 4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = scalar(tid >> 6), qi = lane & 31, hf = lane >> 5;
+    const int q = b.q0 + qi, qc = q < b.lq ? q : b.lq - 1;
+    const bf16 *const Q = static_cast<const bf16 *>(a.q) + (int64_t)(b.qrow + qc) * a.qs +
+                          (int64_t)b.head * D + hf * 8;
+    bf16x8 qf[D / 16];
 #pragma unroll
-    for (int s = 0; s < D / 4; ++s) qf[s] = Q[4 * s];
+    for (int s = 0; s < D / 16; ++s) qf[s] = *reinterpret_cast<const bf16x8 *>(Q + 16 * s);
     const int seen = q < b.lq ? keys_seen(b, q) : 0;
-    const int qlast = b.q0 + BM - 1 < b.lq - 1 ? b.q0 + BM - 1 : b.lq - 1;
-    const int kend = keys_seen(b, qlast), kfull = keys_seen(b, b.q0);
-    const float *const K = static_cast<const float *>(a.k) + (int64_t)b.krow * a.ks + (int64_t)b.kvh * D;
-    const float *const V = static_cast<const float *>(a.v) + (int64_t)b.krow * a.vs + (int64_t)b.kvh * D;
-    f32x4 o[D / 16];
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) o[i] = zero4();
-    float m = -__builtin_inff(), sum = 0.0f;
-    if (tid == 0) hidden = 0;
-    __syncthreads();
-    for (int j0 = 0; j0 < kend; j0 += BN) {
+    const int qlast = b.q0 + 31 < b.lq - 1 ? b.q0 + 31 : b.lq - 1;
+    const int kend = keys_seen(b, qlast), kfull = b.q0 + 31 < b.lq ? keys_seen(b, b.q0) : 0;
+    const int kopen = keys_seen(b, b.q0);          // keys that all queries there are see
+    const bf16 *const K = static_cast<const bf16 *>(a.k) + (int64_t)b.krow * a.ks + (int64_t)b.kvh * D;
+    const bf16 *const V = static_cast<const bf16 *>(a.v) + (int64_t)b.krow * a.vs + (int64_t)b.kvh * D;
+    bf16 *const vw = reinterpret_cast<bf16 *>(raw) + wave * BN * VP;
+
+    u32x4 kr[D / 16], vr[VL];
+    auto request_k = [&](int j0) __attribute__((always_inline)) {
         const int rows = b.lk - j0 < BN ? b.lk - j0 : BN;
-        const rsrc_t rk = make_rsrc(K + (int64_t)j0 * a.ks, (uint32_t)((rows - 1) * (int)a.ks + D) * 4);
-        const rsrc_t rv = make_rsrc(V + (int64_t)j0 * a.vs, (uint32_t)((rows - 1) * (int)a.vs + D) * 4);
-        u32x4 kr[VEC], vr[VEC];
+        const rsrc_t rs = make_rsrc(K + (int64_t)j0 * a.ks,
+                                    rows > 0 ? (uint32_t)((rows - 1) * (int)a.ks + D) * 2 : 0u);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const int row = (tid + 256 * i) / RPT, c = tid % RPT;
-            kr[i] = __builtin_bit_cast(u32x4, buf_ld16(rk, (uint32_t)(row * (int)a.ks + 4 * c) * 4));
-            vr[i] = __builtin_bit_cast(u32x4, buf_ld16(rv, (uint32_t)(row * (int)a.vs + 4 * c) * 4));
+        for (int s = 0; s < D / 16; ++s)
+            kr[s] = __builtin_bit_cast(u32x4, buf_ld16(rs, (uint32_t)(qi * (int)a.ks + 16 * s + 8 * hf) * 2));
+    };
+    auto request_v = [&](int j0) __attribute__((always_inline)) {
+        const int rows = b.lk - j0 < BN ? b.lk - j0 : BN;
+        const rsrc_t rs = make_rsrc(V + (int64_t)j0 * a.vs,
+                                    rows > 0 ? (uint32_t)((rows - 1) * (int)a.vs + D) * 2 : 0u);
+#pragma unroll
+        for (int l = 0; l < VL; ++l)
+            vr[l] = __builtin_bit_cast(u32x4, buf_ld16(rs, (uint32_t)((l * RV + lane / LPV) * (int)a.vs +
+                                                                     lane % LPV * 8) * 2));
+    };
+    f32x16 o[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
+    float m = -__builtin_inff(), sum = 0.0f;
+    bool odd = false;
+    const int jl = lane & 15;
+    const int vo = (4 * hf + (jl >> 2)) * VP + ((lane >> 4) & 1) * 16 + 4 * (jl & 3);
+    if (wave * BN < kend) {
+        request_k(wave * BN);
+        request_v(wave * BN);
+    }
+    for (int j0 = wave * BN; j0 < kend; j0 += NW * BN) {
+        f32x16 s;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = 0.0f;
+#pragma unroll
+        for (int st = 0; st < D / 16; ++st)
+            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kr[st]), qf[st], s, 0, 0, 0);
+        request_k(j0 + NW * BN);
+        if (j0 + BN > kopen) {
+#pragma unroll
+            for (int l = 0; l < VL; ++l) odd |= take_out(vr[l], bf16());
         }
-        __syncthreads();                       // the last tile's reads are done
+#pragma unroll
+        for (int l = 0; l < VL; ++l)
+            *reinterpret_cast<u32x4 *>(vw + (l * RV + lane / LPV) * VP + lane % LPV * 8) = vr[l];
+        request_v(j0 + NW * BN);
         if (j0 + BN > kfull) {
-            bool any = false;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) any |= take_out(vr[i], 0.0f);
-            if (any) hidden = 1;
+            for (int e = 0; e < 16; ++e)
+                if (j0 + 8 * (e >> 2) + 4 * hf + (e & 3) >= seen) s[e] = -__builtin_inff();
         }
+        float top = s[0];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const int row = (tid + 256 * i) / RPT, c = tid % RPT;
-            *reinterpret_cast<u32x4 *>(&kt[row * P + 4 * c]) = kr[i];
-            *reinterpret_cast<u32x4 *>(&vt[row * P + 4 * c]) = vr[i];
-        }
-        __syncthreads();
-        f32x4 s[2];
-        float top = -__builtin_inff();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            s[h] = zero4();
-#pragma unroll
-            for (int st = 0; st < D / 4; ++st)
-                s[h] = Mma<float>::run(kt[(16 * h + qi) * P + 4 * st + g], qf[st], s[h]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[h][e] = j0 + 16 * h + 4 * g + e < seen ? s[h][e] * a.scale2 : -__builtin_inff();
-                top = fmaxf(top, s[h][e]);
-            }
-        }
-        top = across32(across16(top, larger), larger);
+        for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e]);
+        top = across32(top, larger) * a.scale2;
         const float was = m;
         m = fmaxf(m, top);
         const float ref = m == -__builtin_inff() ? 0.0f : m, f = __builtin_amdgcn_exp2f(was - ref);
         sum *= f;
+        bf16x8 p[2];
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) o[i] *= f;
+        for (int e = 0; e < 16; ++e) {
+            const float w = __builtin_amdgcn_exp2f(s[e] * a.scale2 - ref);
+            sum += w;
+            p[e >> 3][e & 7] = static_cast<bf16>(w);
+        }
+        if (__any(top > was)) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+            for (int i = 0; i < D / 32; ++i) o[i] *= f;
+        }
+        wave_lds_sync();
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const v4i16 lo = lds_read_tr16(vw + vo + 16 * w * VP + 32 * i);
+                const v4i16 hi = lds_read_tr16(vw + vo + (16 * w + 8) * VP + 32 * i);
+                typedef short v8i16 __attribute__((ext_vector_type(8)));
+                const v8i16 both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, both), p[w],
+                                                               o[i], 0, 0, 0);
+            }
+        wave_lds_sync();
+    }
+    if (__any(odd)) {              // the values taken out, from the wave that had their tile
+        for (int k = kopen / BN * BN; k < kend; ++k)
+            if (k / BN % NW == wave && k < seen)
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float v = to_f32(V[(int64_t)k * a.vs + 32 * i + 8 * (e >> 2) + 4 * hf + (e & 3)]);
+                        if (!(fabsf(v) < __builtin_inff())) o[i][e] += v;
+                    }
+    }
+    sum = across32(sum, added);
+    if (hf == 0) {
+        ml[wave][0][qi] = m;
+        ml[wave][1][qi] = sum;
+    }
+    __syncthreads();               // (also: the value tiles are done with)
+    JS &js = *reinterpret_cast<JS *>(raw);
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int w = 0; w < NW; ++w) top = fmaxf(top, ml[w][0][qi]);
+    const float f = __builtin_amdgcn_exp2f(m - (top == -__builtin_inff() ? 0.0f : top));
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            f32x4 v;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = o[i][e + k] * f;
+            *reinterpret_cast<f32x4 *>(&js.o[wave][qi * (D + 4) + 32 * i + 2 * e + 4 * hf]) = v;
+        }
+    __syncthreads();
+    join_waves<bf16, D, 32, NW>(a, b, js.o, ml);
+}
+
+// float heads of D, on the float32 matrix instructions (16 x 16 tiles, 4 dimensions
+// or keys a step; their rate, an eighth of bf16's, is the bound): 16 QT queries a
+// block, 4 waves that take tiles of 16 keys in turn. A lane holds the scores of
+// query lane % 16 for keys 4 (lane / 16) + v; keys and values go straight from
+// memory to the operands, 16 bytes (keys) or one element (values) a lane.
+template <int D, int QT>
+__global__ __launch_bounds__(256, 1) void attn_f32_kernel(AttnArgs a)
+{
+    constexpr int NW = 4, BN = 16, NQ = 16 * QT;
+    typedef JoinSmem<D, NQ, NW> JS;
+    __shared__ JS js;
+    __shared__ float ml[NW][2][NQ];
+    const AttnBlock b = attn_block(a, NQ);
+    if (b.seq < 0) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = scalar(tid >> 6), qi = lane & 15, g = lane >> 4;
+    f32x4 qf[QT][D / 16];
+    int seen[QT];
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        const int q = b.q0 + 16 * t + qi, qc = q < b.lq ? q : b.lq - 1;
+        const float *const Q = static_cast<const float *>(a.q) + (int64_t)(b.qrow + qc) * a.qs +
+                               (int64_t)b.head * D + 4 * g;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) qf[t][s] = *reinterpret_cast<const f32x4 *>(Q + 16 * s);
+        seen[t] = q < b.lq ? keys_seen(b, q) : 0;
+    }
+    const int qlast = b.q0 + NQ - 1 < b.lq - 1 ? b.q0 + NQ - 1 : b.lq - 1;
+    const int kend = keys_seen(b, qlast), kopen = keys_seen(b, b.q0);
+    const float *const K = static_cast<const float *>(a.k) + (int64_t)b.krow * a.ks + (int64_t)b.kvh * D;
+    const float *const V = static_cast<const float *>(a.v) + (int64_t)b.krow * a.vs + (int64_t)b.kvh * D;
+    f32x4 kr[D / 16];
+    float vr[4][D / 16];
+    auto request_k = [&](int j0) __attribute__((always_inline)) {
+        const int rows = b.lk - j0 < BN ? b.lk - j0 : BN;
+        const rsrc_t rs = make_rsrc(K + (int64_t)j0 * a.ks,
+                                    rows > 0 ? (uint32_t)((rows - 1) * (int)a.ks + D) * 4 : 0u);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+            kr[s] = __builtin_bit_cast(f32x4, buf_ld16(rs, (uint32_t)(qi * (int)a.ks + 16 * s + 4 * g) * 4));
+    };
+    auto request_v = [&](int j0) __attribute__((always_inline)) {
+        const int rows = b.lk - j0 < BN ? b.lk - j0 : BN;
+        const rsrc_t rs = make_rsrc(V + (int64_t)j0 * a.vs,
+                                    rows > 0 ? (uint32_t)((rows - 1) * (int)a.vs + D) * 4 : 0u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                vr[e][i] = buf_ldf(rs, (uint32_t)((4 * g + e) * (int)a.vs + 16 * i + qi) * 4);
+    };
+    f32x4 o[QT][D / 16];
+    float m[QT], sum[QT];
+    bool odd = false;
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        m[t] = -__builtin_inff();
+        sum[t] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) o[t][i] = zero4();
+    }
+    if (wave * BN < kend) {
+        request_k(wave * BN);
+        request_v(wave * BN);
+    }
+    for (int j0 = wave * BN; j0 < kend; j0 += NW * BN) {
+        f32x4 s[QT];
+#pragma unroll
+        for (int t = 0; t < QT; ++t) s[t] = zero4();
+#pragma unroll
+        for (int st = 0; st < D / 16; ++st)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+#pragma unroll
+                for (int t = 0; t < QT; ++t) s[t] = Mma<float>::run(kr[st][v], qf[t][st][v], s[t]);
+        request_k(j0 + NW * BN);
+        if (j0 + BN > kopen) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const bool bad = !(fabsf(vr[e][i]) < __builtin_inff());
+                    odd |= bad;
+                    vr[e][i] = bad ? 0.0f : vr[e][i];
+                }
+        }
+        float p[QT][4];
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+            float top = -__builtin_inff();
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float p = __builtin_amdgcn_exp2f(s[h][e] - ref);
-                sum += p;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    o[i] = Mma<float>::run(vt[(16 * h + 4 * g + e) * P + 16 * i + qi], p, o[i]);
+                s[t][e] = j0 + 4 * g + e < seen[t] ? s[t][e] * a.scale2 : -__builtin_inff();
+                top = fmaxf(top, s[t][e]);
             }
+            top = across32(across16(top, larger), larger);
+            const float was = m[t];
+            m[t] = fmaxf(was, top);
+            const float ref = m[t] == -__builtin_inff() ? 0.0f : m[t];
+            const float f = __builtin_amdgcn_exp2f(was - ref);
+            sum[t] *= f;
+            if (__any(top > was)) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) o[t][i] *= f;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                p[t][e] = __builtin_amdgcn_exp2f(s[t][e] - ref);
+                sum[t] += p[t][e];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int t = 0; t < QT; ++t) o[t][i] = Mma<float>::run(vr[e][i], p[t][e], o[t][i]);
+        request_v(j0 + NW * BN);
     }
-    if (hidden)                                // the values taken out, for the queries that see them
-        for (int j = kfull / BN * BN; j < kend; ++j)
-            if (j < seen)
+    if (__any(odd)) {              // the values taken out, from the wave that had their tile
+        for (int k = kopen / BN * BN; k < kend; ++k)
+            if (k / BN % NW == wave)
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float v = V[(int64_t)j * a.vs + 16 * i + 4 * g + e];
-                        if (!(fabsf(v) < __builtin_inff())) o[i][e] += v;
-                    }
-    sum = across32(across16(sum, added), added);
-    if (q < b.lq) {
-        const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-        float *const out = static_cast<float *>(a.out) + (int64_t)(b.qrow + q) * a.os +
-                           (int64_t)b.head * D + 4 * g;
+                        const float v = V[(int64_t)k * a.vs + 16 * i + 4 * g + e];
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) *reinterpret_cast<f32x4 *>(out + 16 * i) = o[i] * inv;
-        if (a.lse && g == 0) {
-            const float ref = m == -__builtin_inff() ? 0.0f : m;
-            a.lse[(int64_t)(b.qrow + q) * a.H + b.head] = (ref + __builtin_amdgcn_logf(sum)) * kLn2;
+                        for (int t = 0; t < QT; ++t)
+                            if (k < seen[t] && !(fabsf(v) < __builtin_inff())) o[t][i][e] += v;
+                    }
+    }
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        sum[t] = across32(across16(sum[t], added), added);
+        if (g == 0) {
+            ml[wave][0][16 * t + qi] = m[t];
+            ml[wave][1][16 * t + qi] = sum[t];
         }
     }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int w = 0; w < NW; ++w) top = fmaxf(top, ml[w][0][16 * t + qi]);
+        const float f = __builtin_amdgcn_exp2f(m[t] - (top == -__builtin_inff() ? 0.0f : top));
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+            *reinterpret_cast<f32x4 *>(&js.o[wave][(16 * t + qi) * (D + 4) + 16 * i + 4 * g]) = o[t][i] * f;
+    }
+    __syncthreads();
+    join_waves<float, D, NQ, NW>(a, b, js.o, ml);
 }
 
 void launch_attn(const AttnDims &d, const void *q, const void *k, const void *v,
@@ -442,15 +669,36 @@ void launch_attn(const AttnDims &d, const void *q, const void *k, const void *v,
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     const AttnArgs a{q, k, v, cuq, cuk, out, lse, d.qs, d.ks, d.vs, d.os, d.Tq, d.Tk, d.S, d.H,
                      d.Hkv, d.causal ? 1 : 0, d.scale * kLog2e};
-    const int BM = d.bf16 ? 128 : 64;
-    const dim3 grid((unsigned)(((int64_t)d.Tq / BM + d.S) * d.H));
-    if (d.bf16) {
-        if (d.D == 128) hipLaunchKernelGGL(attn_kernel<128>, grid, dim3(256), 0, st, a);
-        else hipLaunchKernelGGL(attn_kernel<64>, grid, dim3(256), 0, st, a);
-    } else {
-        if (d.D == 128) hipLaunchKernelGGL(attn_f32_kernel<128>, grid, dim3(256), 0, st, a);
-        else hipLaunchKernelGGL(attn_f32_kernel<64>, grid, dim3(256), 0, st, a);
-    }
+    const int64_t Tq = d.Tq, S = d.S, H = d.H, group = H / d.Hkv;
+    // bf16: the waves of a block on 4 or 2 heads of a group where that divides it, or
+    // where sequences are too short to fill 128 queries of one (32 sequences of 32
+    // queries on 4224 cached keys: 32 heads of 128 on 8 key heads 325 us with one head
+    // a block, 150 us with 4; 40 heads of 64, five to a key head, 255 and 131 us)
+    const int hpb = group % 4 == 0 || (group > 2 && Tq <= 40 * S) ? 4 : (group % 2 == 0 ? 2 : 1);
+    // ... or sharing the keys of 32 queries of one head, where there are no blocks for
+    // most of the 256 CUs (1523 tokens, 2 heads: 25 us without, 13 us with; 5 prompts to
+    // 3513 tokens, 2 heads, 128 blocks: 52 and 28 us; 4096 tokens, 8 heads, 264 blocks:
+    // 94 and 103 us; one of 512 tokens, 32 heads, 128 blocks: 19 and 21 us)
+    const int64_t blocks = (Tq * hpb / 128 + S) * d.Hkv * ((group + hpb - 1) / hpb);
+    const bool split = blocks <= 64 || (blocks <= 224 && (int64_t)d.Tk > 512 * S);
+    // float: two tiles of queries share the keys once there are enough of them
+    const bool two = (Tq / 32 + S) * H >= 512;
+#define SSD_ATTN(KERNEL, BM, HEADS, THREADS) \
+    hipLaunchKernelGGL((KERNEL), dim3((unsigned)((Tq / (BM) + S) * (HEADS))), dim3(THREADS), 0, st, a)
+#define SSD_ATTN_D(DD)                                                                        \
+    do {                                                                                      \
+        if (d.bf16 && split) SSD_ATTN(attn_split_kernel<DD>, 32, H, 512);                     \
+        else if (d.bf16 && hpb == 4)                                                          \
+            SSD_ATTN((attn_kernel<DD, 4>), 32, d.Hkv * ((group + 3) / 4), 256);               \
+        else if (d.bf16 && hpb == 2) SSD_ATTN((attn_kernel<DD, 2>), 64, H / 2, 256);          \
+        else if (d.bf16) SSD_ATTN((attn_kernel<DD, 1>), 128, H, 256);                         \
+        else if (two) SSD_ATTN((attn_f32_kernel<DD, 2>), 32, H, 256);                         \
+        else SSD_ATTN((attn_f32_kernel<DD, 1>), 16, H, 256);                                  \
+    } while (0)
+    if (d.D == 128) SSD_ATTN_D(128);
+    else SSD_ATTN_D(64);
+#undef SSD_ATTN_D
+#undef SSD_ATTN
 }
 
 }  // namespace ssd

@@ -306,8 +306,8 @@ int attention_varlen(const attn_problem *p, const void *q, const void *k, const 
     if (p->num_seqs == 0 && (p->total_q > 0 || p->total_k > 0)) return SSD_ERR_SHAPE;
     if (!float_ok(p->dtype)) return SSD_ERR_DTYPE;
     if (!headdim_ok(p->headdim)) return SSD_ERR_UNSUPPORTED;
-    // grid limit: query tiles of at least 64 rows, one more a sequence, times heads
-    if (((int64_t)p->total_q / 64 + p->num_seqs) * p->nheads > 0x7fffffffLL)
+    // grid limit: query tiles of at least 16 rows, one more a sequence, times heads
+    if (((int64_t)p->total_q / 16 + p->num_seqs) * p->nheads > 0x7fffffffLL)
         return SSD_ERR_UNSUPPORTED;
     ssd::AttnDims d;
     const int64_t qr = (int64_t)p->nheads * p->headdim, kr = (int64_t)p->nkv_heads * p->headdim;

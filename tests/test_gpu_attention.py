@@ -40,9 +40,10 @@ def compare(out, lse, ref, D, nk, dt):
     bad = ~(np.abs(got - want) <= tol)
     assert not bad.any(), (int(bad.sum()), float(np.nanmax(np.abs(got - want))))
     if lse is not None:
+        f = np.isfinite(wl)
         gl = lse.cpu().double().numpy()
         assert np.array_equal(np.isneginf(gl), np.isneginf(wl))
-        f = np.isfinite(wl)
+        gl, wl = np.where(f, gl, 0), np.where(f, wl, 0)
         tl = (2 * D + 8) * 2.0 ** -24 * top + (nk + 16) * 2.0 ** -24 + 2.0 ** -22 * np.abs(
             np.where(f, wl, 0))
         assert np.all(np.abs(gl - wl)[f] <= tl[f])
@@ -72,6 +73,23 @@ def test_heads(dt, H, Hkv):
     run(H, [70, 33], [70, 90], H, Hkv, 64, dt)
 
 
+# many heads: whole blocks of 1, 2 or 4 heads of a group, and groups that do not fill them
+MANY = [(64, 64), (64, 32), (64, 16), (40, 8), (48, 16)]
+
+
+@pytest.mark.parametrize("H,Hkv", MANY)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,klens", [([63, 0, 65, 1], [63, 9, 100, 129]), ([129], [300]),
+                                        ([9, 33, 20, 2], [40, 33, 10, 0])])
+def test_many_heads(H, Hkv, D, lens, klens):
+    run(H + Hkv, lens, klens, H, Hkv, D, BF)
+
+
+@pytest.mark.parametrize("H,Hkv,dt", [(64, 64, BF), (64, 16, BF), (64, 32, F32)])
+def test_many_heads_full(H, Hkv, dt):
+    run(12, [70, 3, 0, 5], [33, 129, 7, 0], H, Hkv, 64, dt, causal=False)
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("D", [64, 128])
 def test_full_and_scaled(dt, D):
@@ -94,11 +112,12 @@ def test_queries_that_see_nothing(dt):
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
-def test_hidden_rows_do_not_matter(dt, D, bad):
+@pytest.mark.parametrize("H,Hkv", [(2, 1), (48, 48), (64, 16)])
+def test_hidden_rows_do_not_matter(dt, D, bad, H, Hkv):
     """Non-finite keys and values behind a query, in the same sequence or the next, change
     nothing; a value seen by a query reaches it."""
     lens, klens = [100, 70], [130, 70]
-    m = make(6, lens, klens, 2, 1, D, dt)
+    m = make(6, lens, klens, H, Hkv, D, dt)
     ref = ol.attention(m["q"], m["k"], m["v"], m["cuq"], m["cuk"])
     k, v = m["k"].clone(), m["v"].clone()
     k[110:130] = bad           # seen by the last 20 queries of sequence 0 at most
