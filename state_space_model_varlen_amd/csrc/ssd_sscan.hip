@@ -354,10 +354,12 @@ static ScanPlan scan_plan(const ScanDims &d)
         best = ScanPlan{16, 0};
     }
     for (int seg = 128; seg <= 512; seg *= 2) {
-        const double e = fmax(2.0 * seg * 280, share * 325) + 12000 + longest / seg * 250 + seg * 50.0;
-        if (longest > seg && e < least) {
-            least = e;
-            best = ScanPlan{4, seg};
+        const double joins = 12000 + longest / seg * 250 + seg * 50.0;
+        const double s4 = fmax(2.0 * seg * 280, share * 325) + joins;
+        const double s16 = fmax(2.0 * seg * 117, share * 4 * 165) + joins;
+        if (longest > seg && fmin(s4, s16) < least) {
+            least = fmin(s4, s16);
+            best = ScanPlan{s16 < s4 ? 16 : 4, seg};
         }
     }
     return best;
