@@ -7,7 +7,12 @@
 // Every (channel, state) has a decay of its own, so the recurrence has no
 // matrix product in it: each token costs one exponential, two products and two
 // multiply-adds per (channel, state) on the vector units, which bound the
-// prompt form. The single-token form is bound by the states it reads and writes.
+// prompt form: a wave issues 38 instructions for a token of its 16 channels (N =
+// 16), 20 of which are those five for its 4 states a lane; the rest prepares step
+// sizes and gates, moves rows and joins lanes. At 4 cycles each (8 an exponential)
+// the 8192 tokens x 4096 channels of 1 prompt, run twice for their segments, take
+// 256 us of issue alone; measured 262 us. The single-token form is bound by the
+// states it reads and writes.
 #include "ssd_layer.h"
 #include "ssd_layer_device.h"
 #include <cmath>
@@ -30,8 +35,11 @@ __device__ __forceinline__ float softplus(float v) {
     p = p * q + 2.0f;
     return fmaxf(v, 0.0f) + p * s;
 }
+__device__ __forceinline__ float transformed(const DtTf &tf, float raw, float bias) {
+    return __builtin_amdgcn_fmed3f(softplus(raw + bias), tf.lo, tf.hi);
+}
 __device__ __forceinline__ float step_size(const DtTf &tf, float raw, float bias) {
-    return tf.on ? __builtin_amdgcn_fmed3f(softplus(raw + bias), tf.lo, tf.hi) : raw;
+    return tf.on ? transformed(tf, raw, bias) : raw;
 }
 __device__ __forceinline__ float silu(float z) {
     return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
@@ -154,7 +162,7 @@ __global__ __launch_bounds__(256) void scan_kernel(
     unsigned id = blockIdx.x;
     if (L == 16 && (id | 31u) < gridDim.x) id = (id & ~31u) | (id & 7u) << 2 | (id >> 3 & 3u);
     const int b = (int)(id / (unsigned)chb), cb = (int)(id % (unsigned)chb);
-    const SeqTile tile = sg.cur == 0 && S > 1 && S <= kWave
+    const SeqTile tile = S > 1 && S <= kWave
                              ? heaviest_first(lane_seqs(a.cu, S, T, sg.seg, 1), S, sg.seg, b)
                              : find_tile(a.cu, S, T, sg.seg, 1, b);
     if (tile.seq < 0) return;
@@ -242,12 +250,22 @@ __global__ __launch_bounds__(256) void scan_kernel(
     for (int t0 = 0; t0 < len; t0 += ST, buf ^= 1) {
 #pragma unroll
         for (int k = 0; k < BCV; ++k) (&bc[buf][0][0][0])[tid + 256 * k] = widen_one<TX>(bv[k]);
+        // (each choice once for all groups, so that their chains of dependent steps run
+        // side by side)
         float x[GROUPS], dt[GROUPS], gate[GROUPS];
 #pragma unroll
         for (int m = 0; m < GROUPS; ++m) {
             x[m] = widen_one<TX>(xv[m]);
-            dt[m] = step_size(tf, widen_one<TX>(dv[m]), bias);
-            gate[m] = gated ? silu(widen_one<TX>(zv[m])) : 1.0f;
+            dt[m] = widen_one<TX>(dv[m]);
+            gate[m] = 1.0f;
+        }
+        if (tf.on) {
+#pragma unroll
+            for (int m = 0; m < GROUPS; ++m) dt[m] = transformed(tf, dt[m], bias);
+        }
+        if (gated && out) {
+#pragma unroll
+            for (int m = 0; m < GROUPS; ++m) gate[m] = silu(widen_one<TX>(zv[m]));
         }
         if (t0 + ST > len) {          // tokens past the end take no step: the state stays
 #pragma unroll
@@ -333,10 +351,11 @@ __global__ __launch_bounds__(256) void scan_kernel(
 // channel (16 channels a wave) and 117 with 16 (4 channels); waves that share
 // a SIMD 175 and 90 each; both launches of the segmented form together 325.
 //   2 prompts of 100 and 156 tokens, 64 channels: 16 lanes 24 us, 4 lanes 34 us
-//   1 of 8192, 4096 channels: 857 us with 4 lanes, 446 us with 16, 267 us in
-//   segments of 256 (279 us of 128, 285 us of 512)
-//   8 of 1 to 1600, 5120 channels: 187 us with 4 lanes, the longest first (274 us
-//   in the order given), 223 us with 16, 207 us in segments of 256
+//   1 of 8192, 4096 channels: 830 us with 4 lanes, 438 us with 16, 262 us in
+//   segments of 256 (271 us of 128, 280 us of 512)
+//   8 of 1 to 1600, 5120 channels: 184 us with 4 lanes, the longest first (274 us
+//   in the order given), 224 us with 16, 209 us in segments of 256
+//   2 of 717 and 1508, 72 channels: 20 us in segments with 16 lanes, 37 us with 4
 // The longest sequence is not known here: 2.5 times the mean stands for it.
 struct ScanPlan {
     int lanes, seg;
