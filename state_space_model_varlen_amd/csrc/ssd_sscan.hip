@@ -355,6 +355,8 @@ __global__ __launch_bounds__(256) void scan_kernel(
 //   segments of 256 (271 us of 128, 280 us of 512)
 //   8 of 1 to 1600, 5120 channels: 184 us with 4 lanes, the longest first (274 us
 //   in the order given), 224 us with 16, 209 us in segments of 256
+//   1 of 1024, 5120 channels: 62 us in segments of 128, 92 us with 16 lanes (1280
+//   waves), 109 us with 4
 //   2 of 717 and 1508, 72 channels: 20 us in segments with 16 lanes, 37 us with 4
 // The longest sequence is not known here: 2.5 times the mean stands for it.
 struct ScanPlan {
@@ -366,8 +368,10 @@ static ScanPlan scan_plan(const ScanDims &d)
     if (d.S <= 0) return best;
     const double T = d.T, waves = (double)d.C * d.N / 16 / 16;
     const double longest = d.S == 1 ? T : fmin(T, 2.5 * T / d.S), share = T * waves / 1024;
-    double least = fmax(longest * 280, share * 175);
-    const double e16 = fmax(longest * 117, share * 4 * 90);
+    // one sequence's waves are all as long: the SIMDs that get one more set the time
+    const double on4 = d.S == 1 ? ceil(waves / 1024) : 1, on16 = d.S == 1 ? ceil(waves * 4 / 1024) : 1;
+    double least = fmax(longest * fmax(280, on4 * 175), share * 175);
+    const double e16 = fmax(longest * fmax(117, on16 * 90), share * 4 * 90);
     if (e16 < least) {
         least = e16;
         best = ScanPlan{16, 0};
