@@ -325,9 +325,9 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a)
 // maximum and sum of its own; they are joined in LDS at the end. The chain of
 // tiles that a wave walks is NW times shorter, and no matrix row is spent on
 // queries that are not there; but every tile of keys is read for fewer queries.
-// Keys go from memory to the operand's registers (any order of the head's
-// dimensions will do, as long as q's registers follow it), the next tile's
-// requested as soon as the scores are formed.
+// A wave's tiles are its own, staged in LDS of its own without barriers: rows read
+// straight into the keys' operand would touch 32 lines with every load (2.1 us a
+// round of 8 tiles of heads of 128, against 1.4).
 //
 // join_waves: the waves' results (o scaled to the common maximum, in rows of
 // D + 4 floats a query) and statistics, one thread per PER elements.
@@ -366,10 +366,11 @@ __device__ __forceinline__ void join_waves(const AttnArgs &a, const AttnBlock &b
 template <int D>
 __global__ __launch_bounds__(512, 1) void attn_split_kernel(AttnArgs a)
 {
-    constexpr int NW = 8, BN = 32, VP = D + 32;
+    constexpr int NW = 8, BN = 32, KP = D + 8, VP = D + 32;
     constexpr int VL = BN * D / 512, LPV = D / 8, RV = 64 / LPV;   // value loads, lanes a row, rows a load
     typedef JoinSmem<D, 32, NW> JS;
-    __shared__ __align__(16) char raw[sizeof(JS) > NW * BN * VP * 2 ? sizeof(JS) : NW * BN * VP * 2];
+    constexpr int TILES = NW * BN * (KP + VP) * 2;
+    __shared__ __align__(16) char raw[sizeof(JS) > TILES ? sizeof(JS) : TILES];
     __shared__ float ml[NW][2][32];
     const AttnBlock b = attn_block(a, 32);
     if (b.seq < 0) return;
@@ -386,25 +387,17 @@ __global__ __launch_bounds__(512, 1) void attn_split_kernel(AttnArgs a)
     const int kopen = keys_seen(b, b.q0);          // keys that all queries there are see
     const bf16 *const K = static_cast<const bf16 *>(a.k) + (int64_t)b.krow * a.ks + (int64_t)b.kvh * D;
     const bf16 *const V = static_cast<const bf16 *>(a.v) + (int64_t)b.krow * a.vs + (int64_t)b.kvh * D;
-    bf16 *const vw = reinterpret_cast<bf16 *>(raw) + wave * BN * VP;
+    bf16 *const kw = reinterpret_cast<bf16 *>(raw) + wave * BN * (KP + VP), *const vw = kw + BN * KP;
 
-    u32x4 kr[D / 16], vr[VL];
-    auto request_k = [&](int j0) __attribute__((always_inline)) {
+    u32x4 kr[VL], vr[VL];
+    auto request = [&](u32x4 (&r)[VL], const bf16 *base, int stride, int j0) __attribute__((always_inline)) {
         const int rows = b.lk - j0 < BN ? b.lk - j0 : BN;
-        const rsrc_t rs = make_rsrc(K + (int64_t)j0 * a.ks,
-                                    rows > 0 ? (uint32_t)((rows - 1) * (int)a.ks + D) * 2 : 0u);
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s)
-            kr[s] = __builtin_bit_cast(u32x4, buf_ld16(rs, (uint32_t)(qi * (int)a.ks + 16 * s + 8 * hf) * 2));
-    };
-    auto request_v = [&](int j0) __attribute__((always_inline)) {
-        const int rows = b.lk - j0 < BN ? b.lk - j0 : BN;
-        const rsrc_t rs = make_rsrc(V + (int64_t)j0 * a.vs,
-                                    rows > 0 ? (uint32_t)((rows - 1) * (int)a.vs + D) * 2 : 0u);
+        const rsrc_t rs = make_rsrc(base + (int64_t)j0 * stride,
+                                    rows > 0 ? (uint32_t)((rows - 1) * stride + D) * 2 : 0u);
 #pragma unroll
         for (int l = 0; l < VL; ++l)
-            vr[l] = __builtin_bit_cast(u32x4, buf_ld16(rs, (uint32_t)((l * RV + lane / LPV) * (int)a.vs +
-                                                                     lane % LPV * 8) * 2));
+            r[l] = __builtin_bit_cast(u32x4, buf_ld16(rs, (uint32_t)((l * RV + lane / LPV) * stride +
+                                                                    lane % LPV * 8) * 2));
     };
     f32x16 o[D / 32];
 #pragma unroll
@@ -416,17 +409,22 @@ __global__ __launch_bounds__(512, 1) void attn_split_kernel(AttnArgs a)
     const int jl = lane & 15;
     const int vo = (4 * hf + (jl >> 2)) * VP + ((lane >> 4) & 1) * 16 + 4 * (jl & 3);
     if (wave * BN < kend) {
-        request_k(wave * BN);
-        request_v(wave * BN);
+        request(kr, K, (int)a.ks, wave * BN);
+        request(vr, V, (int)a.vs, wave * BN);
     }
     for (int j0 = wave * BN; j0 < kend; j0 += NW * BN) {
+#pragma unroll
+        for (int l = 0; l < VL; ++l)
+            *reinterpret_cast<u32x4 *>(kw + (l * RV + lane / LPV) * KP + lane % LPV * 8) = kr[l];
+        request(kr, K, (int)a.ks, j0 + NW * BN);
+        wave_lds_sync();
         f32x16 s;
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[e] = 0.0f;
 #pragma unroll
         for (int st = 0; st < D / 16; ++st)
-            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kr[st]), qf[st], s, 0, 0, 0);
-        request_k(j0 + NW * BN);
+            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                *reinterpret_cast<const bf16x8 *>(kw + qi * KP + 16 * st + 8 * hf), qf[st], s, 0, 0, 0);
         if (j0 + BN > kopen) {
 #pragma unroll
             for (int l = 0; l < VL; ++l) odd |= take_out(vr[l], bf16());
@@ -434,7 +432,7 @@ __global__ __launch_bounds__(512, 1) void attn_split_kernel(AttnArgs a)
 #pragma unroll
         for (int l = 0; l < VL; ++l)
             *reinterpret_cast<u32x4 *>(vw + (l * RV + lane / LPV) * VP + lane % LPV * 8) = vr[l];
-        request_v(j0 + NW * BN);
+        request(vr, V, (int)a.vs, j0 + NW * BN);
         if (j0 + BN > kfull) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
@@ -676,11 +674,13 @@ void launch_attn(const AttnDims &d, const void *q, const void *k, const void *v,
     // a block, 150 us with 4; 40 heads of 64, five to a key head, 255 and 131 us)
     const int hpb = group % 4 == 0 || (group > 2 && Tq <= 40 * S) ? 4 : (group % 2 == 0 ? 2 : 1);
     // ... or sharing the keys of 32 queries of one head, where there are no blocks for
-    // most of the 256 CUs (1523 tokens, 2 heads: 25 us without, 13 us with; 5 prompts to
-    // 3513 tokens, 2 heads, 128 blocks: 52 and 28 us; 4096 tokens, 8 heads, 264 blocks:
-    // 94 and 103 us; one of 512 tokens, 32 heads, 128 blocks: 19 and 21 us)
+    // most of the 256 CUs, or barely and the keys are long, the more blocks the longer
+    // (without and with, us: 1523 tokens, 2 heads, 24 blocks: 25 and 12; 5 prompts to
+    // 3513 tokens, 2 heads, 128 blocks: 52 and 24; 4 prompts of 700, 8 heads, 200
+    // blocks: 22 and 27; 4096 tokens, 8 heads, 264 blocks: 94 and 81; 1024 tokens, 32
+    // heads on 8, 264 blocks: 30 and 39; 3000 tokens, 12 heads, 288 blocks: 69 and 74)
     const int64_t blocks = (Tq * hpb / 128 + S) * d.Hkv * ((group + hpb - 1) / hpb);
-    const bool split = blocks <= 64 || (blocks <= 224 && (int64_t)d.Tk > 512 * S);
+    const bool split = blocks <= 64 || (blocks <= 272 && (int64_t)d.Tk > 4 * blocks * S);
     // float: two tiles of queries share the keys once there are enough of them
     const bool two = (Tq / 32 + S) * H >= 512;
 #define SSD_ATTN(KERNEL, BM, HEADS, THREADS) \
