@@ -674,13 +674,19 @@ void launch_attn(const AttnDims &d, const void *q, const void *k, const void *v,
     // a block, 150 us with 4; 40 heads of 64, five to a key head, 255 and 131 us)
     const int hpb = group % 4 == 0 || (group > 2 && Tq <= 40 * S) ? 4 : (group % 2 == 0 ? 2 : 1);
     // ... or sharing the keys of 32 queries of one head, where there are no blocks for
-    // most of the 256 CUs, or barely and the keys are long, the more blocks the longer
-    // (without and with, us: 1523 tokens, 2 heads, 24 blocks: 25 and 12; 5 prompts to
-    // 3513 tokens, 2 heads, 128 blocks: 52 and 24; 4 prompts of 700, 8 heads, 200
-    // blocks: 22 and 27; 4096 tokens, 8 heads, 264 blocks: 94 and 81; 1024 tokens, 32
-    // heads on 8, 264 blocks: 30 and 39; 3000 tokens, 12 heads, 288 blocks: 69 and 74)
+    // most of the 256 CUs (without and with, us: 1523 tokens, 2 heads, 24 blocks: 25 and
+    // 12; 11 prompts of 981 on 1352 keys, 8 heads on 2, 82 blocks: 36 and 17; 120 on 106,
+    // 40 heads on 8, 128 blocks: 10 and 8; 512 tokens, 32 heads on 8, 136 blocks: 19 and
+    // 17; 9 prompts of 950 on 308, 16 heads on 4, 152 blocks: 19 and 20), or barely and
+    // the keys are long, the more blocks the longer. Of several sequences one is taken
+    // to be twice the mean: the lengths are not known here, and the cost of a long one
+    // missed is the greater (15 prompts of 4789 on 4321, the longest on 4134, 4 heads,
+    // 164 blocks: 90 and 35; 4 of 700, 8 heads, 200 blocks: 22 and 27; 1024 tokens, 32
+    // heads on 8, 264 blocks: 30 and 39; 4096, 8 heads, 264 blocks: 94 and 81; 3000, 12
+    // heads, 288 blocks: 69 and 74)
     const int64_t blocks = (Tq * hpb / 128 + S) * d.Hkv * ((group + hpb - 1) / hpb);
-    const bool split = blocks <= 64 || (blocks <= 272 && (int64_t)d.Tk > 4 * blocks * S);
+    const int64_t longest = S == 1 ? d.Tk : 2 * (int64_t)d.Tk / S;
+    const bool split = blocks <= 144 || (blocks <= 272 && longest > 4 * blocks);
     // float: two tiles of queries share the keys once there are enough of them
     const bool two = (Tq / 32 + S) * H >= 512;
 #define SSD_ATTN(KERNEL, BM, HEADS, THREADS) \
