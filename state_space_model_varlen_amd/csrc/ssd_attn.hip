@@ -510,7 +510,10 @@ __global__ __launch_bounds__(512, 1) void attn_split_kernel(AttnArgs a)
 // or keys a step; their rate, an eighth of bf16's, is the bound): 16 QT queries a
 // block, 4 waves that take tiles of 16 keys in turn. A lane holds the scores of
 // query lane % 16 for keys 4 (lane / 16) + v; keys and values go straight from
-// memory to the operands, 16 bytes (keys) or one element (values) a lane.
+// memory to the operands, 16 bytes a lane: the four dimensions that a lane gets
+// of a value belong to four products, so row r of product 4 i + c is dimension
+// 64 i + 4 r + c (with one element a load 199 us instead of 161: 19 prompts of 20,
+// one of them on 8000 keys, 16 heads of 128).
 template <int D, int QT>
 __global__ __launch_bounds__(256, 1) void attn_f32_kernel(AttnArgs a)
 {
@@ -537,7 +540,7 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(AttnArgs a)
     const float *const K = static_cast<const float *>(a.k) + (int64_t)b.krow * a.ks + (int64_t)b.kvh * D;
     const float *const V = static_cast<const float *>(a.v) + (int64_t)b.krow * a.vs + (int64_t)b.kvh * D;
     f32x4 kr[D / 16];
-    float vr[4][D / 16];
+    f32x4 vr[4][D / 64];
     auto request_k = [&](int j0) __attribute__((always_inline)) {
         const int rows = b.lk - j0 < BN ? b.lk - j0 : BN;
         const rsrc_t rs = make_rsrc(K + (int64_t)j0 * a.ks,
@@ -553,8 +556,9 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(AttnArgs a)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-                vr[e][i] = buf_ldf(rs, (uint32_t)((4 * g + e) * (int)a.vs + 16 * i + qi) * 4);
+            for (int i = 0; i < D / 64; ++i)
+                vr[e][i] = __builtin_bit_cast(f32x4, buf_ld16(rs, (uint32_t)((4 * g + e) * (int)a.vs +
+                                                                            64 * i + 4 * qi) * 4));
     };
     f32x4 o[QT][D / 16];
     float m[QT], sum[QT];
@@ -586,9 +590,9 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(AttnArgs a)
             for (int e = 0; e < 4; ++e)
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
-                    const bool bad = !(fabsf(vr[e][i]) < __builtin_inff());
+                    const bool bad = !(fabsf(vr[e][i / 4][i % 4]) < __builtin_inff());
                     odd |= bad;
-                    vr[e][i] = bad ? 0.0f : vr[e][i];
+                    vr[e][i / 4][i % 4] = bad ? 0.0f : vr[e][i / 4][i % 4];
                 }
         }
         float p[QT][4];
@@ -621,7 +625,7 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(AttnArgs a)
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-                for (int t = 0; t < QT; ++t) o[t][i] = Mma<float>::run(vr[e][i], p[t][e], o[t][i]);
+                for (int t = 0; t < QT; ++t) o[t][i] = Mma<float>::run(vr[e][i / 4][i % 4], p[t][e], o[t][i]);
         request_v(j0 + NW * BN);
     }
     if (__any(odd)) {              // the values taken out, from the wave that had their tile
@@ -631,7 +635,7 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(AttnArgs a)
                 for (int i = 0; i < D / 16; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float v = V[(int64_t)k * a.vs + 16 * i + 4 * g + e];
+                        const float v = V[(int64_t)k * a.vs + 64 * (i / 4) + 16 * g + 4 * e + i % 4];
 #pragma unroll
                         for (int t = 0; t < QT; ++t)
                             if (k < seen[t] && !(fabsf(v) < __builtin_inff())) o[t][i][e] += v;
@@ -653,8 +657,13 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(AttnArgs a)
         for (int w = 0; w < NW; ++w) top = fmaxf(top, ml[w][0][16 * t + qi]);
         const float f = __builtin_amdgcn_exp2f(m[t] - (top == -__builtin_inff() ? 0.0f : top));
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-            *reinterpret_cast<f32x4 *>(&js.o[wave][(16 * t + qi) * (D + 4) + 16 * i + 4 * g]) = o[t][i] * f;
+        for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const f32x4 v = {o[t][4 * i][e] * f, o[t][4 * i + 1][e] * f, o[t][4 * i + 2][e] * f,
+                                 o[t][4 * i + 3][e] * f};
+                *reinterpret_cast<f32x4 *>(&js.o[wave][(16 * t + qi) * (D + 4) + 64 * i + 16 * g + 4 * e]) = v;
+            }
     }
     __syncthreads();
     join_waves<float, D, NQ, NW>(a, b, js.o, ml);
