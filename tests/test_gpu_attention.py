@@ -133,6 +133,33 @@ def test_hidden_rows_do_not_matter(dt, D, bad, H, Hkv):
     assert not np.isfinite(got[100 + 40:, :, 3]).any()
 
 
+# enough heads for a whole block of queries each (with fewer, waves share the keys): blocks
+# of 1, 2 and 4 heads of a group, and of groups of 5
+MOST = [(160, 160), (160, 80), (160, 40), (160, 32)]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("-inf")])
+@pytest.mark.parametrize("H,Hkv", MOST)
+def test_hidden_rows_do_not_matter_to_most_heads(D, bad, H, Hkv):
+    test_hidden_rows_do_not_matter(BF, D, bad, H, Hkv)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H,Hkv", MOST)
+def test_most_heads(D, H, Hkv):
+    run(20 + D, [40, 1, 130], [104, 200, 131], H, Hkv, D, BF)
+    run(21 + D, [9, 33, 0, 20, 2], [40, 33, 5, 10, 0], H, Hkv, D, BF)
+    run(22 + D, [70, 3, 0, 5], [33, 129, 7, 0], H, Hkv, D, BF, causal=False)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,klens", [([1100], [1100]), ([40, 33, 2, 1], [900, 33, 1500, 1]), ([33], [1300])])
+def test_few_heads_on_long_keys(D, lens, klens):
+    """Several rounds of key tiles for the waves that share them, past a queries' tile end too."""
+    run(30 + D, lens, klens, 4, 2, D, BF)
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_rows_of_a_fused_projection(dt):
     g = torch.Generator().manual_seed(8)
