@@ -275,6 +275,7 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(
     const int k1 = L - k0 < part.span ? L : k0 + part.span;
     if (k0 >= k1 && split > 0) return;         // (the join reads no such split)
     const int32_t *const tab = table + (int64_t)r * max_pages;
+    const int shared = L - T + 1;              // keys that all of the request's tokens see
 
     // q of row n16 of every row tile, and how many keys the row sees
     bf16x8 qf[NRT][STEPS];
@@ -287,7 +288,7 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(
 #pragma unroll
         for (int s = 0; s < STEPS; ++s)
             qf[m][s] = *reinterpret_cast<const bf16x8 *>(qp + dim_of<E4M3>(s, g));
-        sees[m] = row < rows ? L - T + 1 + t : 0;
+        sees[m] = row < rows ? shared + t : 0;
     }
 
     const char *const kc = static_cast<const char *>(c.k), *const vc = static_cast<const char *>(c.v);
@@ -361,7 +362,7 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(
         // some of the request's tokens do not see all of its keys, a masked weight is
         // zero but zero times an infinity is not: non-finite values stay out of the
         // product and are added below to the rows that see them.
-        const bool partial = key + 32 > L - T + 1;
+        const bool partial = key + 32 > shared;
 #pragma unroll
         for (int l = 0; l < TL::VL; ++l) {
             const int vr = l * (64 / TL::LPV) + lane / TL::LPV;
@@ -420,8 +421,9 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(
     }
 
     if (__any(odd)) {
-        // back to the rows that see them, from the wave that had their tile
-        for (int j = L - T + 1 > k0 ? L - T + 1 : k0; j < k1; ++j) {
+        // back to the rows that see them, from the wave that had their tile: values are taken
+        // out of whole tiles, so this starts with the first key of the tile that `shared` is in
+        for (int j = shared > k0 ? shared - (shared - k0) % 32 : k0; j < k1; ++j) {
             if (((j - k0) >> 5 & 3) != wave) continue;
             const int64_t b = base_of(j & ~15);
             if (b < 0) continue;
