@@ -796,6 +796,8 @@ typedef struct {
  * context_lens[r] - T + 1 + t of them. A token that sees none gets zeros (lse
  * -infinity). A context is cut to max_pages * page_size tokens, and keys on
  * a page whose table entry lies outside [0, num_pages) are not seen.
+ * Products are on bf16 MFMA with float32 accumulation; a softmax weight goes
+ * into them in two bf16 parts that are off by at most 2^-16 of it together.
  *   q, out [R,T,H,D]; block_table [R,max_pages], context_lens [R] int32
  *   lse [R,T,H] float32 or NULL
  *   workspace   attn_decode_workspace_bytes(p) bytes, 16-byte aligned (NULL

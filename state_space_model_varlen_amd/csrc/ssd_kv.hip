@@ -379,7 +379,12 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(
                 *reinterpret_cast<u32x4 *>(to) = w;
         }
         wave_lds_sync();
-        bf16x8 pf[NRT];
+        // The matrix products take bf16. A weight goes in as its rounded value and what the
+        // rounding left: two products in place of one, on matrix units that are a twentieth
+        // busy (128 requests of 1 K to 4 K keys in 8 bits 151 -> 155 us, one of 32769 in bf16
+        // 33.5 -> 34.1), against an eighth bit rounded (a result's error 1.25 times its own
+        // rounding's).
+        bf16x8 pf[NRT], pr[NRT];
 #pragma unroll
         for (int m = 0; m < NRT; ++m) {
             float sc[8], top = -__builtin_inff();
@@ -403,6 +408,7 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(
                 const float p = __builtin_amdgcn_exp2f(sc[e] - ref);
                 sum[m] += p;
                 pf[m][e] = static_cast<bf16>(p);
+                pr[m][e] = static_cast<bf16>(p - to_f32(pf[m][e]));
             }
             if (__any(top > was))
 #pragma unroll
@@ -412,7 +418,8 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(
         for (int i = 0; i < DT; ++i) {
             const bf16x8 vf = mfma_frag_tr_split(vw, VP, 0, 16 * i, lane);
 #pragma unroll
-            for (int m = 0; m < NRT; ++m) o[m][i] = Mma<bf16>::run(vf, pf[m], o[m][i]);
+            for (int m = 0; m < NRT; ++m)
+                o[m][i] = Mma<bf16>::run(vf, pr[m], Mma<bf16>::run(vf, pf[m], o[m][i]));
         }
         wave_lds_sync();
         cur = next;
@@ -420,30 +427,57 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(
         b1 = n1;
     }
 
-    if (__any(odd)) {
-        // back to the rows that see them, from the wave that had their tile: values are taken
-        // out of whole tiles, so this starts with the first key of the tile that `shared` is in
-        for (int j = shared > k0 ? shared - (shared - k0) % 32 : k0; j < k1; ++j) {
-            if (((j - k0) >> 5 & 3) != wave) continue;
-            const int64_t b = base_of(j & ~15);
-            if (b < 0) continue;
-            const int64_t at = (b + (j & 15)) * D + 4 * g;
+    // Values that are not finite go back to the rows that see them, from the wave that had
+    // their tile: those taken out, from the tile that `shared` is in on; and all of them where
+    // a sum came out as NaN, because an infinity times a weight's remainder has either sign, or
+    // is NaN (8 bits hold no infinities).
+    bool lost = false;
+    if constexpr (!E4M3) {
+#pragma unroll
+        for (int m = 0; m < NRT; ++m)
+#pragma unroll
             for (int i = 0; i < DT; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float v;
-                    if constexpr (E4M3)
-                        v = (static_cast<const uint8_t *>(c.v)[at + 16 * i + e] & 0x7f) == 0x7f
-                                ? __builtin_nanf("") : 0.0f;
-                    else
-                        v = to_f32(static_cast<const bf16 *>(c.v)[at + 16 * i + e]);
-                    v = fabsf(v) < __builtin_inff() ? 0.0f : v;
+                for (int e = 0; e < 4; ++e) lost |= o[m][i][e] != o[m][i][e];
+        lost = __any(lost);
+    }
+    if (lost || __any(odd)) {
+        const int from = shared > k0 && !lost ? (shared - k0) / 32 * 32 : 0, mine = wave * 32;
+        const int first = k0 + mine + (from > mine ? (from - mine + 127) / 128 * 128 : 0);
+        for (int i = 0; i < DT; ++i) {
+            f32x4 back[NRT];
 #pragma unroll
-                    for (int k = 0; k < DT; ++k)
+            for (int m = 0; m < NRT; ++m) back[m] = zero4();
+            for (int half = first; half < k1; half += half & 16 ? 112 : 16) {
+                const int64_t b = base_of(half);
+                if (b < 0) continue;
+                const char *const row = vc + (b * D + 16 * i + 4 * g) * TL::EB;
+#pragma unroll 4
+                for (int u = 0; u < 16; ++u) {
+                    float v[4];
+                    if constexpr (E4M3) {
+                        const uint32_t w = *reinterpret_cast<const uint32_t *>(row + u * D);
 #pragma unroll
-                        for (int m = 0; m < NRT; ++m)
-                            if (k == i && j < sees[m]) o[m][k][e] += v;
+                        for (int e = 0; e < 4; ++e)
+                            v[e] = (w >> (8 * e) & 0x7f) == 0x7f ? __builtin_nanf("") : 0.0f;
+                    } else
+                        load4<bf16>(reinterpret_cast<const bf16 *>(row) + u * D, v);
+#pragma unroll
+                    for (int m = 0; m < NRT; ++m)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (half + u < sees[m] && !(fabsf(v[e]) < __builtin_inff())) back[m][e] += v[e];
                 }
+            }
+#pragma unroll
+            for (int k = 0; k < DT; ++k)
+#pragma unroll
+                for (int m = 0; m < NRT; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float was = o[m][k][e], v = back[m][e];
+                        if (k == i) o[m][k][e] = was != was && v != 0.0f ? v : was + v;
+                    }
         }
     }
 
