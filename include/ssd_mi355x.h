@@ -713,7 +713,7 @@ typedef struct {
     int32_t dtype;     /* ssd_dtype of q, k, v, out (SSD_F32 or SSD_BF16) */
     int32_t causal;    /* 1: query i of Lq sees keys 0 .. i + Lk - Lq; 0: all keys */
     float scale;       /* of the scores, positive (0: 1 / sqrt(headdim)) */
-    int32_t reserved;  /* 0 */
+    int32_t bf16_weights; /* 1: softmax weights may be rounded to bf16; 0: they are not */
     int64_t q_stride, k_stride, v_stride, o_stride;
 } attn_problem;
 
@@ -728,8 +728,11 @@ typedef struct {
  *   q, out [total_q,H,D]; k, v [total_k,nkv_heads,D]; lse [total_q,H] float32
  *   (log of the sum of exponentials) or NULL
  *   cu_seqlens_q, cu_seqlens_k [S+1] int32
- * bf16: products on bf16 MFMA with float32 accumulation; the probabilities
- * (before their division by the sum) are rounded to bf16. q, k, v, out and
+ * bf16: products on bf16 MFMA with float32 accumulation; a softmax weight
+ * (before its division by the sum) goes into them in two bf16 parts that are
+ * off by at most 2^-16 of it together. With bf16_weights = 1 it may be its
+ * rounded value alone, 2^-8: a quarter less time on long prompts for an error
+ * about 1.25 times that of the result's own rounding. q, k, v, out and
  * their strides must keep every row 16-byte aligned (SSD_ERR_ALIGN).
  */
 int attention_varlen(const attn_problem *p, const void *q, const void *k, const void *v,

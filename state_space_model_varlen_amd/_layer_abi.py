@@ -25,7 +25,7 @@ class scan_problem(ctypes.Structure):
 class attn_problem(ctypes.Structure):
     _fields_ = [(n, _i32) for n in (
         "total_q", "total_k", "num_seqs", "nheads", "nkv_heads", "headdim", "dtype",
-        "causal")] + [("scale", _f), ("reserved", _i32)] + [(n, _i64) for n in (
+        "causal")] + [("scale", _f), ("bf16_weights", _i32)] + [(n, _i64) for n in (
             "q_stride", "k_stride", "v_stride", "o_stride")]
 
 

@@ -85,6 +85,70 @@ __device__ __forceinline__ bool take_out(u32x4 &w, bf16) {
     }
     return any;
 }
+// Whether an element of a query's sum of values came out as NaN for no fault of its
+// weights. (A weight goes into the products as two parts, its rounded value and the
+// rest; an infinity times the rest has either sign, or is NaN.)
+template <int D> __device__ __forceinline__ bool lost_sums(const f32x16 (&o)[D / 32], float sum) {
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) nan |= o[i][e] != o[i][e];
+    return __any(nan && sum == sum);
+}
+// Adds the non-finite values among keys from .. kend - 1 (whole tiles of 32 that the
+// wave answers for) to the sums of the queries that see them; a sum that is NaN is
+// replaced by theirs. A tile is looked through as it lies first: most have none.
+template <int D, typename F>
+__device__ __forceinline__ void give_back(const bf16 *V, int64_t vs, int from, int kend, int seen,
+                                          f32x16 (&o)[D / 32], F mine) {
+    constexpr int LPV = D / 8, RV = 64 / LPV;                      // lanes a row, rows a load
+    const int lane = threadIdx.x & 63, hf = lane >> 5;
+    f32x16 back[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) back[i][e] = 0.0f;
+    for (int j = from; j < kend; j += 32) {
+        if (!mine(j)) continue;
+        bool any = false;
+#pragma unroll
+        for (int r = 0; r < 32; r += RV) {
+            const int k = j + r + lane / LPV;
+            u32x4 w = *reinterpret_cast<const u32x4 *>(V + (int64_t)(k < kend ? k : kend - 1) * vs +
+                                                       lane % LPV * 8);
+            any |= take_out(w, bf16());
+        }
+        if (!__any(any)) continue;
+        const int end = j + 32 < kend ? j + 32 : kend;
+        for (int k = j; k < end; ++k)
+            if (k < seen)
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        float v[4];
+                        load4<bf16>(V + (int64_t)k * vs + 32 * i + 2 * e + 4 * hf, v);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            if (!(fabsf(v[u]) < __builtin_inff())) back[i][e + u] += v[u];
+                    }
+        bool more = false;                                         // (all NaN: no need to go on)
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) more |= o[i][e] == o[i][e] || back[i][e] == back[i][e];
+        if (!__any(more)) break;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float was = o[i][e], v = back[i][e];
+            o[i][e] = was != was && v != 0.0f ? v : was + v;
+        }
+}
+
 // bf16 heads of D. A block of 4 waves takes 32 queries of one head a wave: of HPB
 // heads that share a key head, BM = 128 / HPB queries of each (fewer queries
 // mean less work beyond the diagonal, and short sequences fill the block),
@@ -92,21 +156,27 @@ __device__ __forceinline__ bool take_out(u32x4 &w, bf16) {
 //
 // Scores are formed transposed, S^T = K Q^T (keys x queries), so that a lane
 // holds 16 of every 32 scores of one query (its partner 32 lanes away the
-// rest): the row maximum and the rescaling are per lane, and the rounded
-// probabilities are, as they stand, the operand of O^T = V^T P^T. The values'
+// rest): the row maximum and the rescaling are per lane, and the weights, in
+// bf16, are as they stand the operand of O^T = V^T P^T. The values'
 // transposed operand comes through the LDS transpose read. Row pitches keep
 // both kinds of reads free of bank conflicts (K: 4 dwords past a multiple of
 // 64 dwords; V: 16 past).
 //
-// The matrix and the vector work of a step are about equally long (D = 128: 512
-// cycles of MFMA, 360 of exponentials, maxima and sums), and a wave that takes
-// one after the other leaves each unit idle half the time. So a step forms the
-// scores of the step after it, adds the values of the step before it, and does
-// the softmax of its own: three pieces that do not depend on one another and
-// are issued interleaved. Keys are therefore needed a step early and values a
-// step late; with two buffers of each, one barrier a tile, between its steps,
-// lets K of the next tile and V of this one be written before it and used
-// after it.
+// The products take bf16, so a weight goes into the second one as its rounded value
+// and, rounded in turn, what that left (off by 2^-16 of it: the result's error is its
+// own rounding's; with the rounded value alone, BF16W, a caller's choice, it is 1.25
+// times that, and 16384 tokens of 32 heads of 128 take 2181 us instead of 2938).
+//
+// The matrix and the vector work of a step are about equally long (D = 128: 768
+// cycles of MFMA, 512 with BF16W; 520 and 360 of exponentials, maxima, sums and
+// parts), and a wave that takes one after the other leaves each unit idle half the
+// time. So a step forms the scores of the step after it, adds the values of the step
+// before it, and does the softmax of its own: three pieces that do not depend on one
+// another and are issued interleaved. Keys are therefore needed a step early and
+// values a step late; with two buffers of each, one barrier a tile, between its
+// steps, lets K of the next tile and V of this one be written before it and used
+// after it. Heads of 128 take 250 registers (with BF16W 256, and 16 bytes of scratch),
+// two waves a SIMD; heads of 64 161, three.
 template <int D> struct AttnSmem {
     static constexpr int BN = 64, KP = D + 8, VP = D + 32;
     __align__(16) bf16 k[2][BN * KP];
@@ -114,7 +184,7 @@ template <int D> struct AttnSmem {
     int hidden;                      // a partly masked tile has non-finite values
 };
 
-template <int D, int HPB>
+template <int D, int HPB, bool BF16W>
 __global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a)
 {
     typedef AttnSmem<D> SM;
@@ -191,7 +261,7 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a)
     // lanes of a half hold the keys 4 hf + v and 8 + 4 hf + v that their weights belong to
     const int jl = lane & 15;
     const int vo = (4 * hf + (jl >> 2)) * VP + ((lane >> 4) & 1) * 16 + 4 * (jl & 3);
-    auto add_values = [&](int buf, int sub, const bf16x8 (&p)[2]) __attribute__((always_inline)) {
+    auto add_values = [&](int buf, int sub, const bf16x8 (&p)[2], const bf16x8 (&r)[2]) __attribute__((always_inline)) {
         const bf16 *const vl = &sm.v[buf][sub * 32 * VP + vo];
 #pragma unroll
         for (int w = 0; w < 2; ++w)
@@ -203,11 +273,14 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a)
                 const v8i16 both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
                 o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, both), p[w],
                                                                o[i], 0, 0, 0);
+                if constexpr (!BF16W)
+                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, both), r[w],
+                                                                   o[i], 0, 0, 0);
             }
     };
     // softmax weights of the 32 keys from key j on; returns what the result so far has
     // to be scaled by, and whether any lane's maximum rose
-    auto weights = [&](f32x16 &s, int j, bool masked, bf16x8 (&p)[2], bool &rose) __attribute__((always_inline)) {
+    auto weights = [&](f32x16 &s, int j, bool masked, bf16x8 (&p)[2], bf16x8 (&r)[2], bool &rose) __attribute__((always_inline)) {
         if (masked) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
@@ -228,14 +301,16 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a)
             const float w = __builtin_amdgcn_exp2f(s[e] * a.scale2 - ref);
             sum += w;
             p[e >> 3][e & 7] = static_cast<bf16>(w);
+            if constexpr (!BF16W) r[e >> 3][e & 7] = static_cast<bf16>(w - to_f32(p[e >> 3][e & 7]));
         }
         rose = top > was;
         return f;
     };
     // (the empty statements keep the weights in front of the branch, where the matrix
     // products they run beside are, and the products with f behind it)
-    auto rescale = [&](float f, bool rose, bf16x8 (&p)[2]) __attribute__((always_inline)) {
+    auto rescale = [&](float f, bool rose, bf16x8 (&p)[2], bf16x8 (&r)[2]) __attribute__((always_inline)) {
         asm volatile("" : "+v"(p[0]), "+v"(p[1]), "+v"(sum));
+        if constexpr (!BF16W) asm volatile("" : "+v"(r[0]), "+v"(r[1]));
         if (__any(rose)) {
             asm volatile("" : "+v"(f));
 #pragma unroll
@@ -244,13 +319,13 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a)
     };
     const int tiles = (kend + BN - 1) / BN;
     f32x16 s0, s1;
-    bf16x8 p0[2], p1[2];
+    bf16x8 p0[2], p1[2], r0[2], r1[2];
     if (tid == 0) sm.hidden = 0;
     // (the values "before the first tile": zeros with zero weights)
 #pragma unroll
     for (int w = 0; w < 2; ++w)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p1[w][e] = static_cast<bf16>(0.0f);
+        for (int e = 0; e < 8; ++e) p1[w][e] = r1[w][e] = static_cast<bf16>(0.0f);
     for (int i = tid; i < BN * VP / 8; i += 256) reinterpret_cast<u32x4 *>(sm.v[1])[i] = u32x4{0, 0, 0, 0};
     if (tiles > 0) {
         request(kr, K, (int)a.ks, 0);
@@ -265,40 +340,31 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a)
         const int j = t * BN, buf = t & 1;
         bool rose;
         s1 = scores(buf, 1);
-        add_values(buf ^ 1, 1, p1);
-        float f = weights(s0, j, masked, p0, rose);
-        rescale(f, rose, p0);
+        add_values(buf ^ 1, 1, p1, r1);
+        float f = weights(s0, j, masked, p0, r0, rose);
+        rescale(f, rose, p0, r0);
         stage_k(t + 1);
         stage_v(t);
         __syncthreads();
         request(kr, K, (int)a.ks, j + 2 * BN);
         request(vr, V, (int)a.vs, j + BN);
         s0 = scores(buf ^ 1, 0);
-        add_values(buf, 0, p0);
-        f = weights(s1, j + 32, masked, p1, rose);
-        rescale(f, rose, p1);
+        add_values(buf, 0, p0, r0);
+        f = weights(s1, j + 32, masked, p1, r1, rose);
+        rescale(f, rose, p1, r1);
     };
     const int open = kfull / BN < tiles ? kfull / BN : tiles;     // tiles without a mask
     for (int t = 0; t < open; ++t) tile(t, std::false_type());
     for (int t = open; t < tiles; ++t) tile(t, std::true_type());
     if (tiles > 0) {
         const int t = tiles - 1;
-        add_values(t & 1, 1, p1);
-        // the values taken out, for the queries that see them
-        if (sm.hidden)
-            for (int k = open * BN; k < kend; ++k)
-                if (k < seen)
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float v = to_f32(V[(int64_t)k * a.vs + 32 * i + 8 * (e >> 2) +
-                                                     4 * hf + (e & 3)]);
-                            if (!(fabsf(v) < __builtin_inff())) o[i][e] += v;
-                        }
+        add_values(t & 1, 1, p1, r1);
     }
-
     sum = across32(sum, added);
+    const bool lost = !BF16W && lost_sums<D>(o, sum);
+    if (lost || sm.hidden)
+        give_back<D>(V, a.vs, lost ? 0 : open * BN, kend, seen, o, [](int) { return true; });
+
     if (q < b.lq && head < b.head_end) {
         // (a NaN sum is passed on; a row without keys gets zeros)
         const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
@@ -446,12 +512,13 @@ __global__ __launch_bounds__(512, 1) void attn_split_kernel(AttnArgs a)
         m = fmaxf(m, top);
         const float ref = m == -__builtin_inff() ? 0.0f : m, f = __builtin_amdgcn_exp2f(was - ref);
         sum *= f;
-        bf16x8 p[2];
+        bf16x8 p[2], r[2];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
             const float w = __builtin_amdgcn_exp2f(s[e] * a.scale2 - ref);
             sum += w;
             p[e >> 3][e & 7] = static_cast<bf16>(w);
+            r[e >> 3][e & 7] = static_cast<bf16>(w - to_f32(p[e >> 3][e & 7]));
         }
         if (__any(top > was)) {
 #pragma unroll
@@ -468,21 +535,16 @@ __global__ __launch_bounds__(512, 1) void attn_split_kernel(AttnArgs a)
                 const v8i16 both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
                 o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, both), p[w],
                                                                o[i], 0, 0, 0);
+                o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, both), r[w],
+                                                               o[i], 0, 0, 0);
             }
         wave_lds_sync();
     }
-    if (__any(odd)) {              // the values taken out, from the wave that had their tile
-        for (int k = kopen / BN * BN; k < kend; ++k)
-            if (k / BN % NW == wave && k < seen)
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float v = to_f32(V[(int64_t)k * a.vs + 32 * i + 8 * (e >> 2) + 4 * hf + (e & 3)]);
-                        if (!(fabsf(v) < __builtin_inff())) o[i][e] += v;
-                    }
-    }
     sum = across32(sum, added);
+    const bool lost = lost_sums<D>(o, sum);
+    if (lost || __any(odd))        // (from the wave that had the tile)
+        give_back<D>(V, a.vs, lost ? 0 : kopen / BN * BN, kend, seen, o,
+                     [&](int j) { return j / BN % NW == wave; });
     if (hf == 0) {
         ml[wave][0][qi] = m;
         ml[wave][1][qi] = sum;
@@ -679,40 +741,47 @@ void launch_attn(const AttnDims &d, const void *q, const void *k, const void *v,
     const int64_t Tq = d.Tq, S = d.S, H = d.H, group = H / d.Hkv;
     // bf16: the waves of a block on 4 or 2 heads of a group where that divides it, or
     // where sequences are too short to fill 128 queries of one (32 sequences of 32
-    // queries on 4224 cached keys: 32 heads of 128 on 8 key heads 325 us with one head
-    // a block, 150 us with 4; 40 heads of 64, five to a key head, 255 and 131 us)
+    // queries on 4224 cached keys: 32 heads of 128 on 8 key heads 409 us with one head
+    // a block, 172 us with 4; 40 heads of 64, five to a key head, 295 and 151 us)
     const int hpb = group % 4 == 0 || (group > 2 && Tq <= 40 * S) ? 4 : (group % 2 == 0 ? 2 : 1);
     // ... or sharing the keys of 32 queries of one head, where there are no blocks for
-    // most of the 256 CUs (without and with, us: 1523 tokens, 2 heads, 24 blocks: 25 and
-    // 12; 11 prompts of 981 on 1352 keys, 8 heads on 2, 82 blocks: 36 and 17; 120 on 106,
-    // 40 heads on 8, 128 blocks: 10 and 8; 512 tokens, 32 heads on 8, 136 blocks: 19 and
-    // 17; 9 prompts of 950 on 308, 16 heads on 4, 152 blocks: 19 and 20), or barely and
-    // the keys are long, the more blocks the longer. Of several sequences one is taken
-    // to be twice the mean: the lengths are not known here, and the cost of a long one
-    // missed is the greater (15 prompts of 4789 on 4321, the longest on 4134, 4 heads,
-    // 164 blocks: 90 and 35; 4 of 700, 8 heads, 200 blocks: 22 and 27; 1024 tokens, 32
-    // heads on 8, 264 blocks: 30 and 39; 4096, 8 heads, 264 blocks: 94 and 81; 3000, 12
-    // heads, 288 blocks: 69 and 74)
+    // most of the 256 CUs, or not for two rounds of them and the keys are long, the more
+    // blocks the longer (heads of 128, without and with, us: 1523 tokens, 2 heads, 24
+    // blocks: 51 and 19; 512 tokens, 32 heads on 8, 136 blocks: 23 and 19; 1500, 12
+    // heads, 144: 53 and 35; 1100, 32 on 8, 280: 42 and 50; 3000, 12 heads, 288: 96 and
+    // 84; 4096, 10 heads, 330: 126 and 115; 6144, 8 heads, 392: 185 and 175; 4000, 16 on
+    // 4, 504: 136 and 167). With rounded weights, which the shared form does not take,
+    // the other one takes a quarter less and the limit is lower (3000, 12 heads: 70 and 84). Of
+    // several sequences one is taken to be twice the mean: the lengths are not known
+    // here, and the cost of a long one missed is the greater (15 prompts of 4789 on 9321,
+    // one of them on 8000, 4 heads, 208 blocks: 221 and 61; 11 prompts of 89 on 123, 8
+    // heads on 2, 82 blocks: 14 and 16)
     const int64_t blocks = (Tq * hpb / 128 + S) * d.Hkv * ((group + hpb - 1) / hpb);
     const int64_t longest = S == 1 ? d.Tk : 2 * (int64_t)d.Tk / S;
-    const bool split = blocks <= 144 || (blocks <= 272 && longest > 4 * blocks);
+    const bool split = blocks <= 144 || (blocks <= (d.bf16w ? 272 : 400) && longest > 4 * blocks);
     // float: two tiles of queries share the keys once there are enough of them
     const bool two = (Tq / 32 + S) * H >= 512;
 #define SSD_ATTN(KERNEL, BM, HEADS, THREADS) \
     hipLaunchKernelGGL((KERNEL), dim3((unsigned)((Tq / (BM) + S) * (HEADS))), dim3(THREADS), 0, st, a)
+#define SSD_ATTN_W(DD, BF16W)                                                                 \
+    do {                                                                                      \
+        if (hpb == 4)                                                                         \
+            SSD_ATTN((attn_kernel<DD, 4, BF16W>), 32, d.Hkv * ((group + 3) / 4), 256);        \
+        else if (hpb == 2) SSD_ATTN((attn_kernel<DD, 2, BF16W>), 64, H / 2, 256);             \
+        else SSD_ATTN((attn_kernel<DD, 1, BF16W>), 128, H, 256);                              \
+    } while (0)
 #define SSD_ATTN_D(DD)                                                                        \
     do {                                                                                      \
         if (d.bf16 && split) SSD_ATTN(attn_split_kernel<DD>, 32, H, 512);                     \
-        else if (d.bf16 && hpb == 4)                                                          \
-            SSD_ATTN((attn_kernel<DD, 4>), 32, d.Hkv * ((group + 3) / 4), 256);               \
-        else if (d.bf16 && hpb == 2) SSD_ATTN((attn_kernel<DD, 2>), 64, H / 2, 256);          \
-        else if (d.bf16) SSD_ATTN((attn_kernel<DD, 1>), 128, H, 256);                         \
+        else if (d.bf16 && d.bf16w) SSD_ATTN_W(DD, true);                                     \
+        else if (d.bf16) SSD_ATTN_W(DD, false);                                               \
         else if (two) SSD_ATTN((attn_f32_kernel<DD, 2>), 32, H, 256);                         \
         else SSD_ATTN((attn_f32_kernel<DD, 1>), 16, H, 256);                                  \
     } while (0)
     if (d.D == 128) SSD_ATTN_D(128);
     else SSD_ATTN_D(64);
 #undef SSD_ATTN_D
+#undef SSD_ATTN_W
 #undef SSD_ATTN
 }
 

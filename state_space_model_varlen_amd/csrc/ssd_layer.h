@@ -46,7 +46,7 @@ void launch_scan_update(const ScanDims &d, const ScanArgs &a, void *inter, void 
 
 struct AttnDims {
     int Tq, Tk, S, H, Hkv, D;
-    bool bf16, causal;
+    bool bf16, causal, bf16w;
     float scale;
     int64_t qs, ks, vs, os;
 };

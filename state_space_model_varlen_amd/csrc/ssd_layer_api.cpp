@@ -306,6 +306,7 @@ int attention_varlen(const attn_problem *p, const void *q, const void *k, const 
     if (p->num_seqs == 0 && (p->total_q > 0 || p->total_k > 0)) return SSD_ERR_SHAPE;
     if (!float_ok(p->dtype)) return SSD_ERR_DTYPE;
     if (!headdim_ok(p->headdim)) return SSD_ERR_UNSUPPORTED;
+    if (p->bf16_weights != 0 && p->bf16_weights != 1) return SSD_ERR_UNSUPPORTED;
     // grid limit: query tiles of at least 16 rows, one more a sequence, times heads
     if (((int64_t)p->total_q / 16 + p->num_seqs) * p->nheads > 0x7fffffffLL)
         return SSD_ERR_UNSUPPORTED;
@@ -331,6 +332,7 @@ int attention_varlen(const attn_problem *p, const void *q, const void *k, const 
     d.D = p->headdim;
     d.bf16 = p->dtype == SSD_BF16;
     d.causal = p->causal != 0;
+    d.bf16w = p->bf16_weights != 0;
     ssd::launch_attn(d, q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, stream);
     return launch_status();
 }

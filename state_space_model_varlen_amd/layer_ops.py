@@ -265,12 +265,13 @@ def selective_scan_update(p: scan_problem, x, dt, A, B, C, D, z, dt_transform, s
 
 def make_attn_problem(total_q: int, total_k: int, num_seqs: int, nheads: int, nkv_heads: int,
                       headdim: int, dtype: torch.dtype, causal: bool = True,
-                      scale: float = 0.0) -> attn_problem:
-    """scale 0: 1 / sqrt(headdim)."""
+                      scale: float = 0.0, bf16_weights: bool = False) -> attn_problem:
+    """scale 0: 1 / sqrt(headdim). bf16_weights: softmax weights may be rounded to bf16."""
     p = attn_problem()
     p.total_q, p.total_k, p.num_seqs = int(total_q), int(total_k), int(num_seqs)
     p.nheads, p.nkv_heads, p.headdim = int(nheads), int(nkv_heads), int(headdim)
     p.dtype, p.causal, p.scale = _DT[dtype], int(bool(causal)), float(scale or 0.0)
+    p.bf16_weights = int(bool(bf16_weights))
     return p
 
 

@@ -234,3 +234,10 @@ def test_binding_checks_tensors():
     with pytest.raises(ValueError, match="no scales"):
         q = ssd.make_kv_cache_problem(1, 64, 1, 64, BF, BF)
         ssd.layer_ops._kv_ptrs(q, x, x, x, x)
+
+
+def test_attention_weights_choice():
+    assert call_attn(attn(bf16_weights=2)) == UNSUP and call_attn(attn(bf16_weights=-1)) == UNSUP
+    assert ssd.make_attn_problem(1, 1, 1, 1, 1, 64, BF).bf16_weights == 0
+    assert ssd.make_attn_problem(1, 1, 1, 1, 1, 64, BF, bf16_weights=True).bf16_weights == 1
+    assert ctypes.sizeof(ssd.attn_problem) == 72       # (the field took a reserved one's place)
