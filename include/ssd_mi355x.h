@@ -674,7 +674,9 @@ typedef struct {
  * in ssd_state_passing: snapshot semantics, skipped bad slots, zero-length
  * sequences written back.
  *   x, dt, z, y [T,C]; B, C [T,G,N]; A [C,N], D [C] float32 (D may be NULL)
- *   dt_transform     NULL: dt as given; else dt is raw and dt_bias is [C]
+ *   dt_transform     NULL: dt as given; else dt is raw and dt_bias is [C] (a NaN
+ *                    stays NaN, as everywhere in this operator; the SSD scan's
+ *                    clamp makes it dt_min)
  *   state_cache      [num_slots,C,N] state_dtype (round to nearest even)
  *   workspace        selective_scan_workspace_bytes(p) bytes, 16-byte aligned
  *                    (NULL when that is 0)

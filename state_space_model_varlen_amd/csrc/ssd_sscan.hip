@@ -35,8 +35,9 @@ __device__ __forceinline__ float softplus(float v) {
     p = p * q + 2.0f;
     return fmaxf(v, 0.0f) + p * s;
 }
+// (a NaN stays one: the median instruction would turn it into a bound)
 __device__ __forceinline__ float transformed(const DtTf &tf, float raw, float bias) {
-    return __builtin_amdgcn_fmed3f(softplus(raw + bias), tf.lo, tf.hi);
+    return __builtin_elementwise_minimum(__builtin_elementwise_maximum(softplus(raw + bias), tf.lo), tf.hi);
 }
 __device__ __forceinline__ float step_size(const DtTf &tf, float raw, float bias) {
     return tf.on ? transformed(tf, raw, bias) : raw;
