@@ -272,6 +272,9 @@ __global__ __launch_bounds__(256) void scan_kernel(
 #pragma unroll
             for (int m = 0; m < GROUPS; ++m)
                 if (t0 + m * L + j0 >= len) dt[m] = 0.0f;
+            // (also where A is -infinity, whose product with 0 is NaN)
+#pragma unroll
+            for (int i = 0; i < SPL; ++i) A2[i] = __builtin_elementwise_maximum(A2[i], -3.4e38f);
         }
         __syncthreads();
         if (t0 + ST < len) request(t0 + ST);

@@ -59,3 +59,22 @@ def test_scan_update_of_a_nan_step(R, T):
     assert np.isnan(want).any()
     same(y, want, ymag, T, F32, "y")
     same(inter, st, smag, T, F32, "states")
+
+
+@pytest.mark.parametrize("lens,C,N", [([40, 1, 33, 64], 48, 16), ([3 + i % 9 for i in range(40)], 900, 32),
+                                      ([1030], 40, 16), ([256], 40, 16)])
+def test_scan_of_states_that_decay_at_once(lens, C, N):
+    """A = -infinity: the state holds its last token alone, also where a sequence ends inside the
+    kernel's stage of tokens."""
+    m = make(23, lens, C, N, 1, F32, F32)
+    m["A"][5], m["A"][:, 2] = -float("inf"), -float("inf")
+    d = dev(m)
+    p = ssd.make_scan_problem(m["T"], m["S"], C, N, 1, m["S"] + 2, F32, F32)
+    tf = ssd.make_dt_transform(d["bias"], 0.0, 1e30)
+    y, cache = torch.full((m["T"], C), 7.0, device=DEV), d["cache"].clone()
+    ssd.selective_scan_varlen(p, d["x"], d["dt"], d["A"], d["B"], d["C_"], d["D"], d["z"], tf, d["cu"],
+                              cache, d["idx"], d["has"], y, ssd.alloc_scan_workspace(p, DEV))
+    want, _, left, ymag, _, cmag = ol.scan(m["x"], m["dt"], m["A"], m["B"], m["C_"], m["D"], m["z"],
+                                           m["cu"], m["cache"], m["idx"], m["has"], m["bias"], 0.0, 1e30)
+    same(y, want, ymag, max(lens), F32, "y")
+    same(cache, left, cmag, max(lens), F32, "cache")
