@@ -683,6 +683,9 @@ typedef struct {
  * state_cache, A and workspace must be 16-byte aligned.
  */
 size_t selective_scan_workspace_bytes(const scan_problem *p);
+/* (for profiles and tests: how the prompt form runs p, its lanes a channel and
+ * segments; "" for a problem that it refuses) */
+const char *selective_scan_varlen_kernel(const scan_problem *p);
 int selective_scan_varlen(const scan_problem *p, const void *x, const void *dt, const float *A,
                           const void *B, const void *C, const float *D, const void *z,
                           const ssd_dt_transform *dt_transform, const int32_t *cu_seqlens,
@@ -737,6 +740,8 @@ typedef struct {
  * about 1.25 times that of the result's own rounding. q, k, v, out and
  * their strides must keep every row 16-byte aligned (SSD_ERR_ALIGN).
  */
+/* (for profiles and tests: the kernel that runs p; "" for a problem refused) */
+const char *attention_varlen_kernel(const attn_problem *p);
 int attention_varlen(const attn_problem *p, const void *q, const void *k, const void *v,
                      const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, void *out,
                      float *lse, void *stream);

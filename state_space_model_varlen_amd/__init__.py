@@ -739,7 +739,8 @@ def alloc_replay_rings(p: ssu_problem, ring_len: int, device="cuda") -> dict:
 
 from .layer_ops import (  # noqa: E402,F401
     ACT_NONE, ACT_SILU, alloc_attn_decode_workspace, alloc_kv_cache, alloc_scan_workspace,
-    attention_decode, attention_varlen, attn_decode_workspace_bytes, causal_conv1d_commit,
-    causal_conv1d_update, causal_conv1d_varlen, kv_cache_load, kv_cache_store,
+    attention_decode, attention_varlen, attention_varlen_kernel, attn_decode_workspace_bytes,
+    causal_conv1d_commit, causal_conv1d_update, causal_conv1d_varlen, kv_cache_load, kv_cache_store,
     make_attn_decode_problem, make_attn_problem, make_conv_problem, make_kv_cache_problem,
-    make_scan_problem, selective_scan_update, selective_scan_varlen, selective_scan_workspace_bytes)
+    make_scan_problem, selective_scan_update, selective_scan_varlen, selective_scan_varlen_kernel,
+    selective_scan_workspace_bytes)

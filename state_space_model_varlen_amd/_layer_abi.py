@@ -49,8 +49,10 @@ LAYER_SIGS = {
     "causal_conv1d_update": ([_cp] + [_vp] * 8 + [_i32, _vp], ctypes.c_int),
     "causal_conv1d_commit": ([_cp] + [_vp] * 5, ctypes.c_int),
     "selective_scan_workspace_bytes": ([_sp], _sz),
+    "selective_scan_varlen_kernel": ([_sp], ctypes.c_char_p),
     "selective_scan_varlen": ([_sp] + [_vp] * 14 + [_sz, _vp], ctypes.c_int),
     "selective_scan_update": ([_sp] + [_vp] * 13, ctypes.c_int),
+    "attention_varlen_kernel": ([_ap], ctypes.c_char_p),
     "attention_varlen": ([_ap] + [_vp] * 8, ctypes.c_int),
     "kv_cache_store": ([_kp, _i32] + [_vp] * 8, ctypes.c_int),
     "kv_cache_load": ([_kp, _i32, _i32, _i32] + [_vp] * 9, ctypes.c_int),

@@ -731,19 +731,22 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(AttnArgs a)
     join_waves<float, D, NQ, NW>(a, b, js.o, ml);
 }
 
-void launch_attn(const AttnDims &d, const void *q, const void *k, const void *v,
-                 const int32_t *cuq, const int32_t *cuk, void *out, float *lse, void *stream)
+// Which kernel a call runs.
+struct AttnPlan {
+    int hpb;      // bf16: heads of a group that a block takes
+    bool split;   // bf16: attn_split_kernel instead
+    bool two;     // float: two tiles of queries a block
+};
+static AttnPlan attn_plan(const AttnDims &d)
 {
-    if (d.S <= 0 || d.Tq <= 0) return;
-    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-    const AttnArgs a{q, k, v, cuq, cuk, out, lse, d.qs, d.ks, d.vs, d.os, d.Tq, d.Tk, d.S, d.H,
-                     d.Hkv, d.causal ? 1 : 0, d.scale * kLog2e};
+    AttnPlan p{1, false, false};
+    if (d.S <= 0 || d.Tq <= 0) return p;
     const int64_t Tq = d.Tq, S = d.S, H = d.H, group = H / d.Hkv;
     // bf16: the waves of a block on 4 or 2 heads of a group where that divides it, or
     // where sequences are too short to fill 128 queries of one (32 sequences of 32
     // queries on 4224 cached keys: 32 heads of 128 on 8 key heads 409 us with one head
     // a block, 172 us with 4; 40 heads of 64, five to a key head, 295 and 151 us)
-    const int hpb = group % 4 == 0 || (group > 2 && Tq <= 40 * S) ? 4 : (group % 2 == 0 ? 2 : 1);
+    p.hpb = group % 4 == 0 || (group > 2 && Tq <= 40 * S) ? 4 : (group % 2 == 0 ? 2 : 1);
     // ... or sharing the keys of 32 queries of one head, where there are no blocks for
     // most of the 256 CUs, or not for two rounds of them and the keys are long, the more
     // blocks the longer (heads of 128, without and with, us: 1523 tokens, 2 heads, 24
@@ -756,26 +759,54 @@ void launch_attn(const AttnDims &d, const void *q, const void *k, const void *v,
     // here, and the cost of a long one missed is the greater (15 prompts of 4789 on 9321,
     // one of them on 8000, 4 heads, 208 blocks: 221 and 61; 11 prompts of 89 on 123, 8
     // heads on 2, 82 blocks: 14 and 16)
-    const int64_t blocks = (Tq * hpb / 128 + S) * d.Hkv * ((group + hpb - 1) / hpb);
+    const int64_t blocks = (Tq * p.hpb / 128 + S) * d.Hkv * ((group + p.hpb - 1) / p.hpb);
     const int64_t longest = S == 1 ? d.Tk : 2 * (int64_t)d.Tk / S;
-    const bool split = blocks <= 144 || (blocks <= (d.bf16w ? 272 : 400) && longest > 4 * blocks);
+    p.split = blocks <= 144 || (blocks <= (d.bf16w ? 272 : 400) && longest > 4 * blocks);
     // float: two tiles of queries share the keys once there are enough of them
-    const bool two = (Tq / 32 + S) * H >= 512;
+    p.two = (Tq / 32 + S) * H >= 512;
+    return p;
+}
+
+const char *attn_kernel_name(const AttnDims &d)
+{
+    const AttnPlan p = attn_plan(d);
+    const int wide = d.D == 128;
+    if (!d.bf16) {
+        static const char *const f[2][2] = {{"attn_f32_kernel<64, 1>", "attn_f32_kernel<128, 1>"},
+                                            {"attn_f32_kernel<64, 2>", "attn_f32_kernel<128, 2>"}};
+        return f[p.two][wide];
+    }
+    if (p.split) return wide ? "attn_split_kernel<128>" : "attn_split_kernel<64>";
+    static const char *const b[3][2] = {{"attn_kernel<64, 1>", "attn_kernel<128, 1>"},
+                                        {"attn_kernel<64, 2>", "attn_kernel<128, 2>"},
+                                        {"attn_kernel<64, 4>", "attn_kernel<128, 4>"}};
+    return b[p.hpb / 2][wide];
+}
+
+void launch_attn(const AttnDims &d, const void *q, const void *k, const void *v,
+                 const int32_t *cuq, const int32_t *cuk, void *out, float *lse, void *stream)
+{
+    if (d.S <= 0 || d.Tq <= 0) return;
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    const AttnArgs a{q, k, v, cuq, cuk, out, lse, d.qs, d.ks, d.vs, d.os, d.Tq, d.Tk, d.S, d.H,
+                     d.Hkv, d.causal ? 1 : 0, d.scale * kLog2e};
+    const int64_t Tq = d.Tq, S = d.S, H = d.H, group = H / d.Hkv;
+    const AttnPlan p = attn_plan(d);
 #define SSD_ATTN(KERNEL, BM, HEADS, THREADS) \
     hipLaunchKernelGGL((KERNEL), dim3((unsigned)((Tq / (BM) + S) * (HEADS))), dim3(THREADS), 0, st, a)
 #define SSD_ATTN_W(DD, BF16W)                                                                 \
     do {                                                                                      \
-        if (hpb == 4)                                                                         \
+        if (p.hpb == 4)                                                                         \
             SSD_ATTN((attn_kernel<DD, 4, BF16W>), 32, d.Hkv * ((group + 3) / 4), 256);        \
-        else if (hpb == 2) SSD_ATTN((attn_kernel<DD, 2, BF16W>), 64, H / 2, 256);             \
+        else if (p.hpb == 2) SSD_ATTN((attn_kernel<DD, 2, BF16W>), 64, H / 2, 256);             \
         else SSD_ATTN((attn_kernel<DD, 1, BF16W>), 128, H, 256);                              \
     } while (0)
 #define SSD_ATTN_D(DD)                                                                        \
     do {                                                                                      \
-        if (d.bf16 && split) SSD_ATTN(attn_split_kernel<DD>, 32, H, 512);                     \
+        if (d.bf16 && p.split) SSD_ATTN(attn_split_kernel<DD>, 32, H, 512);                     \
         else if (d.bf16 && d.bf16w) SSD_ATTN_W(DD, true);                                     \
         else if (d.bf16) SSD_ATTN_W(DD, false);                                               \
-        else if (two) SSD_ATTN((attn_f32_kernel<DD, 2>), 32, H, 256);                         \
+        else if (p.two) SSD_ATTN((attn_f32_kernel<DD, 2>), 32, H, 256);                         \
         else SSD_ATTN((attn_f32_kernel<DD, 1>), 16, H, 256);                                  \
     } while (0)
     if (d.D == 128) SSD_ATTN_D(128);

@@ -41,6 +41,7 @@ struct ScanArgs {
     void *cache, *y;
 };
 size_t scan_workspace(const ScanDims &d);
+const char *scan_kernel_name(const ScanDims &d);
 void launch_scan(const ScanDims &d, const ScanArgs &a, void *workspace, void *stream);
 void launch_scan_update(const ScanDims &d, const ScanArgs &a, void *inter, void *stream);
 
@@ -50,6 +51,7 @@ struct AttnDims {
     float scale;
     int64_t qs, ks, vs, os;
 };
+const char *attn_kernel_name(const AttnDims &d);
 void launch_attn(const AttnDims &d, const void *q, const void *k, const void *v,
                  const int32_t *cuq, const int32_t *cuk, void *out, float *lse, void *stream);
 

@@ -154,6 +154,39 @@ bool scale_of(float given, int headdim, float *out)
     return std::isfinite(*out) && *out > 0.0f;
 }
 
+int attn_dims(const attn_problem *p, ssd::AttnDims *d)
+{
+    if (!p) return SSD_ERR_NULL;
+    if (p->total_q < 0 || p->total_k < 0 || p->num_seqs < 0 || p->nheads <= 0 ||
+        p->nkv_heads <= 0 || p->headdim <= 0)
+        return SSD_ERR_SHAPE;
+    if (p->nheads % p->nkv_heads != 0) return SSD_ERR_SHAPE;
+    if (p->num_seqs == 0 && (p->total_q > 0 || p->total_k > 0)) return SSD_ERR_SHAPE;
+    if (!float_ok(p->dtype)) return SSD_ERR_DTYPE;
+    if (!headdim_ok(p->headdim)) return SSD_ERR_UNSUPPORTED;
+    if (p->bf16_weights != 0 && p->bf16_weights != 1) return SSD_ERR_UNSUPPORTED;
+    // grid limit: query tiles of at least 16 rows, one more a sequence, times heads
+    if (((int64_t)p->total_q / 16 + p->num_seqs) * p->nheads > 0x7fffffffLL)
+        return SSD_ERR_UNSUPPORTED;
+    const int64_t qr = (int64_t)p->nheads * p->headdim, kr = (int64_t)p->nkv_heads * p->headdim;
+    if (!stride_of(p->q_stride, qr, &d->qs) || !stride_of(p->k_stride, kr, &d->ks) ||
+        !stride_of(p->v_stride, kr, &d->vs) || !stride_of(p->o_stride, qr, &d->os))
+        return SSD_ERR_SHAPE;
+    // a tile of up to 256 rows is addressed by 32-bit byte offsets
+    if (d->qs > (1 << 21) || d->ks > (1 << 21) || d->vs > (1 << 21)) return SSD_ERR_UNSUPPORTED;
+    if (!scale_of(p->scale, p->headdim, &d->scale)) return SSD_ERR_SHAPE;
+    d->Tq = p->total_q;
+    d->Tk = p->total_k;
+    d->S = p->num_seqs;
+    d->H = p->nheads;
+    d->Hkv = p->nkv_heads;
+    d->D = p->headdim;
+    d->bf16 = p->dtype == SSD_BF16;
+    d->causal = p->causal != 0;
+    d->bf16w = p->bf16_weights != 0;
+    return SSD_OK;
+}
+
 int kv_dims(const kv_cache_problem *p, ssd::KvDims *d)
 {
     if (!p) return SSD_ERR_NULL;
@@ -252,6 +285,12 @@ size_t selective_scan_workspace_bytes(const scan_problem *p)
     return scan_dims(p, false, nullptr, &d) ? 0 : ssd::scan_workspace(d);
 }
 
+const char *selective_scan_varlen_kernel(const scan_problem *p)
+{
+    ssd::ScanDims d;
+    return scan_dims(p, false, nullptr, &d) ? "" : ssd::scan_kernel_name(d);
+}
+
 int selective_scan_varlen(const scan_problem *p, const void *x, const void *dt, const float *A,
                           const void *B, const void *C, const float *D, const void *z,
                           const ssd_dt_transform *dt_transform, const int32_t *cu_seqlens,
@@ -294,45 +333,25 @@ int selective_scan_update(const scan_problem *p, const void *x, const void *dt, 
     return launch_status();
 }
 
+const char *attention_varlen_kernel(const attn_problem *p)
+{
+    ssd::AttnDims d;
+    return attn_dims(p, &d) ? "" : ssd::attn_kernel_name(d);
+}
+
 int attention_varlen(const attn_problem *p, const void *q, const void *k, const void *v,
                      const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, void *out,
                      float *lse, void *stream)
 {
-    if (!p) return SSD_ERR_NULL;
-    if (p->total_q < 0 || p->total_k < 0 || p->num_seqs < 0 || p->nheads <= 0 ||
-        p->nkv_heads <= 0 || p->headdim <= 0)
-        return SSD_ERR_SHAPE;
-    if (p->nheads % p->nkv_heads != 0) return SSD_ERR_SHAPE;
-    if (p->num_seqs == 0 && (p->total_q > 0 || p->total_k > 0)) return SSD_ERR_SHAPE;
-    if (!float_ok(p->dtype)) return SSD_ERR_DTYPE;
-    if (!headdim_ok(p->headdim)) return SSD_ERR_UNSUPPORTED;
-    if (p->bf16_weights != 0 && p->bf16_weights != 1) return SSD_ERR_UNSUPPORTED;
-    // grid limit: query tiles of at least 16 rows, one more a sequence, times heads
-    if (((int64_t)p->total_q / 16 + p->num_seqs) * p->nheads > 0x7fffffffLL)
-        return SSD_ERR_UNSUPPORTED;
     ssd::AttnDims d;
-    const int64_t qr = (int64_t)p->nheads * p->headdim, kr = (int64_t)p->nkv_heads * p->headdim;
-    if (!stride_of(p->q_stride, qr, &d.qs) || !stride_of(p->k_stride, kr, &d.ks) ||
-        !stride_of(p->v_stride, kr, &d.vs) || !stride_of(p->o_stride, qr, &d.os))
-        return SSD_ERR_SHAPE;
-    // a tile of up to 256 rows is addressed by 32-bit byte offsets
-    if (d.qs > (1 << 21) || d.ks > (1 << 21) || d.vs > (1 << 21)) return SSD_ERR_UNSUPPORTED;
-    if (!scale_of(p->scale, p->headdim, &d.scale)) return SSD_ERR_SHAPE;
+    const int rc = attn_dims(p, &d);
+    if (rc) return rc;
     if (!q || !k || !v || !cu_seqlens_q || !cu_seqlens_k || !out) return SSD_ERR_NULL;
     const size_t e = size_of(p->dtype);
     if (!row_aligned(q, d.qs, e) || !row_aligned(k, d.ks, e) || !row_aligned(v, d.vs, e) ||
         !row_aligned(out, d.os, e) || !aligned(lse, 4) || !aligned(cu_seqlens_q, 4) ||
         !aligned(cu_seqlens_k, 4))
         return SSD_ERR_ALIGN;
-    d.Tq = p->total_q;
-    d.Tk = p->total_k;
-    d.S = p->num_seqs;
-    d.H = p->nheads;
-    d.Hkv = p->nkv_heads;
-    d.D = p->headdim;
-    d.bf16 = p->dtype == SSD_BF16;
-    d.causal = p->causal != 0;
-    d.bf16w = p->bf16_weights != 0;
     ssd::launch_attn(d, q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, stream);
     return launch_status();
 }

@@ -396,6 +396,16 @@ static int64_t scan_segments(const ScanDims &d, const ScanPlan &p)
     return p.seg ? (int64_t)d.T / p.seg + d.S : 0;
 }
 
+const char *scan_kernel_name(const ScanDims &d)
+{
+    static const char *const name[2][4] = {
+        {"4 lanes", "4 lanes, segments of 128", "4 lanes, segments of 256", "4 lanes, segments of 512"},
+        {"16 lanes", "16 lanes, segments of 128", "16 lanes, segments of 256",
+         "16 lanes, segments of 512"}};
+    const ScanPlan p = scan_plan(d);
+    return name[p.lanes == 16][p.seg / 128 - p.seg / 512];
+}
+
 size_t scan_workspace(const ScanDims &d)
 {
     return (size_t)scan_segments(d, scan_plan(d)) * d.C * (d.N + 1) * sizeof(float);

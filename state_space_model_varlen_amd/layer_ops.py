@@ -199,6 +199,11 @@ def selective_scan_workspace_bytes(p: scan_problem) -> int:
     return int(_lib.selective_scan_workspace_bytes(ctypes.byref(p)))
 
 
+def selective_scan_varlen_kernel(p: scan_problem) -> str:
+    """How the prompt form runs p: its lanes a channel and segments ("": p is refused)."""
+    return _lib.selective_scan_varlen_kernel(ctypes.byref(p)).decode()
+
+
 def alloc_scan_workspace(p: scan_problem, device="cuda"):
     """Workspace of selective_scan_varlen, or None where it needs none."""
     n = selective_scan_workspace_bytes(p)
@@ -273,6 +278,11 @@ def make_attn_problem(total_q: int, total_k: int, num_seqs: int, nheads: int, nk
     p.dtype, p.causal, p.scale = _DT[dtype], int(bool(causal)), float(scale or 0.0)
     p.bf16_weights = int(bool(bf16_weights))
     return p
+
+
+def attention_varlen_kernel(p: attn_problem) -> str:
+    """The kernel that runs p ("": p is refused)."""
+    return _lib.attention_varlen_kernel(ctypes.byref(p)).decode()
 
 
 def attention_varlen(p: attn_problem, q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse=None,
