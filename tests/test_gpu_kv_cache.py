@@ -304,3 +304,16 @@ def test_another_stream_and_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("ct", [BF, E4])
+@pytest.mark.parametrize("full,T", [(96, 1), (1536, 3)])
+def test_decode_context_beyond_the_table(ct, full, T):
+    """A context longer than the table's pages is cut to them: what the whole table holds."""
+    lens = [full, 40]
+    p, c, table, q, rk, rv = make(8, ct, lens, T, 2, 1, 64, 16)
+    assert table.shape[1] * 16 == full
+    ref = ol.decode_attention(q, rk, rv, lens)
+    for much in (full + 1, 10 ** 9, 2 ** 31 - 1):
+        out, lse = decode(p, c, table, q, [much, 40])
+        compare(out, lse, ref, 64, full)
