@@ -432,15 +432,19 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(
     // a sum came out as NaN, because an infinity times a weight's remainder has either sign, or
     // is NaN (8 bits hold no infinities).
     bool lost = false;
-    if constexpr (!E4M3) {
 #pragma unroll
-        for (int m = 0; m < NRT; ++m)
+    for (int m = 0; m < NRT; ++m) {
+        sum[m] = across32(across16(sum[m], added), added);
+        if constexpr (!E4M3) {
+            bool nan = false;
 #pragma unroll
             for (int i = 0; i < DT; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) lost |= o[m][i][e] != o[m][i][e];
-        lost = __any(lost);
+                for (int e = 0; e < 4; ++e) nan |= o[m][i][e] != o[m][i][e];
+            lost |= nan && sum[m] == sum[m];
+        }
     }
+    lost = __any(lost);
     if (lost || __any(odd)) {
         const int from = shared > k0 && !lost ? (shared - k0) / 32 * 32 : 0, mine = wave * 32;
         const int first = k0 + mine + (from > mine ? (from - mine + 127) / 128 * 128 : 0);
@@ -483,13 +487,11 @@ __global__ __launch_bounds__(256, 2) void decode_attn_kernel(
 
     // join the waves: common maximum, then the four results summed through LDS
 #pragma unroll
-    for (int m = 0; m < NRT; ++m) {
-        const float tot = across32(across16(sum[m], added), added);
+    for (int m = 0; m < NRT; ++m)
         if (g == 0) {
             ml[wave][0][m * 16 + n16] = mx[m];
-            ml[wave][1][m * 16 + n16] = tot;
+            ml[wave][1][m * 16 + n16] = sum[m];
         }
-    }
     __syncthreads();
     for (int m = 0; m < NRT; ++m) {
         const int at = m * 16 + n16;
