@@ -393,7 +393,7 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a)
 // queries that are not there; but every tile of keys is read for fewer queries.
 // A wave's tiles are its own, staged in LDS of its own without barriers: rows read
 // straight into the keys' operand would touch 32 lines with every load (2.1 us a
-// round of 8 tiles of heads of 128, against 1.4).
+// round of 8 tiles of heads of 128, against 1.4; 1.6 since weights have two parts).
 //
 // join_waves: the waves' results (o scaled to the common maximum, in rows of
 // D + 4 floats a query) and statistics, one thread per PER elements.

@@ -621,9 +621,11 @@ static int row_tiles(const DecodeAttnDims &d)
 // (twice, written and read) and the join's launch, so there are no more than
 // bring 1024 blocks, of at least 512 keys; but with few requests a block's
 // chain of key tiles is what takes time, and up to 512 blocks of at least 128
-// keys are made. (128 requests of 1 K to 4 K keys, 8 key heads, 8 bits: 173 us
-// unsplit, 199 us in two, 206 us in four. One request of 32769 keys in bf16: 35
-// us in 65 splits of 512, 41 us in 128 of 256.)
+// keys are made. (128 requests of 1 K to 4 K keys, 8 key heads, 8 bits: 164 us
+// unsplit, 190 us in two, 198 us in four. One request of 32769 keys in bf16: 31
+// us in 65 splits of 512, 33 us in 128 of 256.) The contexts are not known here,
+// their table's width is: a table far wider than they are makes few, long splits
+// (8 requests of 1500 keys: 13 us with a table for 1536, 53 us with one for 32768).
 static DecodePart plan(const DecodeAttnDims &d)
 {
     DecodePart p{nullptr, nullptr, 1, 128};

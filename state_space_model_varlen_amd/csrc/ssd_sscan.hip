@@ -121,7 +121,11 @@ template <typename T, int M> __device__ __forceinline__ void store_state(T *p, c
 // last from zero (the first one from its cached state, finished at once) and
 // keeps its final state and the sum of its steps; a second one chains those in
 // front of it, exp(A sum dt) state + final, and runs each later segment again,
-// with outputs. `cur` says which launch this is: 0 the only one, 1 and 2.
+// with outputs. `cur` says which launch this is: 0 the only one, 1 and 2. Every
+// later segment reads the final states of all before it, which grows with the
+// square of their number: nothing at 8192 tokens, an eighth of the time at 262144
+// (2048 channels, 512 segments of 512: 4551 us, where 16 times the 8192 tokens x 4096
+// channels are 4040), and more beyond.
 struct ScanSegs {
     int seg, cur;
     float *fin, *sum;   // [segments][C][N] final states, [segments][C] sums of steps
@@ -362,7 +366,11 @@ __global__ __launch_bounds__(256) void scan_kernel(
 //   1 of 1024, 5120 channels: 62 us in segments of 128, 92 us with 16 lanes (1280
 //   waves), 109 us with 4
 //   2 of 717 and 1508, 72 channels: 20 us in segments with 16 lanes, 37 us with 4
-// The longest sequence is not known here: 2.5 times the mean stands for it.
+// The longest sequence is not known here: 2.5 times the mean stands for it (prompt
+// attention, whose rule was measured by itself, takes twice). With N = 32 and 64 a
+// wave has 2 and 4 times the states, which `waves` counts and the cycles of a wave
+// alone do not: 265 us for the 8 of 1 to 1600 with N = 32, 544 us for 2560 channels
+// with N = 64, both in whole sequences; other ways were not measured there.
 struct ScanPlan {
     int lanes, seg;
 };
