@@ -75,6 +75,14 @@ class Stack:
         f = x.float()
         return (f * torch.rsqrt(f.square().mean(-1, keepdim=True) + 1e-5)).to(BF)
 
+    def _check_room(self, slots, counts):
+        """Before any state changes: every slot's pages hold the new tokens too."""
+        room = self.pages_per_seq * self.PAGE
+        for s, n in zip(slots, counts):
+            if int(self.lens[s]) + n > room:
+                raise ValueError(f"slot {s} holds {int(self.lens[s])} tokens and has room for {room} "
+                                 f"(got {n} more)")
+
     def _positions(self, slots, counts):
         """Cache position of every new row: page * page size + place."""
         pos = torch.cat([torch.arange(int(self.lens[s]), int(self.lens[s]) + n)
@@ -90,6 +98,7 @@ class Stack:
 
     def prompt(self, x, slots, counts):
         """x [T,hidden]: counts[i] new tokens for slot slots[i], behind what it holds."""
+        self._check_room(slots, counts)
         T, S, d, N, dev = x.shape[0], len(slots), self.inner, self.D_STATE, self.dev
         cu = torch.tensor([0] + counts).cumsum(0).to(torch.int32).to(dev)
         idx = torch.tensor(slots, dtype=torch.int32, device=dev)
@@ -142,6 +151,7 @@ class Stack:
     def verify(self, x, slots, tokens):
         """x [R T,hidden]: `tokens` tokens for every slot of `slots`; states stay where they were
         until commit() says how many of them count."""
+        self._check_room(slots, [tokens] * len(slots))
         R, T, d, N, dev = len(slots), tokens, self.inner, self.D_STATE, self.dev
         idx = torch.tensor(slots, dtype=torch.int32, device=dev)
         new = lambda *s, dtype=BF: torch.empty(*s, dtype=dtype, device=dev)                  # noqa: E731
