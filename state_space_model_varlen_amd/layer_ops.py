@@ -15,7 +15,7 @@ import math
 
 import torch
 
-from . import _DT, _TORCH, _check, _lib, _stream
+from . import _DT, _TORCH, _check, _lib, _stream, ssd_dt_transform
 from ._layer_abi import (attn_decode_problem, attn_problem, conv_problem, kv_cache_problem,
                          scan_problem)
 
@@ -226,6 +226,8 @@ def _scan_common(p, x, dt, A, B, C, D, z, y):
 def _scan_transform(p, tf):
     if tf is None:
         return None
+    if not isinstance(tf, ssd_dt_transform):
+        raise TypeError("dt_transform must come from make_dt_transform")
     bias = getattr(tf, "_dt_bias_tensor", None)
     if bias is not None and tuple(bias.shape) != (p.channels,):
         raise ValueError(f"dt_bias must have shape {(p.channels,)} (got {tuple(bias.shape)})")

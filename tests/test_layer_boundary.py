@@ -241,3 +241,14 @@ def test_attention_weights_choice():
     assert ssd.make_attn_problem(1, 1, 1, 1, 1, 64, BF).bf16_weights == 0
     assert ssd.make_attn_problem(1, 1, 1, 1, 1, 64, BF, bf16_weights=True).bf16_weights == 1
     assert ctypes.sizeof(ssd.attn_problem) == 72       # (the field took a reserved one's place)
+
+
+def test_scan_takes_step_size_transforms_only():
+    """Another struct's bytes would be read as a device pointer and bounds."""
+    p = scan()
+    for wrong in (conv(), p, 0.5, (0.0, 1.0)):
+        with pytest.raises(TypeError, match="dt_transform"):
+            ssd.layer_ops._scan_transform(p, wrong)
+    good = ssd.make_dt_transform(None, 0.0, 1.0)
+    assert ssd.layer_ops._scan_transform(p, good) == ctypes.addressof(good)
+    assert ssd.layer_ops._scan_transform(p, None) is None
