@@ -820,6 +820,162 @@ int attention_decode(const attn_decode_problem *p, const void *q, const void *k_
                      const int32_t *block_table, const int32_t *context_lens, void *out,
                      float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Operators between and behind the layers of a serving step
+ * ---------------------------------------------------------
+ * The conventions are those of the operators of the layers above: strided
+ * token rows, float32 parameters, element alignment unless an entry point says
+ * more, every check on the host before the first launch, no result that
+ * depends on the order in which blocks run. A workspace holds nothing between
+ * calls, and calls that may run at the same time need one each. Arrays of one
+ * call must not overlap, except where an entry point says so.
+ */
+
+/* Root-mean-square norm (host struct). */
+typedef struct {
+    int32_t rows;           /* token rows */
+    int32_t hidden;         /* elements a row */
+    int32_t ngroups;        /* a row is normed in this many equal parts (1: as a whole) */
+    int32_t in_dtype;       /* ssd_dtype of x and gate (SSD_F32 or SSD_BF16) */
+    int32_t residual_dtype; /* ssd_dtype of residual and residual_out (SSD_F32 or SSD_BF16) */
+    int32_t out_dtype;      /* SSD_F32, SSD_BF16 or SSD_E4M3 */
+    float eps;              /* >= 0 */
+    int32_t reserved;       /* 0 */
+    int64_t x_stride, gate_stride, residual_stride, residual_out_stride, out_stride;
+} norm_problem;
+
+/*
+ *   v      = x, x + residual, or x * silu(gate)
+ *   out[i] = v[i] / sqrt(mean of v^2 over i's group + eps) * weight[i]
+ * in float32. residual_out takes v = x + residual (rounded to residual_dtype;
+ * the norm is of the unrounded sum); it may be residual itself.
+ *   x, gate, residual, residual_out, out [rows,hidden]; gate and residual
+ *   exclude each other, both may be NULL; residual_out NULL: not kept
+ *   weight [hidden] float32, or NULL (ones)
+ *   out_scale [rows,hidden/32] uint8 with SSD_E4M3, else NULL
+ * SSD_E4M3 writes 8-bit rows for linear_w4: the 32 elements of block b stand
+ * for code * 2^(scale[b] - 127), with the least power of two for which none
+ * exceeds 448 of it (at least 2^-126; 32 zeros have scale byte 1), each
+ * element rounded once, to nearest even; infinities and NaN are stored as NaN
+ * and do not enter the scale. hidden / ngroups must be a multiple of 32 then.
+ */
+int rms_norm(const norm_problem *p, const void *x, const void *gate, const void *residual,
+             const float *weight, void *out, uint8_t *out_scale, void *residual_out,
+             void *stream);
+
+/* Products with 4-bit weights (host struct). */
+typedef struct {
+    int32_t tokens;       /* T */
+    int32_t in_features;  /* K, a multiple of 32 */
+    int32_t out_features; /* N */
+    int32_t x_dtype;      /* SSD_BF16 or SSD_E4M3 */
+    int32_t out_dtype;    /* SSD_BF16 or SSD_F32 */
+    int32_t reserved;     /* 0 */
+    int64_t x_stride, out_stride;
+} linear_problem;
+
+/*
+ *   out[t,n] = sum over k of x[t,k] w[n,k] + bias[n]
+ * with float32 accumulation of exact products, for one token (the weights'
+ * bytes bound it) to long prompts (the matrix units do).
+ *   weight [N,K/2] uint8: two codes a byte, the even k in the low half. A code
+ *   is a sign bit and 0, 0.5, 1, 1.5, 2, 3, 4 or 6; the 32 codes of block b of
+ *   a row stand for value * 2^(weight_scale[b] - 127)
+ *   weight_scale [N,K/32] uint8 (255: NaN)
+ *   x [T,K] bfloat16 with x_scale NULL, or SSD_E4M3 with x_scale [T,K/32]
+ *   uint8 as rms_norm writes them: the matrix instruction takes 8-bit rows,
+ *   codes and both scales as they are; for bfloat16 rows the weights are
+ *   widened to bfloat16, which is exact
+ *   bias [N] float32 or NULL; out [T,N]
+ * x and its stride must keep every row 16-byte aligned, weight must be 16-byte
+ * aligned (SSD_ERR_ALIGN).
+ *   workspace   linear_w4_workspace_bytes(p) bytes, 16-byte aligned (NULL when
+ *               that is 0)
+ */
+size_t linear_w4_workspace_bytes(const linear_problem *p);
+/* (for profiles and tests: the kernel that runs p; "" for a problem refused) */
+const char *linear_w4_kernel(const linear_problem *p);
+int linear_w4(const linear_problem *p, const void *x, const uint8_t *x_scale,
+              const uint8_t *weight, const uint8_t *weight_scale, const float *bias, void *out,
+              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Codes and scales of weights w [N,K] (dtype SSD_F32 or SSD_BF16, contiguous,
+ * 16-byte aligned): for every 32 of a row the least power of two for which
+ * none exceeds 6 of it (2^-126 to 2^125; 32 zeros have scale byte 1), each
+ * element rounded to the nearest value, of two equally near ones to the even
+ * code; infinities become 6 and NaN 0 and do not enter the scale. Uses
+ * in_features and out_features of p alone.
+ */
+int linear_w4_encode(const linear_problem *p, int32_t dtype, const void *w, uint8_t *weight,
+                     uint8_t *weight_scale, void *stream);
+
+/* Probabilities of tokens (host struct). */
+typedef struct {
+    int32_t num_reqs;       /* R */
+    int32_t tokens_per_req; /* T */
+    int32_t vocab;          /* V */
+    int32_t in_dtype;       /* ssd_dtype of the logits (SSD_F32 or SSD_BF16) */
+    int64_t logits_stride, probs_stride;
+} probs_problem;
+
+/*
+ *   probs[r,t,v] = exp(logits[r,t,v] / temperature[r]) / sum over v of the same
+ * in float32. A temperature of 0 (or less, or NaN) puts 1 on the largest logit
+ * of the row, of equal ones on the first, and 0 elsewhere. Logits of -infinity
+ * have probability 0; a row of nothing else is all zeros. A NaN or +infinity
+ * makes its row NaN (temperature 0 passes NaN over).
+ *   logits [R,T,V] in_dtype, probs [R,T,V] float32
+ *   temperature [R] float32, or NULL (ones)
+ *   workspace   token_probs_workspace_bytes(p) bytes, 16-byte aligned (NULL
+ *               when that is 0)
+ */
+size_t token_probs_workspace_bytes(const probs_problem *p);
+int token_probs(const probs_problem *p, const void *logits, const float *temperature,
+                float *probs, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Verification of drafted tokens (host struct). */
+typedef struct {
+    int32_t num_reqs;       /* R */
+    int32_t tokens_per_req; /* T: 1 + the most drafts of a request, at most 65 */
+    int32_t vocab;          /* V */
+    int32_t reserved;       /* 0 */
+    int64_t target_stride, draft_stride; /* between rows of V probabilities */
+} verify_problem;
+
+/*
+ * Which drafts of a verify step stand, and the token that follows them, such
+ * that tokens are distributed as the target's probabilities say. Draft i of a
+ * request, token d, is accepted iff
+ *   uniform[r,i] * draft_probs[r,i,d] < target_probs[r,i,d],
+ * up to the first that is not (a token outside [0, V) never is). The next
+ * token is drawn from the weights w = max(target - draft, 0) of the row where
+ * a draft was turned down (from the target's row itself where these are all
+ * zero), or from the target's row behind the last draft: the lowest v of
+ * positive weight with
+ *   w[0] + ... + w[v] > uniform[r,T-1] * sum of w
+ * (rounding may leave none: the last v of positive weight). Products, weights
+ * and sums are in 64 bits, so that a token does not depend on how a sum is
+ * split. Probabilities that are negative or NaN count as zero; rows need not
+ * sum to one. A row without positive weight gives token -1.
+ *   target_probs [R,T,V] float32: row i is the target's for the place of draft
+ *   i, row T-1 (num_drafts[r] of a request with fewer) the one behind
+ *   draft_probs [R,T-1,V] float32, or NULL: the drafts are certain (their
+ *   probability 1, everything else's 0)
+ *   draft_tokens [R,T-1] int32; num_drafts [R] int32, clamped to [0, T-1], or
+ *   NULL (T-1 each); uniform [R,T] float32 in [0, 1)
+ *   num_accepted [R] int32, as ssd_state_commit and the other commits take it
+ *   tokens [R,T] int32: the accepted drafts, the next token, then -1
+ *   workspace   verify_drafts_workspace_bytes(p) bytes, 16-byte aligned (NULL
+ *               when that is 0)
+ * T = 1 samples from the target (draft_probs and draft_tokens may be NULL).
+ */
+size_t verify_drafts_workspace_bytes(const verify_problem *p);
+int verify_drafts(const verify_problem *p, const float *target_probs, const float *draft_probs,
+                  const int32_t *draft_tokens, const int32_t *num_drafts, const float *uniform,
+                  int32_t *num_accepted, int32_t *tokens, void *workspace,
+                  size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

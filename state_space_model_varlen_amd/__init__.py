@@ -15,7 +15,9 @@ Decode: x, y [R,T,H,P]; dt [R,T,H]; B, C [R,T,G,N]; intermediate states
 [R,T,H,P,N]; num_accepted [R] int32.
 
 The operators of the layers around the scan (short convolution, channel-wise
-scan, attention, paged key / value cache) are bound in ``layer_ops``.
+scan, attention, paged key / value cache) are bound in ``layer_ops``, those
+between and behind the layers (norm, products with 4-bit weights, token
+probabilities, verification of drafts) in ``step_ops``.
 """
 from __future__ import annotations
 
@@ -27,6 +29,8 @@ import torch
 
 from ._layer_abi import (LAYER_SIGS, attn_decode_problem, attn_problem, conv_problem,  # noqa: F401
                          kv_cache_problem, scan_problem)
+from ._step_abi import (STEP_SIGS, linear_problem, norm_problem, probs_problem,  # noqa: F401
+                        verify_problem)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libssd_mi355x.so")
@@ -118,6 +122,7 @@ _SIGS = {
     "ssd_combined_varlen_noalloc": ([_pp] + [_vp] * 13, ctypes.c_int),
 }
 _SIGS.update(LAYER_SIGS)
+_SIGS.update(STEP_SIGS)
 for _name, (_args, _res) in _SIGS.items():
     _f = getattr(_lib, _name)
     _f.argtypes = _args
@@ -744,3 +749,12 @@ from .layer_ops import (  # noqa: E402,F401
     make_attn_decode_problem, make_attn_problem, make_conv_problem, make_kv_cache_problem,
     make_scan_problem, selective_scan_update, selective_scan_varlen, selective_scan_varlen_kernel,
     selective_scan_workspace_bytes)
+
+# ---------------------------------------------------------------------------
+# the operators between and behind the layers
+
+from .step_ops import (  # noqa: E402,F401
+    alloc_linear_weights, alloc_linear_workspace, alloc_probs_workspace, alloc_verify_workspace,
+    linear_w4, linear_w4_encode, linear_w4_kernel, linear_w4_workspace_bytes, make_linear_problem,
+    make_norm_problem, make_probs_problem, make_verify_problem, rms_norm, token_probs,
+    token_probs_workspace_bytes, verify_drafts, verify_drafts_workspace_bytes)

@@ -11,8 +11,9 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libssd_mi355x.so")
 SOURCES = ["ssd_api.cpp", "ssd_prefill.hip", "ssd_decode.hip", "ssd_replay.hip",
            "ssd_noalloc.hip", "ssd_layer_api.cpp", "ssd_conv.hip", "ssd_sscan.hip", "ssd_attn.hip",
-           "ssd_kv.hip"]
-HEADERS = ["ssd_device.h", "ssd_launch.h", "ssd_layer.h", "ssd_layer_device.h"]
+           "ssd_kv.hip", "ssd_step_api.cpp", "ssd_norm.hip", "ssd_w4.hip", "ssd_sample.hip"]
+HEADERS = ["ssd_device.h", "ssd_launch.h", "ssd_layer.h", "ssd_layer_device.h",
+           "ssd_step.h"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
