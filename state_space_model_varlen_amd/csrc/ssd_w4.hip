@@ -22,9 +22,17 @@ namespace ssd {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+enum LinearMode {
+    kEight,      // 8-bit rows, scaled 8-bit instruction
+    kSixteen,    // bfloat16 rows
+    kWidened     // 8-bit rows widened to bfloat16
+};
+
 
 // Byte offset of a lane that has nothing to read: past every resource's end.
-constexpr uint32_t kNothing = 0x80000000u;
+constexpr uint32_t kNothing = 0x40000000u;     // (twice it is still past the end)
 
 // (`at`, the same in every lane, is added to the address; that a lane's own offset lies past the
 // end is seen with and without it)
@@ -52,113 +60,7 @@ __device__ __forceinline__ bf16x8 widen_codes(uint32_t w, uint32_t byte) {
     return r;
 }
 
-__device__ __forceinline__ f32x4 mma_8bit(i32x4 w, int ws, i32x4 x0, i32x4 x1, int xs, f32x4 c) {
-    const i32x8 a = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
-    const i32x8 b = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
-    // (first operand 4-bit, second e4m3; exponents from the lowest byte)
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 0, 0, ws, 0, xs);
-}
-
-// What a block of 4 waves works on: 16 RT weight rows, 16 TT tokens; the waves
-// take the K steps in turn and are joined in LDS.
-template <bool E4M3, int TT, int RT, typename TO>
-__global__ __launch_bounds__(256) void linear_kernel(LinearDims d, LinearArgs a)
-{
-    __shared__ f32x4 part[4][RT * TT][64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = scalar(tid >> 6), n16 = lane & 15, g = lane >> 4;
-    const int n0 = (int)blockIdx.x * 16 * RT, t0 = (int)blockIdx.y * 16 * TT;
-    const int blocks = d.K / 32;                                  // of 32 in a row
-    constexpr int EX = E4M3 ? 1 : 2;
-    const int nrows = d.N - n0 < 16 * RT ? d.N - n0 : 16 * RT, ntok = d.T - t0 < 16 * TT ? d.T - t0 : 16 * TT;
-    const rsrc_t rw = make_rsrc(a.w + (int64_t)n0 * (d.K / 2), (uint32_t)nrows * (uint32_t)(d.K / 2));
-    const rsrc_t rs = make_rsrc(a.w_scale + (int64_t)n0 * blocks, (uint32_t)nrows * (uint32_t)blocks);
-    const rsrc_t rx = make_rsrc(static_cast<const char *>(a.x) + (int64_t)t0 * d.xs * EX,
-                                (uint32_t)((ntok - 1) * d.xs + d.K) * EX);
-    const rsrc_t rxs = make_rsrc(a.x_scale + (int64_t)t0 * blocks, E4M3 ? (uint32_t)ntok * (uint32_t)blocks : 0);
-    f32x4 acc[RT][TT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int t = 0; t < TT; ++t) acc[r][t] = zero4();
-
-    for (int s = wave; s * 4 < blocks; s += 4) {
-        const int b = 4 * s + g;                                  // this lane's block of 32
-        const bool in = b < blocks;
-        i32x4 w[RT];
-        int ws[RT];
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const int row = 16 * r + n16;
-            w[r] = buf16(rw, in ? (uint32_t)row * (uint32_t)(d.K / 2) + 16u * b : kNothing);
-            ws[r] = buf1(rs, in ? (uint32_t)row * (uint32_t)blocks + b : kNothing);
-        }
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            const int tok = 16 * t + n16;
-            const bool live = tok < ntok;
-            const uint32_t at = (uint32_t)tok * (uint32_t)d.xs * EX;
-            if constexpr (E4M3) {
-                const uint32_t k0 = 128u * s + 16u * g, k1 = k0 + 64u;
-                const i32x4 x0 = buf16(rx, live && k0 < (uint32_t)d.K ? at + k0 : kNothing);
-                const i32x4 x1 = buf16(rx, live && k1 < (uint32_t)d.K ? at + k1 : kNothing);
-                const int xs = buf1(rxs, live && in ? (uint32_t)tok * (uint32_t)blocks + b : kNothing);
-#pragma unroll
-                for (int r = 0; r < RT; ++r) acc[r][t] = mma_8bit(w[r], ws[r], x0, x1, xs, acc[r][t]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t k = 128u * s + 32u * g + 8u * i;
-                    const bf16x8 x = __builtin_bit_cast(bf16x8, buf16(rx, live && in ? at + 2u * k : kNothing));
-#pragma unroll
-                    for (int r = 0; r < RT; ++r)
-                        acc[r][t] = Mma<bf16>::run(widen_codes((uint32_t)w[r][i], (uint32_t)ws[r]), x, acc[r][t]);
-                }
-            }
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int t = 0; t < TT; ++t) part[wave][r * TT + t][lane] = acc[r][t];
-    __syncthreads();
-    TO *const out = static_cast<TO *>(a.out);
-    for (int i = wave; i < RT * TT; i += 4) {
-        f32x4 y = part[0][i][lane];
-#pragma unroll
-        for (int k = 1; k < 4; ++k) {
-            const f32x4 o = part[k][i][lane];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] += o[e];
-        }
-        const int tok = t0 + 16 * (i % TT) + n16, n = n0 + 16 * (i / TT) + 4 * g;
-        if (tok < d.T)
-            for (int e = 0; e < 4; ++e)
-                if (n + e < d.N)
-                    out[(int64_t)tok * d.os + n + e] = from_f32<TO>(y[e] + (a.bias ? a.bias[n + e] : 0.0f));
-    }
-}
-
-// ---------------------------------------------------------------------------
-// Many tokens: a block of 4 waves takes 16 TT tokens and 64 RT weight rows, 16 RT
-// of them a wave. The weights go straight from memory to registers, where they
-// are operands as they lie, each read by one wave; the tokens' rows are shared
-// and go through LDS, 128 of their values a stage, written there by the loads
-// themselves. While a stage is multiplied the next one is on its way.
-//
-// A row's 16-byte chunk c lies in place c ^ row % 16 (of 16) or c ^ row / 2 % 8
-// (of 8), so that the 16 rows that a fragment reads together touch all banks.
-//
-// Rows of a fragment are dealt such that a lane's results of its RT fragments
-// are 4 RT neighbouring outputs.
-enum LinearMode {
-    kEight,      // 8-bit rows, scaled 8-bit instruction
-    kSixteen,    // bfloat16 rows
-    kWidened     // 8-bit rows widened to bfloat16
-};
-
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-typedef __attribute__((address_space(3))) void lds_void;
-
+// 8 values of 8 bits widened to bfloat16 and scaled by s, a power of two.
 __device__ __forceinline__ bf16x8 widen_8bit(u32x2 w, float s) {
     bf16x8 r;
     bf16x2 p[4];
@@ -174,90 +76,205 @@ __device__ __forceinline__ bf16x8 widen_8bit(u32x2 w, float s) {
     return r;
 }
 
-template <int MODE, int TT, int RT, typename TO>
-__global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearDims d, LinearArgs a, int ttiles, int ntiles)
-{
-    constexpr int EX = MODE == kSixteen ? 2 : 1;
-    constexpr int TOK = 16 * TT, CH = 8 * EX;             // CH: 16-byte chunks of a token a stage
-    constexpr int PITCH = 16 * CH, LOADS = TOK * CH / 256;
-    static_assert(TOK * CH % 256 == 0, "whole loads");
-    __shared__ __align__(16) char xa[TOK * PITCH], xb[TOK * PITCH];
-    // (scales of 8-bit rows: 4 a token)
-    __shared__ uint8_t sa[MODE == kSixteen ? 1 : 4 * TOK], sb[MODE == kSixteen ? 1 : 4 * TOK];
-    const int tid = threadIdx.x, lane = tid & 63, wave = scalar(tid >> 6), n16 = lane & 15, g = lane >> 4;
+__device__ __forceinline__ f32x4 mma_8bit(i32x4 w, int ws, i32x4 x0, i32x4 x1, int xs, f32x4 c) {
+    const i32x8 a = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
+    const i32x8 b = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
+    // (first operand 4-bit, second e4m3; exponents from the lowest byte)
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 0, 0, ws, 0, xs);
+}
 
-    // tiles in groups of 8 token tiles, so that the blocks of one L2 share rows and weights
-    constexpr int kGroup = 8;
+// ---------------------------------------------------------------------------
+// Many tokens: a block of WT x WN waves takes 16 TT WT tokens and 16 RT WN weight
+// rows, 16 TT by 16 RT a wave. Tokens, weights and scales go to LDS by the loads
+// themselves, a stage of K (128 values of 8-bit rows, 64 of bfloat16) in one of
+// NBUF buffers: while a stage is multiplied the next NBUF - 1 are on their way.
+//
+// A token's 128 bytes of a stage are 8 chunks, chunk c in place c ^ token / 2 % 8,
+// so that the 16 tokens that a fragment reads together touch all banks. Weight
+// rows lie in the order in which the fragments take them, which is such that a
+// lane's results of its RT fragments are 4 RT neighbouring outputs.
+//
+// Scales take a word each: with WORDS the 4 bytes of a stage in one (their
+// arrays' rows are whole words then), else one byte.
+typedef __attribute__((address_space(3))) void lds_void;
+
+// Loads of 16, 4 or 1 bytes a lane straight to LDS, the lanes' one behind the other from `to` on (a
+// word each for 4 and 1), written as instructions that the compiler does not count: it would wait for
+// all of them before it reads any other LDS. What waits for them is wait_and_meet(). They have no
+// result register, and the address is taken when they are issued. (m0 has no other user here.)
+struct LdsSource {
+    i32x4 r;
+    __device__ __forceinline__ LdsSource(const void *base, uint32_t bytes) {
+        const uint64_t b = (uint64_t)base;
+        r = i32x4{(int)(uint32_t)b, (int)(uint32_t)(b >> 32) & 0xffff, (int)bytes, 0x00020000};
+    }
+};
+__device__ __forceinline__ uint32_t lds_address(const void *p) { return (uint32_t)(uintptr_t)(const lds_void *)p; }
+__device__ __forceinline__ void to_lds16(i32x4 r, uint32_t to, uint32_t off, uint32_t at) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to), "v"(off),
+                 "s"(r), "s"(at) : "memory");
+}
+__device__ __forceinline__ void to_lds4(i32x4 r, uint32_t to, uint32_t off, uint32_t at) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(to), "v"(off),
+                 "s"(r), "s"(at) : "memory");
+}
+__device__ __forceinline__ void to_lds1(i32x4 r, uint32_t to, uint32_t off, uint32_t at) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, %3 offen lds" ::"s"(to), "v"(off),
+                 "s"(r), "s"(at) : "memory");
+}
+
+// Every wave waits for all but its newest `N` loads and for its own LDS reads, then for the others.
+template <int N> __device__ __forceinline__ void wait_and_meet() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Buffer I of a block (objects of their own: the compiler then sees that a read of one does not
+// depend on loads on their way to another).
+template <typename B, int I> __device__ __forceinline__ B &buffer() {
+    __shared__ __align__(16) B b;
+    return b;
+}
+template <int N, int I = 0, typename F> __device__ __forceinline__ void each(F f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        each<N, I + 1>(f);
+    }
+}
+
+template <int MODE, int WT, int WN, int WK, int TT, int RT, int NSUB, int NBUF, bool WORDS, int PERCU, typename TO>
+__global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) void linear_tile_kernel(LinearDims d, LinearArgs a,
+                                                                                           int ttiles, int ntiles)
+{
+    constexpr int THREADS = 64 * WT * WN * WK, TOK = 16 * TT * WT, ROWS = 16 * RT * WN;
+    constexpr int EX = MODE == kSixteen ? 2 : 1, KS = 128 / EX, BS = KS / 32;    // values, blocks a stage
+    constexpr int CW = KS / 32;                                                 // chunks of a weight row a stage
+    constexpr int LX = (TOK * 8 + THREADS - 1) / THREADS, LW = (ROWS * CW + THREADS - 1) / THREADS;     // loads of a thread
+    // words of scales: the tokens' and, from a whole wave's on, the weights'
+    constexpr int SX = MODE == kSixteen ? 0 : WORDS ? TOK : TOK * BS, SO = (SX + 63) / 64 * 64;
+    constexpr int SW = WORDS && MODE != kSixteen ? ROWS : ROWS * BS;
+    constexpr int LS = (SO + SW + THREADS - 1) / THREADS;
+    constexpr int LOADS = LX + LW + LS;
+    static_assert(RT == 1 || RT == 2 || RT == 4 || RT == 8, "whole stores");
+    static_assert(NSUB % WK == 0 && LOADS * NSUB * (NBUF - 2) < 64, "waits that can be counted");
+    // chunks and words of a step, rounded up to a wave's load; every wave makes the same number of
+    // loads, those that have nothing to bring into `spare`
+    constexpr int NX = (TOK * 8 + 63) / 64 * 64, NW = (ROWS * CW + 63) / 64 * 64, NS = (SO + SW + 63) / 64 * 64;
+    struct Step {
+        char x[NX * 16], w[NW * 16];
+        uint32_t s[NS];
+    };
+    struct Buffer {
+        Step step[NSUB];
+    };
+    const int tid = threadIdx.x, lane = tid & 63, wave = scalar(tid >> 6), n16 = lane & 15, g = lane >> 4;
+    __shared__ __align__(16) char spare[1024];
+    const uint32_t nowhere = lds_address(spare);
+    const int wt = wave / WN % WT, wn = wave % WN, wk = wave / (WN * WT);
+
+    // tiles in groups of token tiles, so that the blocks of one L2 share rows and weights
+    constexpr int kGroup = 1024 / TOK;
     const int id = xcd_logical_block((int)blockIdx.x, ttiles * ntiles);
     const int grp = id / (kGroup * ntiles), in = id - grp * (kGroup * ntiles);
     const int gm = ttiles - grp * kGroup < kGroup ? ttiles - grp * kGroup : kGroup;
-    const int nt = in / gm, t0 = (grp * kGroup + in - nt * gm) * TOK, n0 = nt * 64 * RT;
+    const int nt = in / gm, t0 = (grp * kGroup + in - nt * gm) * TOK, n0 = nt * ROWS;
 
-    const int blocks = d.K / 32, stages = (blocks + 3) / 4;
-    const int nrows = d.N - n0 < 64 * RT ? d.N - n0 : 64 * RT, ntok = d.T - t0 < TOK ? d.T - t0 : TOK;
-    const rsrc_t rw = make_rsrc(a.w + (int64_t)n0 * (d.K / 2), (uint32_t)nrows * (uint32_t)(d.K / 2));
-    const rsrc_t rx = make_rsrc(static_cast<const char *>(a.x) + (int64_t)t0 * d.xs * EX,
+    const int blocks = d.K / 32, stages = (blocks + BS * NSUB - 1) / (BS * NSUB);
+    const int nrows = d.N - n0 < ROWS ? d.N - n0 : ROWS, ntok = d.T - t0 < TOK ? d.T - t0 : TOK;
+    const LdsSource rw(a.w + (int64_t)n0 * (d.K / 2), (uint32_t)nrows * (uint32_t)(d.K / 2));
+    const LdsSource rx(static_cast<const char *>(a.x) + (int64_t)t0 * d.xs * EX,
                                 (uint32_t)((ntok - 1) * d.xs + d.K) * EX);
-    const rsrc_t rs = make_rsrc(a.w_scale + (int64_t)n0 * blocks, (uint32_t)nrows * (uint32_t)blocks);
-    const rsrc_t rxs = make_rsrc(a.x_scale + (int64_t)t0 * blocks,
+    const LdsSource rs(a.w_scale + (int64_t)n0 * blocks, (uint32_t)nrows * (uint32_t)blocks);
+    const LdsSource rxs(a.x_scale + (int64_t)t0 * blocks,
                                  MODE == kSixteen ? 0 : (uint32_t)ntok * (uint32_t)blocks);
 
-    // this lane's first weight row (the others follow 4 rows apart), and the chunks and scales that
-    // this thread brings to LDS
-    const int row0 = wave * 16 * RT + 4 * RT * (n16 >> 2) + (n16 & 3);
-    const uint32_t srow = (uint32_t)row0 * (uint32_t)blocks + g, sstep = 4u * (uint32_t)blocks;
-    // (row / CH of a chunk's place: the same for all of a thread's chunks)
-    const int turn = CH == 16 ? n16 : n16 >> 1;
-    const uint32_t chunk = 16u * ((tid % CH) ^ ((tid >> 4) & (CH - 1)));
-    const uint32_t xrow = (uint32_t)(tid / CH) * (uint32_t)d.xs * EX + chunk;
-    const uint32_t xstep = (256u / CH) * (uint32_t)d.xs * EX;
-    const uint32_t xsrow = (uint32_t)(tid >> 2) * (uint32_t)blocks + (tid & 3), xsstep = 64u * (uint32_t)blocks;
-    constexpr int XS = MODE == kSixteen ? 0 : (TT + 3) / 4;      // scale loads of a thread
-
-    struct Stage {
-        i32x4 w[RT];
-        int s[RT], xs[XS ? XS : 1];
+    // the weight row in place p of the tile
+    auto row_in = [](int p) {
+        const int m = p & 15, r = (p >> 4) % RT, w = p / (16 * RT);
+        return w * 16 * RT + 4 * RT * (m >> 2) + 4 * r + (m & 3);
     };
+    // what this thread brings to LDS: offsets in the tile, and the block in the stage
+    const uint32_t chunk = 16u * ((tid & 7) ^ ((tid >> 4) & 7));
+    const uint32_t xrow = tid < TOK * 8 ? (uint32_t)(tid >> 3) * (uint32_t)d.xs * EX + chunk : kNothing;
+    const uint32_t xstep = (THREADS / 8u) * (uint32_t)d.xs * EX;
+    uint32_t wrow[LW], srow[LS];
+    int sblk[LS];
+#pragma unroll
+    for (int q = 0; q < LW; ++q) {
+        const int c = q * THREADS + tid;
+        wrow[q] = c < ROWS * CW ? (uint32_t)row_in(c / CW) * (uint32_t)(d.K / 2) + 16u * (c % CW) : kNothing;
+    }
+#pragma unroll
+    for (int q = 0; q < LS; ++q) {
+        const int e = q * THREADS + tid;
+        constexpr bool one = WORDS && MODE != kSixteen;
+        const int f = e < SO ? e : e - SO, at = one ? f : f / BS;
+        sblk[q] = one ? 0 : f % BS;
+        srow[q] = f < (e < SO ? SX : SW) ? (uint32_t)(e < SO ? at : row_in(at)) * (uint32_t)blocks + sblk[q] : kNothing;
+    }
+
     f32x4 acc[RT][TT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int t = 0; t < TT; ++t) acc[r][t] = zero4();
 
-    // everything of stage s on its way: tokens to LDS, the rest to registers; what lies past a row's
-    // or the tile's end comes back as zeros
-    auto request = [&](int s, char *x, Stage &w) {
-        const uint32_t xo = xrow + (chunk + (uint32_t)PITCH * s < (uint32_t)d.K * EX ? 0u : kNothing);
+    // everything of step s on its way; what lies past a row's or the tile's end comes as zeros
+    auto request_step = [&](int s, const Step &b) {
+        const uint32_t bx = lds_address(b.x), bw = bx + sizeof(b.x), bs = bw + sizeof(b.w);
+        const uint32_t xo = xrow + (chunk + 128u * s < (uint32_t)d.K * EX ? 0u : kNothing);
 #pragma unroll
-        for (int q = 0; q < LOADS; ++q)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void *)(x + (q * 256 + wave * 64) * 16), 16,
-                                                     xo + q * xstep, PITCH * s, 0, 0);
-        // (a scale byte for 16 bytes of weights)
-        const uint32_t so = srow + (4 * s + g < blocks ? 0u : kNothing / 16), wo = 16u * so;
+        for (int q = 0; q < LX; ++q) {
+            const int c = q * THREADS + wave * 64;
+            to_lds16(rx.r, c < NX ? bx + 16 * c : nowhere, xo + q * xstep, 128u * s);
+        }
+        const uint32_t wo = BS * s + tid % CW < blocks ? 0u : kNothing;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            w.w[r] = buf16(rw, wo + r * (16u * sstep), 64u * s);
-            w.s[r] = buf1(rs, so + r * sstep, 4u * s);
+        for (int q = 0; q < LW; ++q) {
+            const int c = q * THREADS + wave * 64;
+            to_lds16(rw.r, c < NW ? bw + 16 * c : nowhere, wrow[q] + wo, 16u * BS * s);
         }
 #pragma unroll
-        for (int q = 0; q < XS; ++q)
-            w.xs[q] = buf1(rxs, xsrow + (4 * s + (tid & 3) < blocks ? 0u : kNothing) + q * xsstep, 4u * s);
+        for (int q = 0; q < LS; ++q) {
+            const int e = q * THREADS + wave * 64;
+            const uint32_t so = srow[q] + (BS * s + sblk[q] < blocks ? 0u : kNothing);
+            const i32x4 r = e < SO ? rxs.r : rs.r;                               // (the same in a wave)
+            const uint32_t to = e < NS ? bs + 4 * e : nowhere;
+            if constexpr (WORDS && MODE != kSixteen) to_lds4(r, to, so, BS * s);
+            else to_lds1(r, to, so, BS * s);
+        }
     };
-    // the tokens' scales next to their values
-    auto deposit = [&](const Stage &w, uint8_t *xs) {
+    auto request = [&](int s, const Buffer &b) {
 #pragma unroll
-        for (int q = 0; q < XS; ++q)
-            if (TT % 4 == 0 || tid < 4 * TOK) xs[q * 256 + tid] = (uint8_t)w.xs[q];
+        for (int u = 0; u < NSUB; ++u) request_step(s * NSUB + u, b.step[u]);
     };
-    auto multiply = [&](const char *x, const uint8_t *xs, const Stage &wt) {
-        const char *const xl = x + n16 * PITCH;
+    // scale of block g of token or row `at`
+    auto scale_of = [&](const uint32_t *p, int at, int blk) -> uint32_t {
+        if constexpr (WORDS && MODE != kSixteen) return reinterpret_cast<const uint8_t *>(p)[4 * at + blk];
+        else return p[at * BS + blk];
+    };
+    auto multiply_step = [&](const Step &b) {
+        const char *const x = b.x + (wt * 16 * TT + n16) * 128;
+        const char *const w = b.w + (wn * 16 * RT + n16) * (CW * 16);
+        const int turn = n16 >> 1;
+        uint32_t ws[RT][MODE == kSixteen ? 2 : 1];      // (by block: a lane group's own, or both)
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int i = 0; i < (MODE == kSixteen ? 2 : 1); ++i)
+                ws[r][i] = scale_of(b.s + SO, wn * 16 * RT + 16 * r + n16, MODE == kSixteen ? i : g);
         if constexpr (MODE == kEight) {
+            i32x4 wf[RT];
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+                wf[r] = *reinterpret_cast<const i32x4 *>(w + r * (256 * CW) + 16 * g);
             i32x4 f[2][2];
-            int b[2];
+            int xs[2];
             auto take = [&](int t) {
-                f[t & 1][0] = *reinterpret_cast<const i32x4 *>(xl + 16 * t * PITCH + 16 * (g ^ turn));
-                f[t & 1][1] = *reinterpret_cast<const i32x4 *>(xl + 16 * t * PITCH + 16 * ((4 + g) ^ turn));
-                b[t & 1] = xs[4 * (16 * t + n16) + g];
+                f[t & 1][0] = *reinterpret_cast<const i32x4 *>(x + t * 2048 + 16 * (g ^ turn));
+                f[t & 1][1] = *reinterpret_cast<const i32x4 *>(x + t * 2048 + 16 * ((4 + g) ^ turn));
+                xs[t & 1] = (int)scale_of(b.s, wt * 16 * TT + 16 * t + n16, g);
             };
             take(0);
 #pragma unroll
@@ -265,52 +282,110 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearDims d, Linea
                 if (t + 1 < TT) take(t + 1);
 #pragma unroll
                 for (int r = 0; r < RT; ++r)
-                    acc[r][t] = mma_8bit(wt.w[r], wt.s[r], f[t & 1][0], f[t & 1][1], b[t & 1], acc[r][t]);
+                    acc[r][t] = mma_8bit(wf[r], (int)ws[r][0], f[t & 1][0], f[t & 1][1], xs[t & 1], acc[r][t]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else if constexpr (MODE == kSixteen) {
+            // lane group g takes K = 8 g .. 8 g + 7 of a block, a block an instruction
+            uint32_t wf[RT][2];
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) wf[r][i] = *reinterpret_cast<const uint32_t *>(w + r * (256 * CW) + 16 * i + 4 * g);
+            // (fragments of the tokens are read AHEAD before they are multiplied)
+            #ifndef AH
+#define AH 3
+#endif
+            constexpr int AHEAD = AH;
+            bf16x8 f[AHEAD + 1];
+            auto take = [&](int k) {
+                f[k % (AHEAD + 1)] = *reinterpret_cast<const bf16x8 *>(x + k % TT * 2048 + 16 * ((4 * (k / TT) + g) ^ turn));
+            };
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) take(k);
+            bf16x8 wv[RT];
+#pragma unroll
+            for (int k = 0; k < 2 * TT; ++k) {
+                if (k + AHEAD < 2 * TT) take(k + AHEAD);
+                if (k % TT == 0)
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) wv[r] = widen_codes(wf[r][k / TT], ws[r][k / TT]);
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+                    acc[r][k % TT] = Mma<bf16>::run(wv[r], f[k % (AHEAD + 1)], acc[r][k % TT]);
                 __builtin_amdgcn_sched_barrier(0);
             }
         } else {
+            // lane group g takes block g, 8 values an instruction
+            i32x4 wf[RT];
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+                wf[r] = *reinterpret_cast<const i32x4 *>(w + r * (256 * CW) + 16 * g);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                bf16x8 w[RT];
+                bf16x8 wv[RT];
 #pragma unroll
-                for (int r = 0; r < RT; ++r) w[r] = widen_codes((uint32_t)wt.w[r][i], (uint32_t)wt.s[r]);
+                for (int r = 0; r < RT; ++r) wv[r] = widen_codes((uint32_t)wf[r][i], ws[r][0]);
 #pragma unroll
                 for (int t = 0; t < TT; ++t) {
-                    bf16x8 v;
-                    if constexpr (MODE == kSixteen)
-                        v = *reinterpret_cast<const bf16x8 *>(xl + 16 * t * PITCH + 16 * ((4 * g + i) ^ turn));
-                    else {
-                        const uint32_t b = xs[4 * (16 * t + n16) + g];
-                        v = widen_8bit(*reinterpret_cast<const u32x2 *>(
-                                           xl + 16 * t * PITCH + 16 * ((2 * g + (i >> 1)) ^ turn) + 8 * (i & 1)),
-                                       __uint_as_float(b << 23));
-                    }
+                    const uint32_t xs = scale_of(b.s, wt * 16 * TT + 16 * t + n16, g);
+                    const bf16x8 v = widen_8bit(*reinterpret_cast<const u32x2 *>(
+                                                    x + t * 2048 + 16 * ((2 * g + (i >> 1)) ^ turn) + 8 * (i & 1)),
+                                                __uint_as_float(xs << 23));
 #pragma unroll
-                    for (int r = 0; r < RT; ++r) acc[r][t] = Mma<bf16>::run(w[r], v, acc[r][t]);
+                    for (int r = 0; r < RT; ++r) acc[r][t] = Mma<bf16>::run(wv[r], v, acc[r][t]);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
     };
-    Stage wa, wb;
-    request(0, xa, wa);
-    deposit(wa, sa);
-    __syncthreads();
+
+    auto multiply = [&](const Buffer &b) {
+#pragma unroll
+        for (int u = 0; u < NSUB / WK; ++u) multiply_step(b.step[u * WK + wk]);
+    };
+
+    // the stage in buffer I of a round of NBUF from `s` on
     int s = 0;
-    for (; s + 2 <= stages; s += 2) {
-        request(s + 1, xb, wb);
-        multiply(xa, sa, wa);
-        deposit(wb, sb);
+    auto stage = [&](auto I) {
+        constexpr int i = decltype(I)::value;
+        request(s + i + NBUF - 1, buffer<Buffer, (i + NBUF - 1) % NBUF>());
+        multiply(buffer<Buffer, i>());
+        wait_and_meet<(NBUF - 2) * NSUB * LOADS>();
+    };
+    auto last = [&](auto I) {
+        if (s + decltype(I)::value < stages) multiply(buffer<Buffer, decltype(I)::value>());
+    };
+    each<NBUF - 1>([&](auto I) { request(decltype(I)::value, buffer<Buffer, decltype(I)::value>()); });
+    wait_and_meet<(NBUF - 2) * NSUB * LOADS>();
+    for (; s + NBUF <= stages; s += NBUF) each<NBUF>(stage);
+    wait_and_meet<0>();
+    each<NBUF - 1>(last);
+
+    if constexpr (WK > 1) {
+        // the waves that took other steps of the same tile, in order
+        __shared__ f32x4 part[WK - 1][WT * WN][RT * TT][64];
+        if (wk > 0)
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int t = 0; t < TT; ++t) part[wk - 1][wave % (WT * WN)][r * TT + t][lane] = acc[r][t];
         __syncthreads();
-        request(s + 2, xa, wa);
-        multiply(xb, sb, wb);
-        deposit(wa, sa);
-        __syncthreads();
+        if (wk > 0) return;
+#pragma unroll
+        for (int k = 0; k < WK - 1; ++k)
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    const f32x4 o = part[k][wave % (WT * WN)][r * TT + t][lane];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[r][t][e] += o[e];
+                }
     }
-    if (s < stages) multiply(xa, sa, wa);
 
     TO *const out = static_cast<TO *>(a.out);
-    const int n = n0 + wave * 16 * RT + 4 * RT * g;
+    const int n = n0 + wn * 16 * RT + 4 * RT * g;
     float bias[4 * RT];
 #pragma unroll
     for (int e = 0; e < 4 * RT; ++e) bias[e] = a.bias && n + e < d.N ? a.bias[n + e] : 0.0f;
@@ -319,7 +394,7 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearDims d, Linea
                                                 (VE * sizeof(TO)) == 0;
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-        const int tok = t0 + 16 * t + n16;
+        const int tok = t0 + wt * 16 * TT + 16 * t + n16;
         if (tok >= d.T) continue;
         float y[4 * RT];
 #pragma unroll
@@ -344,52 +419,90 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearDims d, Linea
 
 size_t linear_workspace(const LinearDims &) { return 0; }
 
-// Which kernel, and its tile.
-struct LinearPlan {
-    bool tile;
-    int mode;
-    const char *name;
-};
-static LinearPlan linear_plan(const LinearDims &d) {
-    LinearPlan p;
-    // float32 results of 8-bit rows come from widened values
-    p.mode = !d.e4m3 ? kSixteen : d.out_bf16 ? kEight : kWidened;
-    p.tile = d.T > 64;
-    p.name = p.tile ? "tile" : "split";
-    return p;
+static LinearMode linear_mode(const LinearDims &d) {
+    // float32 results of 8-bit rows come from widened values: the 8-bit instruction cuts the products of
+    // 32 values off at 2^-13 of the largest, 4e-6 of a result's size, which bfloat16 does not see
+    return !d.e4m3 ? kSixteen : d.out_bf16 ? kEight : kWidened;
 }
-const char *linear_kernel_name(const LinearDims &d) { return linear_plan(d).name; }
 
-template <int MODE, int TT, int RT, typename TO>
+// The tiles that are built. One is taken by its estimated time on the CU that gets the most of
+// them: its bytes, its products at the rate that the tile reached on 4096 tokens, 4096 to 18560
+// (TFLOP/s of 8-bit and bfloat16 rows; the whole chip), or its steps at the time of one; and a
+// time a round of blocks. On 105 sizes (1 to 4096 tokens, 512 to 8192 values, 300 to 18560 outputs)
+// the tile so taken was on average 0.6 % (8 bits) and 1.4 % (bfloat16) slower than the best of them, at
+// most 11 and 19 %.
+struct Tile {
+    int tokens, rows, per_cu, steps;      // steps of 128 (bfloat16: 64) values a stage
+    double rate8, rate16;
+};
+static constexpr Tile kTiles[] = {
+    {16, 16, 2, 4, 134, 68}, {16, 32, 2, 1, 366, 202}, {32, 32, 2, 4, 408, 213}, {64, 64, 2, 2, 899, 584},
+    {128, 128, 2, 1, 1767, 1003}, {128, 256, 1, 1, 2008, 1270}, {256, 256, 1, 1, 2227, 1309}};
+static const char *const kTileNames[] = {"16x16", "16x32", "32x32", "64x64", "128x128", "128x256", "256x256"};
+
+static int linear_tile_of(const LinearDims &d) {
+    const bool wide = !d.e4m3;            // bfloat16 rows (also for the pace of widened ones)
+    int best = 0;
+    double least = 0;
+    for (int i = 0; i < (int)(sizeof kTiles / sizeof *kTiles); ++i) {
+        const Tile &t = kTiles[i];
+        const int64_t blocks = (int64_t)((d.T + t.tokens - 1) / t.tokens) * ((d.N + t.rows - 1) / t.rows);
+        const double most = (double)((blocks + 255) / 256);       // of a CU
+        const int per_cu = wide && i == 5 ? 2 : t.per_cu;
+        const double rounds = (double)(((int64_t)most + per_cu - 1) / per_cu);
+        const double bytes = (double)d.K * ((d.T < t.tokens ? d.T : t.tokens) * (wide ? 2 : 1) + t.rows * 0.53);
+        const double flops = 2.0 * t.tokens * t.rows * d.K;
+        const double stages = d.K / (wide ? 64.0 : 128.0) / t.steps;
+        // microseconds
+        const double by_bytes = most * bytes / (wide ? 6.95e4 : 4.47e4);
+        const double by_products = most * flops * 256e-6 / (wide ? t.rate16 * 0.817 : t.rate8 * 0.477);
+        const double by_stages = rounds * stages * (wide ? 0.202 * (1 + 0.189 * t.steps) : 0.2 * (1 + 0.371 * t.steps));
+        double time = by_bytes > by_products ? by_bytes : by_products;
+        time = (time > by_stages ? time : by_stages) + rounds * (wide ? 3.8 : 0.743);
+        if (i == 0 || time < least) {
+            least = time;
+            best = i;
+        }
+    }
+    return best;
+}
+const char *linear_kernel_name(const LinearDims &d) { return kTileNames[linear_tile_of(d)]; }
+
+template <int MODE, int WT, int WN, int WK, int TT, int RT, int NSUB, int NBUF, bool WORDS, int PERCU, typename TO>
 static void linear_tile(const LinearDims &d, const LinearArgs &a, hipStream_t st) {
-    const int tt = (d.T + 16 * TT - 1) / (16 * TT), nt = (d.N + 64 * RT - 1) / (64 * RT);
-    hipLaunchKernelGGL((linear_tile_kernel<MODE, TT, RT, TO>), dim3((unsigned)(tt * nt)), dim3(256), 0, st, d, a, tt,
-                       nt);
+    const int tt = (d.T + 16 * TT * WT - 1) / (16 * TT * WT), nt = (d.N + 16 * RT * WN - 1) / (16 * RT * WN);
+    hipLaunchKernelGGL((linear_tile_kernel<MODE, WT, WN, WK, TT, RT, NSUB, NBUF, WORDS, PERCU, TO>),
+                       dim3((unsigned)(tt * nt)), dim3(64 * WT * WN * WK), 0, st, d, a, tt, nt);
 }
-template <bool E4M3, typename TO>
-static void linear_split(const LinearDims &d, const LinearArgs &a, hipStream_t st) {
-    const unsigned nb = (unsigned)((d.N + 15) / 16);
-    if (d.T <= 16)
-        hipLaunchKernelGGL((linear_kernel<E4M3, 1, 1, TO>), dim3(nb, 1), dim3(256), 0, st, d, a);
-    else
-        hipLaunchKernelGGL((linear_kernel<E4M3, 4, 2, TO>), dim3((unsigned)((d.N + 31) / 32), (unsigned)((d.T + 63) / 64)),
-                           dim3(256), 0, st, d, a);
-}
-template <int MODE, typename TO>
-static void linear_t(const LinearDims &d, const LinearArgs &a, const LinearPlan &p, hipStream_t st) {
-    if (p.tile) linear_tile<MODE, 8, 4, TO>(d, a, st);
-    else linear_split<MODE != kSixteen, TO>(d, a, st);
+template <int MODE, bool WORDS, typename TO>
+static void linear_t(const LinearDims &d, const LinearArgs &a, hipStream_t st) {
+    // (blocks a CU that the buffers leave room for)
+    constexpr int two = WORDS || MODE == kSixteen ? 2 : 1;
+    switch (linear_tile_of(d)) {
+    case 0: return linear_tile<MODE, 1, 1, 4, 1, 1, 4, 3, WORDS, 2, TO>(d, a, st);
+    case 1: return linear_tile<MODE, 1, 2, 1, 1, 1, 1, 8, WORDS, 2, TO>(d, a, st);
+    case 2: return linear_tile<MODE, 1, 1, 4, 2, 2, 4, 3, WORDS, 1, TO>(d, a, st);
+    case 3: return linear_tile<MODE, 1, 4, 1, 4, 1, 2, 3, WORDS, two, TO>(d, a, st);
+    case 4: return linear_tile<MODE, 2, 4, 1, 4, 2, 1, 3, WORDS, two, TO>(d, a, st);
+    case 5:
+        if constexpr (MODE == kSixteen) return linear_tile<MODE, 1, 4, 1, 8, 4, 1, 2, WORDS, 2, TO>(d, a, st);
+        else return linear_tile<MODE, 2, 4, 1, 4, 4, 1, 3, WORDS, 1, TO>(d, a, st);
+    default:
+        // (scales of a byte a word leave room for two buffers)
+        return linear_tile<MODE, 2, 4, 1, 8, 4, 1, WORDS || MODE == kSixteen ? 3 : 2, WORDS, 1, TO>(d, a, st);
+    }
 }
 
 void launch_linear(const LinearDims &d, const LinearArgs &a, void *, void *stream)
 {
     if (d.T <= 0) return;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-    const LinearPlan p = linear_plan(d);
-    if (p.mode == kEight) linear_t<kEight, bf16>(d, a, p, st);
-    else if (p.mode == kWidened) linear_t<kWidened, float>(d, a, p, st);
-    else if (d.out_bf16) linear_t<kSixteen, bf16>(d, a, p, st);
-    else linear_t<kSixteen, float>(d, a, p, st);
+    const LinearMode m = linear_mode(d);
+    const bool words = d.K % 128 == 0 && ((uintptr_t)a.x_scale | (uintptr_t)a.w_scale) % 4 == 0;
+    if (m == kEight) words ? linear_t<kEight, true, bf16>(d, a, st) : linear_t<kEight, false, bf16>(d, a, st);
+    else if (m == kWidened) words ? linear_t<kWidened, true, float>(d, a, st) : linear_t<kWidened, false, float>(d, a, st);
+    else if (d.out_bf16) linear_t<kSixteen, false, bf16>(d, a, st);
+    else linear_t<kSixteen, false, float>(d, a, st);
 }
 
 // ---------------------------------------------------------------------------

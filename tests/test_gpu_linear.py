@@ -43,10 +43,11 @@ def run(codes, ws, x, xs, N, to, bias=None, out=None):
     return out
 
 
-def check(out, xv, w, bias=None):
+def check(out, xv, w, bias=None, xt=BF):
     y, mag = os_.linear(xv, w, bias)
+    cut = os_.cut_products(xv, w) if xt == E4 and out.dtype == BF else 0.0
     got = out.cpu().double().numpy()
-    bad = ~(np.abs(got - y) <= os_.linear_tolerance(y, mag, w.shape[1], out.dtype))
+    bad = ~(np.abs(got - y) <= os_.linear_tolerance(y, mag, w.shape[1], out.dtype, cut))
     assert not bad.any(), (int(bad.sum()), float(np.nanmax(np.abs(got - y))))
 
 
@@ -61,10 +62,47 @@ SIZES = [(1, 32, 1), (1, 2560, 100), (2, 96, 17), (3, 160, 33), (5, 1056, 64), (
 def test_whole_numbers(T, K, N, xt):
     codes, ws, x, xs, w, xv = make(T + K + N, T, K, N, xt, True)
     y, mag = os_.linear(xv, w)
-    # multiples of 2^-3 (8-bit rows: 2^-4 with their own scales) below 2^20: every partial sum is exact
+    # multiples of 2^-3 (8-bit rows: 2^-4 with their own scales) below 2^20: every partial sum is exact;
+    # within a block of 32 products the largest is at most 48 times the smallest
     assert mag.max() < 2.0 ** 20
-    got = run(codes, ws, x, xs, N, F32).cpu().double().numpy()
-    assert np.array_equal(got, y), np.argwhere(got != y)[:5]
+    for to in (F32, BF):
+        got = run(codes, ws, x, xs, N, to).cpu()
+        assert torch.equal(got, torch.from_numpy(y).to(to)), (to, np.argwhere(got.double().numpy() != y)[:5])
+
+
+# a size for each tile that is built (per type of the rows), K ending inside a step or not
+TILES = {"16x16": (5, 4096, 300), "16x32": (16, 512, 9000), "32x32": (64, 8192, 4000), "64x64": (64, 512, 9000),
+         "128x128": (300, 256, 9000), "128x256": (384, 640, 18560), "256x256": (2048, 256, 16000)}
+
+
+@pytest.mark.parametrize("xt", [BF, E4])
+@pytest.mark.parametrize("to", [BF, F32])
+@pytest.mark.parametrize("tile", list(TILES))
+@pytest.mark.parametrize("odd", [0, 1])
+def test_every_tile(tile, xt, to, odd):
+    T, K, N = TILES[tile]
+    if odd:
+        T, K, N = T - 3, K - 96 if K > 512 else K + 32, N - 7
+    p = ssd.make_linear_problem(T, K, N, xt, to)
+    took = ssd.linear_w4_kernel(p)
+    g = torch.Generator(DEV).manual_seed(K)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, dtype=U8, device=DEV)
+    ws = torch.randint(126, 129, (N, K // 32), generator=g, dtype=U8, device=DEV)
+    x = torch.randint(-4, 5, (T, K), generator=g, device=DEV).float()
+    xs = torch.randint(126, 129, (T, K // 32), generator=g, dtype=U8, device=DEV) if xt == E4 else None
+    out = torch.empty(T, N, dtype=to, device=DEV)
+    ssd.linear_w4(p, x.to(xt), codes, ws, out, xs, None, ssd.alloc_linear_workspace(p, DEV))
+    # the same sums in float32, exact in any order: whole multiples of 2^-4 below 2^20
+    lut = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], device=DEV)
+    c = torch.stack([codes & 15, codes >> 4], -1).flatten(1).int()
+    w = torch.where(c >= 8, -1.0, 1.0) * lut[c & 7] * torch.exp2(ws.float() - 127).repeat_interleave(32, 1)
+    if xt == E4:
+        x = x * torch.exp2(xs.float() - 127).repeat_interleave(32, 1)
+    want = torch.cat([(x[a:a + 512].double() @ w.double().t()) for a in range(0, T, 512)])
+    assert float((x.abs().amax(0) * w.abs().amax(0)).sum()) < 2.0 ** 20
+    assert torch.equal(out, want.to(to)), took
+    if not odd:
+        assert took == tile
 
 
 @pytest.mark.parametrize("xt", [BF, E4])
@@ -73,8 +111,8 @@ def test_whole_numbers(T, K, N, xt):
 def test_values(T, K, N, xt, to):
     codes, ws, x, xs, w, xv = make(T * K, T, K, N, xt, False)
     bias = torch.randn(N, generator=torch.Generator().manual_seed(1))
-    check(run(codes, ws, x, xs, N, to), xv, w)
-    check(run(codes, ws, x, xs, N, to, bias), xv, w, bias)
+    check(run(codes, ws, x, xs, N, to), xv, w, xt=xt)
+    check(run(codes, ws, x, xs, N, to, bias), xv, w, bias, xt)
 
 
 @pytest.mark.parametrize("xt", [BF, E4])
@@ -102,7 +140,7 @@ def test_odd_output_rows(T, xt):
     codes, ws, x, xs, w, xv = make(T, T, K, N, xt, True)
     buf = torch.full((T * N + 3,), 7.0, dtype=BF, device=DEV)
     run(codes, ws, x, xs, N, BF, out=buf[1:1 + T * N].view(T, N))
-    check(buf[1:1 + T * N].view(T, N), xv, w)
+    check(buf[1:1 + T * N].view(T, N), xv, w, xt=xt)
     assert float(buf[0]) == 7 and bool((buf[-2:] == 7).all())
 
 
@@ -213,7 +251,7 @@ def test_streams_graphs_and_repeats(T, xt):
     go = lambda: ssd.linear_w4(p, d[2], d[0], d[1], out, d[3], None, wsp)       # noqa: E731
     go()
     want = out.clone()
-    check(want, xv, w)
+    check(want, xv, w, xt=xt)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
