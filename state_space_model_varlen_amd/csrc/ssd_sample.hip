@@ -10,11 +10,24 @@ namespace ssd {
 // ---------------------------------------------------------------------------
 // Probabilities.
 
+// A row (short ones) or a part of a row by one block, its logits kept in
+// registers from their only load. A row that one block cannot hold, or that
+// would leave the chip idle, is cut into parts: the first launch leaves each
+// part's largest logit and sum, the second joins them and writes. Bound by the
+// bytes of logits (read twice, the second time mostly from the last-level cache)
+// and probabilities.
 struct Peak {
-    float m;    // the largest logit so far (-infinity: none)
+    float m;    // the largest logit (-infinity: none)
     float s;    // sum of exp((x - m) / T)
     int at;     // first place of the largest
+    int pad;
 };
+__device__ __forceinline__ void take_larger(Peak &k, float m, int at) {
+    if (m > k.m || (m == k.m && at < k.at)) {
+        k.m = m;
+        k.at = at;
+    }
+}
 
 // exp(d / T) of d <= 0, with c = log2(e) / T in two parts: the product's
 // rounding, which would be d 2^-24 in the exponent, is put back.
@@ -22,91 +35,179 @@ struct InvTemp {
     float hi, lo;
     __device__ __forceinline__ explicit InvTemp(float t) {
         const double c = 1.4426950408889634 / (double)t;
-        hi = (float)c;
-        lo = (float)(c - (double)hi);
-        if (!(fabsf(hi) < __builtin_inff())) lo = 0.0f;
+        hi = c < 3.0e38 ? (float)c : 3.0e38f;          // (a difference of 0 times infinity is no number)
+        lo = c < 3.0e38 ? (float)(c - (double)hi) : 0.0f;
     }
     __device__ __forceinline__ float operator()(float d) const {
         const float y = d * hi;
         const float rest = fmaf(d, hi, -y) + d * lo;
         const float e = __builtin_amdgcn_exp2f(y);
-        const float r = e + e * (rest * kLn2);
-        return fabsf(y) < 1000.0f ? r : e;
+        return y > -1000.0f ? fmaf(e, rest * kLn2, e) : e;      // (NaN passes through e)
     }
 };
 
-template <typename T>
-__global__ __launch_bounds__(1024) void probs_kernel(int V, int per_req, const T *__restrict__ logits,
-                                                     int64_t ls, const float *__restrict__ temperature,
-                                                     float *__restrict__ probs, int64_t ps)
-{
-    __shared__ Peak part[16];
-    const int64_t row = blockIdx.x;
-    const T *const x = logits + row * ls;
-    float *const p = probs + row * ps;
-    const float t = temperature ? temperature[row / per_req] : 1.0f;
-    const bool greedy = !(t > 0.0f);
-    const InvTemp inv(greedy ? 1.0f : t);
-    Peak k{-__builtin_inff(), 0.0f, V};
-    for (int i = (int)threadIdx.x; i < V; i += 1024) {
-        const float v = to_f32(x[i]);
-        if (v > k.m) {
-            k.m = v;
-            k.at = i;
-        }
-    }
+// A thread's N vectors of 16 bytes, `threads` vectors apart; elements past the row's end are
+// -infinity. Rows start on their element.
+template <typename T, int N> struct Logits {
+    static constexpr int E = 16 / sizeof(T);
+    typedef T vec __attribute__((ext_vector_type(E)));
+    typedef vec any __attribute__((aligned(sizeof(T))));
+    vec v[N];
+    __device__ __forceinline__ void load(const T *x, int from, int end, int threads) {
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        const float m = __shfl_xor(k.m, off, kWave);
-        const int at = __shfl_xor(k.at, off, kWave);
-        if (m > k.m || (m == k.m && at < k.at)) {
-            k.m = m;
-            k.at = at;
+        for (int j = 0; j < N; ++j) {
+            const int i = from + (j * threads + (int)threadIdx.x) * E;
+            if (i + E <= end) v[j] = *reinterpret_cast<const any *>(x + i);
+            else
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[j][e] = i + e < end ? x[i + e] : from_f32<T>(-__builtin_inff());
         }
     }
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = k;
-    __syncthreads();
-    for (int i = 0; i < 16; ++i) {
-        const Peak o = part[i];
-        if (o.m > k.m || (o.m == k.m && o.at < k.at)) k = o;
+    template <typename F> __device__ __forceinline__ void each(int from, int threads, F f) const {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int e = 0; e < E; ++e) f(from + (j * threads + (int)threadIdx.x) * E + e, to_f32(v[j][e]), j, e);
     }
+};
+
+// The part's peak and sum, the same in every thread of the block.
+template <typename T, int N, int W>
+__device__ __forceinline__ Peak block_peak(const Logits<T, N> &l, int from, const InvTemp &inv) {
+    __shared__ Peak part[W];
+    __shared__ float sums[W];
+    Peak k{-__builtin_inff(), 0.0f, 0x7fffffff, 0};
+    l.each(from, 64 * W, [&](int i, float v, int, int) {
+        // (places rise: an equal one later does not replace)
+        k.at = v > k.m ? i : k.at;
+        k.m = v > k.m ? v : k.m;
+    });
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) take_larger(k, __shfl_xor(k.m, off, kWave), __shfl_xor(k.at, off, kWave));
+    const int wave = (int)threadIdx.x >> 6, lane = threadIdx.x & 63;
+    if (lane == 0) part[wave] = k;
     __syncthreads();
-    if (greedy) {
-        for (int i = (int)threadIdx.x; i < V; i += 1024) p[i] = i == k.at ? 1.0f : 0.0f;
-        return;
-    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) take_larger(k, part[i].m, part[i].at);
     const float top = k.m == -__builtin_inff() ? 0.0f : k.m;
     float s = 0.0f;
-    for (int i = (int)threadIdx.x; i < V; i += 1024) {
-        const float v = to_f32(x[i]);
-        s += v == -__builtin_inff() ? 0.0f : inv(v - top);
-    }
+    l.each(from, 64 * W, [&](int, float v, int, int) { s += v == -__builtin_inff() ? 0.0f : inv(v - top); });
     s = group_sum(s, 64);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6].s = s;
+    if (lane == 0) sums[wave] = s;
     __syncthreads();
-    s = 0.0f;
-    for (int i = 0; i < 16; ++i) s += part[i].s;
-    const float r = s == 0.0f ? 0.0f : 1.0f / s;
-    for (int i = (int)threadIdx.x; i < V; i += 1024) {
-        const float v = to_f32(x[i]);
-        p[i] = v == -__builtin_inff() ? 0.0f * s : inv(v - top) * r;
+    k.s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) k.s += sums[i];
+    return k;
+}
+
+template <typename T, int N, int W>
+__device__ __forceinline__ void write_probs(const Logits<T, N> &l, int from, int end, const Peak &k, bool greedy,
+                                            const InvTemp &inv, float *p) {
+    constexpr int E = Logits<T, N>::E;
+    typedef float vec4 __attribute__((ext_vector_type(4)));
+    typedef vec4 any4 __attribute__((aligned(4)));
+    const float top = k.m == -__builtin_inff() ? 0.0f : k.m, r = k.s == 0.0f ? 0.0f : 1.0f / k.s;
+    const float none = 0.0f * k.s;                  // what a masked logit gets: 0, or NaN with its row
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int i = from + (j * 64 * W + (int)threadIdx.x) * E;
+        float y[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float v = to_f32(l.v[j][e]);
+            y[e] = greedy ? (i + e == k.at ? 1.0f : 0.0f) : v == -__builtin_inff() ? none : inv(v - top) * r;
+        }
+        if (i + E <= end)
+#pragma unroll
+            for (int e = 0; e < E; e += 4) {
+                const vec4 o = {y[e], y[e + 1], y[e + 2], y[e + 3]};
+                *reinterpret_cast<any4 *>(p + i + e) = o;
+            }
+        else
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (i + e < end) p[i + e] = y[e];
     }
 }
 
-size_t probs_workspace(const ProbsDims &) { return 0; }
+// STEP 0: whole rows; 1: the parts' peaks; 2: parts joined and written.
+template <typename T, int N, int W, int STEP>
+__global__ __launch_bounds__(64 * W) void probs_kernel(int V, int per_req, const T *__restrict__ logits, int64_t ls,
+                                                       const float *__restrict__ temperature,
+                                                       float *__restrict__ probs, int64_t ps, int parts,
+                                                       Peak *__restrict__ peaks)
+{
+    constexpr int SPAN = 64 * W * Logits<T, N>::E * N;
+    const int part = STEP == 0 ? 0 : (int)blockIdx.x % parts;
+    const int64_t row = STEP == 0 ? blockIdx.x : blockIdx.x / parts;
+    const int from = part * SPAN, end = V - from < SPAN ? V : from + SPAN;
+    Logits<T, N> l;
+    l.load(logits + row * ls, from, end, 64 * W);
+    const float t = temperature ? temperature[row / per_req] : 1.0f;
+    const bool greedy = !(t > 0.0f);
+    const InvTemp inv(greedy ? 1.0f : t);
+    Peak k;
+    if constexpr (STEP < 2) {
+        k = block_peak<T, N, W>(l, from, inv);
+        if constexpr (STEP == 1) {
+            if (threadIdx.x == 0) peaks[blockIdx.x] = k;
+            return;
+        }
+    } else {
+        // every wave joins the row's parts by itself
+        const int lane = threadIdx.x & 63;
+        const Peak *const mine = peaks + row * parts;
+        k = Peak{-__builtin_inff(), 0.0f, 0x7fffffff, 0};
+        for (int i = lane; i < parts; i += 64) take_larger(k, mine[i].m, mine[i].at);
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) take_larger(k, __shfl_xor(k.m, off, kWave), __shfl_xor(k.at, off, kWave));
+        float s = 0.0f;
+        for (int i = lane; i < parts; i += 64) {
+            const Peak o = mine[i];
+            s += o.m == -__builtin_inff() ? o.s : o.s * inv(o.m - k.m);
+        }
+        k.s = group_sum(s, 64);
+    }
+    write_probs<T, N, W>(l, from, end, k, greedy, inv, probs + row * ps);
+}
+
+// Rows of up to 8 K logits (bfloat16: 16 K) are taken whole, others in parts of 4 K (8 K).
+template <typename T> static constexpr int probs_span() { return 256 * Logits<T, 4>::E * 4; }
+static int probs_parts(const ProbsDims &d) {
+    const int span = d.bf16 ? probs_span<bf16>() : probs_span<float>();
+    return d.V <= 2 * span ? 0 : (d.V + span - 1) / span;
+}
+size_t probs_workspace(const ProbsDims &d) { return (size_t)d.R * d.T * probs_parts(d) * sizeof(Peak); }
+
+template <typename T>
+static void probs_t(const ProbsDims &d, const void *logits, const float *temperature, float *probs, Peak *peaks,
+                    hipStream_t st)
+{
+    const unsigned rows = (unsigned)(d.R * d.T);
+    const T *const x = static_cast<const T *>(logits);
+    constexpr int E = Logits<T, 1>::E;
+    const int parts = probs_parts(d);
+    if (parts) {
+        hipLaunchKernelGGL((probs_kernel<T, 4, 4, 1>), dim3(rows * parts), dim3(256), 0, st, d.V, d.T, x, d.ls,
+                           temperature, probs, d.ps, parts, peaks);
+        hipLaunchKernelGGL((probs_kernel<T, 4, 4, 2>), dim3(rows * parts), dim3(256), 0, st, d.V, d.T, x, d.ls,
+                           temperature, probs, d.ps, parts, peaks);
+    } else if (d.V <= 256 * E)
+        hipLaunchKernelGGL((probs_kernel<T, 1, 4, 0>), dim3(rows), dim3(256), 0, st, d.V, d.T, x, d.ls, temperature,
+                           probs, d.ps, 1, peaks);
+    else
+        hipLaunchKernelGGL((probs_kernel<T, 2, 16, 0>), dim3(rows), dim3(1024), 0, st, d.V, d.T, x, d.ls, temperature,
+                           probs, d.ps, 1, peaks);
+}
 
 void launch_probs(const ProbsDims &d, const void *logits, const float *temperature, float *probs,
-                  void *, void *stream)
+                  void *workspace, void *stream)
 {
-    const int rows = d.R * d.T;
-    if (rows <= 0) return;
+    if ((int64_t)d.R * d.T <= 0) return;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-    if (d.bf16)
-        hipLaunchKernelGGL(probs_kernel<bf16>, dim3((unsigned)rows), dim3(1024), 0, st, d.V, d.T,
-                           static_cast<const bf16 *>(logits), d.ls, temperature, probs, d.ps);
-    else
-        hipLaunchKernelGGL(probs_kernel<float>, dim3((unsigned)rows), dim3(1024), 0, st, d.V, d.T,
-                           static_cast<const float *>(logits), d.ls, temperature, probs, d.ps);
+    if (d.bf16) probs_t<bf16>(d, logits, temperature, probs, static_cast<Peak *>(workspace), st);
+    else probs_t<float>(d, logits, temperature, probs, static_cast<Peak *>(workspace), st);
 }
 
 // ---------------------------------------------------------------------------
@@ -118,12 +219,12 @@ void launch_probs(const ProbsDims &d, const void *logits, const float *temperatu
 // step, far less than the distance of a uniform number of 24 bits from a
 // border that it does not lie on.
 //
-// Two launches: the weights of each segment of 4096 entries are summed (one
-// block a segment and request), then one block a request finds the segment
-// that the draw falls into and goes through its entries. Bound by the rows'
-// bytes, for few requests by the chain draft -> its probabilities -> row.
+// Two launches: the weights of every 2048 entries are summed (a wave each), then
+// one block a request finds the 2048 that the draw falls into and goes through
+// their entries. Bound by the rows' bytes, for few requests by the chain draft ->
+// its probabilities -> row.
 
-constexpr int kSeg = 4096, kSegThreads = 256, kPerThread = kSeg / kSegThreads;
+constexpr int kGrain = 2048, kPickThreads = 256, kPerThread = kGrain / kPickThreads;
 
 struct Decision {
     int count, accepted;     // drafts of the request, and how many of them stand
@@ -169,130 +270,174 @@ struct Row {
     }
 };
 
-__device__ __forceinline__ double shfl_xor64(double v, int off) { return __shfl_xor(v, off, kWave); }
+// 4 entries from v on (zeros past the row's end); rows start on their element.
+__device__ __forceinline__ void load_entries(const float *row, int v, int V, float *x) {
+    typedef float vec4 __attribute__((ext_vector_type(4)));
+    typedef vec4 any4 __attribute__((aligned(4)));
+    if (v + 4 <= V) {
+        const vec4 q = *reinterpret_cast<const any4 *>(row + v);
+        x[0] = q[0]; x[1] = q[1]; x[2] = q[2]; x[3] = q[3];
+    } else
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = v + i < V ? row[v + i] : 0.0f;
+}
 
-__global__ __launch_bounds__(kSegThreads) void verify_sums_kernel(VerifyDims d, VerifyArgs a, int segs,
-                                                                  double *__restrict__ sums)
+__global__ __launch_bounds__(256) void verify_sums_kernel(VerifyDims d, VerifyArgs a, int grains,
+                                                          double *__restrict__ sums)
 {
-    __shared__ double part[2][kSegThreads / 64];
-    const int seg = blockIdx.x, r = blockIdx.y;
+    const int lane = threadIdx.x & 63, grain = (int)blockIdx.x * 4 + ((int)threadIdx.x >> 6), r = blockIdx.y;
+    if (grain >= grains) return;
     const Decision k = decide(d, a, r);
     const Row row(d, a, r, k);
+    constexpr int VECS = kGrain / 256;
+    float p[VECS][4], q[VECS][4] = {};
+#pragma unroll
+    for (int j = 0; j < VECS; ++j) load_entries(row.p, grain * kGrain + (j * 64 + lane) * 4, d.V, p[j]);
+    if (row.q)
+#pragma unroll
+        for (int j = 0; j < VECS; ++j) load_entries(row.q, grain * kGrain + (j * 64 + lane) * 4, d.V, q[j]);
     double sw = 0.0, sp = 0.0;
-    for (int j = 0; j < kPerThread; ++j) {
-        const int v = seg * kSeg + j * kSegThreads + (int)threadIdx.x;
-        if (v < d.V) {
-            double w, p;
-            row.weigh(v, row.p[v], row.q ? row.q[v] : 0.0f, w, p);
+#pragma unroll
+    for (int j = 0; j < VECS; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            double w, pl;
+            row.weigh(grain * kGrain + (j * 64 + lane) * 4 + i, p[j][i], q[j][i], w, pl);
             sw += w;
-            sp += p;
+            sp += pl;
         }
-    }
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) {
-        sw += shfl_xor64(sw, off);
-        sp += shfl_xor64(sp, off);
+        sw += __shfl_xor(sw, off, kWave);
+        sp += __shfl_xor(sp, off, kWave);
     }
-    if ((threadIdx.x & 63) == 0) {
-        part[0][threadIdx.x >> 6] = sw;
-        part[1][threadIdx.x >> 6] = sp;
+    if (lane == 0) {
+        sums[((int64_t)r * grains + grain) * 2] = sw;
+        sums[((int64_t)r * grains + grain) * 2 + 1] = sp;
     }
-    __syncthreads();
-    if (threadIdx.x < 2) {
-        double s = 0.0;
-        for (int i = 0; i < kSegThreads / 64; ++i) s += part[threadIdx.x][i];
-        sums[((int64_t)r * segs + seg) * 2 + threadIdx.x] = s;
-    }
-    if (seg == 0) {
-        if (threadIdx.x == 0) a.accepted[r] = k.accepted;
-        for (int i = (int)threadIdx.x; i < d.T; i += kSegThreads)
+    if (grain == 0) {
+        if (lane == 0) a.accepted[r] = k.accepted;
+        for (int i = lane; i < d.T; i += 64)
             if (i != k.accepted)
                 a.out[(int64_t)r * d.T + i] = i < k.accepted ? a.tokens[(int64_t)r * (d.T - 1) + i] : -1;
     }
 }
 
-__global__ __launch_bounds__(kSegThreads) void verify_pick_kernel(VerifyDims d, VerifyArgs a, int segs,
-                                                                  const double *__restrict__ sums)
-{
-    __shared__ double incl[kSegThreads];
-    __shared__ int found, last;
-    const int r = blockIdx.x, tid = threadIdx.x;
-    const Decision k = decide(d, a, r);
-    const Row row(d, a, r, k);
-    const double *const s = sums + (int64_t)r * segs * 2;
-    // every thread adds the segments up in the same order
-    double tw = 0.0, tp = 0.0;
-    for (int i = 0; i < segs; ++i) {
-        tw += s[2 * i];
-        tp += s[2 * i + 1];
+// Inclusive sums over the block's threads, in their order.
+__device__ __forceinline__ double block_scan(double v, double *part) {
+    const int lane = threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const double o = __shfl_up(v, off, kWave);
+        if (lane >= off) v += o;
     }
-    const int which = tw > 0.0 ? 0 : 1;
-    const double total = which ? tp : tw, want = total * (double)a.uniform[(int64_t)r * d.T + d.T - 1];
+    if (lane == 63) part[wave] = v;
+    __syncthreads();
     double before = 0.0;
-    int seg = -1;
-    double seg_before = 0.0;
-    for (int i = 0; i < segs; ++i) {
-        const double w = s[2 * i + which];
-        if (w > 0.0) {                       // (the last one of positive weight, if none passes)
-            seg = i;
-            seg_before = before;
-            if (before + w > want) break;
-        }
-        before += w;
-    }
-    int token = -1;
-    if (seg >= 0) {                          // (the same in every thread)
-        double w[kPerThread], mine = 0.0;
-        const int v0 = seg * kSeg + tid * kPerThread;
-        int lastpos = -1;
-#pragma unroll
-        for (int j = 0; j < kPerThread; ++j) {
-            const int v = v0 + j;
-            double x = 0.0, p = 0.0;
-            if (v < d.V) row.weigh(v, row.p[v], row.q ? row.q[v] : 0.0f, x, p);
-            w[j] = which ? p : x;
-            mine += w[j];
-            if (w[j] > 0.0) lastpos = v;
-        }
-        if (tid == 0) {
-            found = 0x7fffffff;
-            last = -1;
-        }
-        incl[tid] = mine;
-        __syncthreads();
-        for (int off = 1; off < kSegThreads; off <<= 1) {
-            const double o = tid >= off ? incl[tid - off] : 0.0;
-            __syncthreads();
-            incl[tid] += o;
-            __syncthreads();
-        }
-        double c = seg_before + (tid ? incl[tid - 1] : 0.0);
-        int hit = 0x7fffffff;
-#pragma unroll
-        for (int j = 0; j < kPerThread; ++j) {
-            c += w[j];
-            if (w[j] > 0.0 && c > want && hit == 0x7fffffff) hit = v0 + j;
-        }
-        if (hit != 0x7fffffff) atomicMin(&found, hit);
-        if (lastpos >= 0) atomicMax(&last, lastpos);
-        __syncthreads();
-        token = found != 0x7fffffff ? found : last;
-    }
-    if (tid == 0) a.out[(int64_t)r * d.T + k.accepted] = token;
+    for (int i = 0; i < wave; ++i) before += part[i];
+    return before + v;
 }
 
-static int segments(const VerifyDims &d) { return (d.V + kSeg - 1) / kSeg; }
-size_t verify_workspace(const VerifyDims &d) { return (size_t)d.R * segments(d) * 2 * sizeof(double); }
+__global__ __launch_bounds__(kPickThreads) void verify_pick_kernel(VerifyDims d, VerifyArgs a, int grains,
+                                                                   const double *__restrict__ sums)
+{
+    __shared__ double part[3][kPickThreads / 64], start;
+    __shared__ int found[2], last[2];
+    const int r = blockIdx.x, tid = threadIdx.x;
+    if (tid < 2) {
+        found[tid] = 0x7fffffff;
+        last[tid] = -1;
+    }
+    const float uniform = a.uniform[(int64_t)r * d.T + d.T - 1];
+    // the first launch's decision
+    int n = a.count ? a.count[r] : d.T - 1;
+    n = n < 0 ? 0 : (n > d.T - 1 ? d.T - 1 : n);
+    const Decision k{n, a.accepted[r]};
+    const Row row(d, a, r, k);
+    const double *const s = sums + (int64_t)r * grains * 2;
+    // a thread's grains follow one another
+    const int per = (grains + kPickThreads - 1) / kPickThreads, g0 = tid * per;
+    double mw = 0.0, mp = 0.0;
+    for (int i = g0; i < g0 + per && i < grains; ++i) {
+        mw += s[2 * i];
+        mp += s[2 * i + 1];
+    }
+    const double iw = block_scan(mw, part[0]), ip = block_scan(mp, part[1]);
+    double tw = 0.0, tp = 0.0;
+#pragma unroll
+    for (int i = 0; i < kPickThreads / 64; ++i) {
+        tw += part[0][i];
+        tp += part[1][i];
+    }
+    const int which = tw > 0.0 ? 0 : 1;
+    const double want = (which ? tp : tw) * (double)uniform;
+    // the first grain that passes `want`, or the last of positive weight
+    double c = which ? ip - mp : iw - mw;
+    int hit = 0x7fffffff, lastpos = -1;
+    for (int i = g0; i < g0 + per && i < grains; ++i) {
+        const double w = s[2 * i + which];
+        if (w > 0.0) {
+            lastpos = i;
+            if (hit == 0x7fffffff && c + w > want) hit = i;
+        }
+        c += w;
+    }
+    if (hit != 0x7fffffff) atomicMin(&found[0], hit);
+    if (lastpos >= 0) atomicMax(&last[0], lastpos);
+    __syncthreads();
+    const int grain = found[0] != 0x7fffffff ? found[0] : last[0];
+    if (grain < 0) {                         // (the same in every thread)
+        if (tid == 0) a.out[(int64_t)r * d.T + k.accepted] = -1;
+        return;
+    }
+    if (grain >= g0 && grain < g0 + per) {
+        double b = which ? ip - mp : iw - mw;
+        for (int i = g0; i < grain; ++i) b += s[2 * i + which];
+        start = b;
+    }
+    float pv[kPerThread], qv[kPerThread] = {};
+    const int v0 = grain * kGrain + tid * kPerThread;
+#pragma unroll
+    for (int j = 0; j < kPerThread; j += 4) {
+        load_entries(row.p, v0 + j, d.V, pv + j);
+        if (row.q) load_entries(row.q, v0 + j, d.V, qv + j);
+    }
+    double w[kPerThread], mine = 0.0;
+    lastpos = -1;
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+        double x, p;
+        row.weigh(v0 + j, pv[j], qv[j], x, p);
+        w[j] = which ? p : x;
+        mine += w[j];
+        if (w[j] > 0.0) lastpos = v0 + j;
+    }
+    const double incl = block_scan(mine, part[2]);          // (start is written by now)
+    c = start + (incl - mine);
+    hit = 0x7fffffff;
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+        c += w[j];
+        if (w[j] > 0.0 && c > want && hit == 0x7fffffff) hit = v0 + j;
+    }
+    if (hit != 0x7fffffff) atomicMin(&found[1], hit);
+    if (lastpos >= 0) atomicMax(&last[1], lastpos);
+    __syncthreads();
+    if (tid == 0) a.out[(int64_t)r * d.T + k.accepted] = found[1] != 0x7fffffff ? found[1] : last[1];
+}
+
+static int grains_of(const VerifyDims &d) { return (d.V + kGrain - 1) / kGrain; }
+size_t verify_workspace(const VerifyDims &d) { return (size_t)d.R * grains_of(d) * 2 * sizeof(double); }
 
 void launch_verify(const VerifyDims &d, const VerifyArgs &a, void *workspace, void *stream)
 {
     if (d.R <= 0) return;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-    const int segs = segments(d);
+    const int grains = grains_of(d);
     double *const sums = static_cast<double *>(workspace);
-    hipLaunchKernelGGL(verify_sums_kernel, dim3((unsigned)segs, (unsigned)d.R), dim3(kSegThreads), 0, st, d, a,
-                       segs, sums);
-    hipLaunchKernelGGL(verify_pick_kernel, dim3((unsigned)d.R), dim3(kSegThreads), 0, st, d, a, segs, sums);
+    hipLaunchKernelGGL(verify_sums_kernel, dim3((unsigned)((grains + 3) / 4), (unsigned)d.R), dim3(256), 0, st, d, a,
+                       grains, sums);
+    hipLaunchKernelGGL(verify_pick_kernel, dim3((unsigned)d.R), dim3(kPickThreads), 0, st, d, a, grains, sums);
 }
 
 }  // namespace ssd

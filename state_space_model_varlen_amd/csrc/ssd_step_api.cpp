@@ -99,8 +99,9 @@ int probs_dims(const probs_problem *p, ssd::ProbsDims *d)
     if (!stride_of(p->logits_stride, p->vocab, &d->ls) ||
         !stride_of(p->probs_stride, p->vocab, &d->ps))
         return SSD_ERR_SHAPE;
-    // grid limits: rows in one dimension, parts of a row in another
-    if ((int64_t)p->num_reqs * p->tokens_per_req > 0x7fffffLL || p->vocab > (1 << 27))
+    // grid limit: rows times their parts of at least 4096 logits
+    const int64_t rows = (int64_t)p->num_reqs * p->tokens_per_req;
+    if (p->vocab > (1 << 27) || rows > 0x7fffffffLL || rows * (p->vocab / 4096 + 1) > 0x7fffffffLL)
         return SSD_ERR_UNSUPPORTED;
     d->R = p->num_reqs;
     d->T = p->tokens_per_req;

@@ -84,6 +84,116 @@ __device__ __forceinline__ f32x4 mma_8bit(i32x4 w, int ws, i32x4 x0, i32x4 x1, i
 }
 
 // ---------------------------------------------------------------------------
+// Very few tokens: a block of 4 waves takes 16 weight rows, all tokens (at most
+// 16) and all of K. The tokens go to LDS once; the waves take K in turn, 256
+// values at a time, their weights straight to registers, all of a wave's first
+// UNITS turns on their way before the tokens are waited for, and are joined in
+// LDS. Bound by the weights' bytes. What counts is few loads, as every one of a
+// wave takes its turn at the address unit whatever it brings: two of weights and,
+// where rows of scales are whole words (WORDS), one of scales for 4 K of products.
+template <int MODE, bool WORDS, typename TO>
+__global__ __launch_bounds__(256) void linear_few_kernel(LinearDims d, LinearArgs a, int pitch)
+{
+    constexpr int EX = MODE == kSixteen ? 2 : 1, W = 4, UNITS = 3;
+    extern __shared__ __align__(16) char xs_[];           // T rows of `pitch` bytes, then their scales
+    __shared__ f32x4 part[W][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = scalar(tid >> 6), n16 = lane & 15, g = lane >> 4;
+    const int n0 = (int)blockIdx.x * 16, blocks = d.K / 32, units = (blocks + 7) / 8;
+    const int nrows = d.N - n0 < 16 ? d.N - n0 : 16;
+    const rsrc_t rw = make_rsrc(a.w + (int64_t)n0 * (d.K / 2), (uint32_t)nrows * (uint32_t)(d.K / 2));
+    const rsrc_t rs = make_rsrc(a.w_scale + (int64_t)n0 * blocks, (uint32_t)nrows * (uint32_t)blocks);
+
+    struct Unit {
+        i32x4 w[2];
+        uint32_t s[2];
+    };
+    // (what lies past a row's or the tile's end, or past the last unit, comes back as zeros)
+    auto request = [&](int u, Unit &t) {
+        const uint32_t row = (uint32_t)n16 * (uint32_t)blocks;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t off = 8 * u + 4 * h + g < blocks ? 0u : kNothing;
+            t.w[h] = buf16(rw, 16u * row + 16u * g + off, 128u * u + 64u * h);
+            if constexpr (!WORDS) t.s[h] = (uint32_t)buf1(rs, row + g + off, 8u * u + 4u * h);
+        }
+        if constexpr (WORDS) {
+            const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, (int)(row + (u < units ? 0u : kNothing)), 8 * u, 0);
+            t.s[0] = (uint32_t)v[0];          // (the lane's byte is taken out where it is used)
+            t.s[1] = (uint32_t)v[1];
+        }
+    };
+    Unit t[UNITS];
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) request(wave + W * i, t[i]);
+
+    // tokens, filled up with zeros to whole units
+    const int chunks = d.K * EX / 16, all = pitch / 16;
+    for (int tok = 0; tok < d.T; ++tok) {
+        const i32x4 *const from = reinterpret_cast<const i32x4 *>(static_cast<const char *>(a.x) + (int64_t)tok * d.xs * EX);
+        for (int c = tid; c < all; c += 256)
+            *reinterpret_cast<i32x4 *>(xs_ + tok * pitch + 16 * c) = c < chunks ? from[c] : i32x4{0, 0, 0, 0};
+    }
+    char *const xscale = xs_ + d.T * pitch;
+    if (MODE != kSixteen)
+        for (int i = tid; i < d.T * 8 * units; i += 256) {
+            const int tok = i / (8 * units), b = i - tok * 8 * units;
+            xscale[i] = b < blocks ? (char)a.x_scale[(int64_t)tok * blocks + b] : 0;
+        }
+    __syncthreads();
+
+    const int tok = n16 < d.T ? n16 : d.T - 1;             // (columns past the last token are not stored)
+    const char *const x = xs_ + tok * pitch;
+    f32x4 acc = zero4();
+    for (int u0 = wave; u0 < units; u0 += W * UNITS) {
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i) {
+            const int u = u0 + W * i;
+            if (u < units) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const char *const xk = x + (256 * u + 128 * h) * EX;
+                    const uint32_t ws = WORDS ? t[i].s[h] >> (8 * g) & 255u : t[i].s[h];
+                    if constexpr (MODE == kSixteen) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            acc = Mma<bf16>::run(widen_codes((uint32_t)t[i].w[h][j], ws),
+                                                 *reinterpret_cast<const bf16x8 *>(xk + 64 * g + 16 * j), acc);
+                    } else {
+                        const uint32_t b = (uint8_t)xscale[tok * 8 * units + 8 * u + 4 * h + g];
+                        if constexpr (MODE == kEight)
+                            acc = mma_8bit(t[i].w[h], (int)ws, *reinterpret_cast<const i32x4 *>(xk + 16 * g),
+                                           *reinterpret_cast<const i32x4 *>(xk + 64 + 16 * g), (int)b, acc);
+                        else
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                acc = Mma<bf16>::run(widen_codes((uint32_t)t[i].w[h][j], ws),
+                                                     widen_8bit(*reinterpret_cast<const u32x2 *>(xk + 32 * g + 8 * j),
+                                                                __uint_as_float(b << 23)), acc);
+                    }
+                }
+            }
+            if (u + W * UNITS < units) request(u + W * UNITS, t[i]);
+        }
+    }
+    part[wave][lane] = acc;
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int k = 1; k < W; ++k) {
+        const f32x4 o = part[k][lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] += o[e];
+    }
+    TO *const out = static_cast<TO *>(a.out);
+    if (n16 < d.T)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int n = n0 + 4 * g + e;
+            if (n < d.N) out[(int64_t)n16 * d.os + n] = from_f32<TO>(acc[e] + (a.bias ? a.bias[n] : 0.0f));
+        }
+}
+
+// ---------------------------------------------------------------------------
 // Many tokens: a block of WT x WN waves takes 16 TT WT tokens and 16 RT WN weight
 // rows, 16 TT by 16 RT a wave. Tokens, weights and scales go to LDS by the loads
 // themselves, a stage of K (128 values of 8-bit rows, 64 of bfloat16) in one of
@@ -466,7 +576,14 @@ static int linear_tile_of(const LinearDims &d) {
     }
     return best;
 }
-const char *linear_kernel_name(const LinearDims &d) { return kTileNames[linear_tile_of(d)]; }
+
+// Up to this many tokens' bytes the block of every 16 weight rows reads them all; with more of them
+// than weights the tiles, which share them, are faster.
+static bool linear_few(const LinearDims &d) {
+    const int64_t bytes = (int64_t)d.T * (d.K + 255) / 256 * 256 * (d.e4m3 ? 1 : 2);
+    return d.T <= (d.e4m3 ? 8 : 4) && bytes <= 48 << 10;
+}
+const char *linear_kernel_name(const LinearDims &d) { return linear_few(d) ? "few" : kTileNames[linear_tile_of(d)]; }
 
 template <int MODE, int WT, int WN, int WK, int TT, int RT, int NSUB, int NBUF, bool WORDS, int PERCU, typename TO>
 static void linear_tile(const LinearDims &d, const LinearArgs &a, hipStream_t st) {
@@ -475,7 +592,19 @@ static void linear_tile(const LinearDims &d, const LinearArgs &a, hipStream_t st
                        dim3((unsigned)(tt * nt)), dim3(64 * WT * WN * WK), 0, st, d, a, tt, nt);
 }
 template <int MODE, bool WORDS, typename TO>
+static void linear_few_t(const LinearDims &d, const LinearArgs &a, hipStream_t st) {
+    const int units = (d.K + 255) / 256, pitch = units * 256 * (MODE == kSixteen ? 2 : 1) + 16;
+    const int scales = MODE == kSixteen ? 0 : d.T * 8 * units;
+    hipLaunchKernelGGL((linear_few_kernel<MODE, WORDS, TO>), dim3((unsigned)((d.N + 15) / 16)), dim3(256),
+                       d.T * pitch + scales, st, d, a, pitch);
+}
+template <int MODE, bool WORDS, typename TO>
 static void linear_t(const LinearDims &d, const LinearArgs &a, hipStream_t st) {
+    if (linear_few(d)) {
+        if (d.K % 256 == 0 && (uintptr_t)a.w_scale % 8 == 0) linear_few_t<MODE, true, TO>(d, a, st);
+        else linear_few_t<MODE, false, TO>(d, a, st);
+        return;
+    }
     // (blocks a CU that the buffers leave room for)
     constexpr int two = WORDS || MODE == kSixteen ? 2 : 1;
     switch (linear_tile_of(d)) {

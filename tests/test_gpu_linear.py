@@ -51,7 +51,7 @@ def check(out, xv, w, bias=None, xt=BF):
     assert not bad.any(), (int(bad.sum()), float(np.nanmax(np.abs(got - y))))
 
 
-SIZES = [(1, 32, 1), (1, 2560, 100), (2, 96, 17), (3, 160, 33), (5, 1056, 64), (16, 512, 48), (17, 544, 65),
+SIZES = [(1, 32, 1), (1, 2560, 100), (1, 4864, 40), (4, 4352, 16), (8, 768, 50), (2, 96, 17), (3, 160, 33), (5, 1056, 64), (16, 512, 48), (17, 544, 65),
          (31, 256, 16), (33, 64, 257), (48, 1024, 130), (64, 320, 31), (65, 128, 96), (77, 1056, 111),
          (100, 32, 300), (127, 96, 129), (128, 256, 256), (129, 288, 255), (200, 2080, 70), (256, 224, 513),
          (300, 128, 40), (513, 160, 272), (1000, 64, 20)]
@@ -71,7 +71,7 @@ def test_whole_numbers(T, K, N, xt):
 
 
 # a size for each tile that is built (per type of the rows), K ending inside a step or not
-TILES = {"16x16": (5, 4096, 300), "16x32": (16, 512, 9000), "32x32": (64, 8192, 4000), "64x64": (64, 512, 9000),
+TILES = {"few": (4, 2560, 300), "16x16": (12, 4096, 300), "16x32": (16, 512, 9000), "32x32": (64, 8192, 4000), "64x64": (64, 512, 9000),
          "128x128": (300, 256, 9000), "128x256": (384, 640, 18560), "256x256": (2048, 256, 16000)}
 
 
@@ -82,7 +82,7 @@ TILES = {"16x16": (5, 4096, 300), "16x32": (16, 512, 9000), "32x32": (64, 8192, 
 def test_every_tile(tile, xt, to, odd):
     T, K, N = TILES[tile]
     if odd:
-        T, K, N = T - 3, K - 96 if K > 512 else K + 32, N - 7
+        T, K, N = max(1, T - 3), K - 96 if K > 512 else K + 32, N - 7
     p = ssd.make_linear_problem(T, K, N, xt, to)
     took = ssd.linear_w4_kernel(p)
     g = torch.Generator(DEV).manual_seed(K)

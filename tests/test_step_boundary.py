@@ -129,7 +129,7 @@ def call_probs(p, *over, ws=1 << 40):
 @pytest.mark.parametrize("kw,status", [
     (dict(num_reqs=-1), SHAPE), (dict(tokens_per_req=-1), SHAPE), (dict(vocab=0), SHAPE), (dict(in_dtype=2), DTYPE),
     (dict(in_dtype=3), DTYPE), (dict(logits_stride=99), SHAPE), (dict(probs_stride=99), SHAPE),
-    (dict(vocab=2 ** 27 + 1), UNSUP), (dict(num_reqs=2 ** 23), UNSUP),
+    (dict(vocab=2 ** 27 + 1), UNSUP), (dict(num_reqs=2 ** 30), UNSUP), (dict(num_reqs=2 ** 17, vocab=2 ** 26), UNSUP),
 ])
 def test_probs_refusals(kw, status):
     assert call_probs(probs(**kw)) == status
