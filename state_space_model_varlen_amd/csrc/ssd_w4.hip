@@ -330,41 +330,47 @@ __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) 
 #pragma unroll
         for (int t = 0; t < TT; ++t) acc[r][t] = zero4();
 
-    // everything of step s on its way; what lies past a row's or the tile's end comes as zeros
-    auto request_step = [&](int s, const Step &b) {
+    // load q of step s on its way; what lies past a row's or the tile's end comes as zeros
+    auto load_one = [&](auto Q, int s, const Step &b) __attribute__((always_inline)) {
+        constexpr int q = decltype(Q)::value;
         const uint32_t bx = lds_address(b.x), bw = bx + sizeof(b.x), bs = bw + sizeof(b.w);
-        const uint32_t xo = xrow + (chunk + 128u * s < (uint32_t)d.K * EX ? 0u : kNothing);
-#pragma unroll
-        for (int q = 0; q < LX; ++q) {
+        if constexpr (q < LX) {
+            const uint32_t xo = xrow + (chunk + 128u * s < (uint32_t)d.K * EX ? 0u : kNothing);
             const int c = q * THREADS + wave * 64;
             to_lds16(rx.r, c < NX ? bx + 16 * c : nowhere, xo + q * xstep, 128u * s);
-        }
-        const uint32_t wo = BS * s + tid % CW < blocks ? 0u : kNothing;
-#pragma unroll
-        for (int q = 0; q < LW; ++q) {
-            const int c = q * THREADS + wave * 64;
-            to_lds16(rw.r, c < NW ? bw + 16 * c : nowhere, wrow[q] + wo, 16u * BS * s);
-        }
-#pragma unroll
-        for (int q = 0; q < LS; ++q) {
-            const int e = q * THREADS + wave * 64;
-            const uint32_t so = srow[q] + (BS * s + sblk[q] < blocks ? 0u : kNothing);
+        } else if constexpr (q < LX + LW) {
+            const uint32_t wo = BS * s + tid % CW < blocks ? 0u : kNothing;
+            const int c = (q - LX) * THREADS + wave * 64;
+            to_lds16(rw.r, c < NW ? bw + 16 * c : nowhere, wrow[q - LX] + wo, 16u * BS * s);
+        } else {
+            constexpr int i = q - LX - LW;
+            const int e = i * THREADS + wave * 64;
+            const uint32_t so = srow[i] + (BS * s + sblk[i] < blocks ? 0u : kNothing);
             const i32x4 r = e < SO ? rxs.r : rs.r;                               // (the same in a wave)
             const uint32_t to = e < NS ? bs + 4 * e : nowhere;
             if constexpr (WORDS && MODE != kSixteen) to_lds4(r, to, so, BS * s);
             else to_lds1(r, to, so, BS * s);
         }
     };
-    auto request = [&](int s, const Buffer &b) {
-#pragma unroll
-        for (int u = 0; u < NSUB; ++u) request_step(s * NSUB + u, b.step[u]);
+    // a share of a stage's loads: those of turn t of `turns`
+    auto request_share = [&](auto T_, auto N_, int s, const Buffer &b) __attribute__((always_inline)) {
+        constexpr int t = decltype(T_)::value, turns = decltype(N_)::value, all = LOADS * NSUB;
+        constexpr int from = all * t / turns, to = all * (t + 1) / turns;
+        each<to - from>([&](auto I) __attribute__((always_inline)) {
+            constexpr int l = from + decltype(I)::value;
+            load_one(std::integral_constant<int, l % LOADS>{}, s * NSUB + l / LOADS, b.step[l / LOADS]);
+        });
+    };
+    auto request = [&](int s, const Buffer &b) __attribute__((always_inline)) {
+        request_share(std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{}, s, b);
     };
     // scale of block g of token or row `at`
-    auto scale_of = [&](const uint32_t *p, int at, int blk) -> uint32_t {
+    auto scale_of = [&](const uint32_t *p, int at, int blk) __attribute__((always_inline)) -> uint32_t {
         if constexpr (WORDS && MODE != kSixteen) return reinterpret_cast<const uint8_t *>(p)[4 * at + blk];
         else return p[at * BS + blk];
     };
-    auto multiply_step = [&](const Step &b) {
+    // (between(turn, turns) is called as the products go)
+    auto multiply_step = [&](const Step &b, auto between) __attribute__((always_inline)) {
         const char *const x = b.x + (wt * 16 * TT + n16) * 128;
         const char *const w = b.w + (wn * 16 * RT + n16) * (CW * 16);
         const int turn = n16 >> 1;
@@ -379,22 +385,26 @@ __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) 
 #pragma unroll
             for (int r = 0; r < RT; ++r)
                 wf[r] = *reinterpret_cast<const i32x4 *>(w + r * (256 * CW) + 16 * g);
-            i32x4 f[2][2];
-            int xs[2];
-            auto take = [&](int t) {
-                f[t & 1][0] = *reinterpret_cast<const i32x4 *>(x + t * 2048 + 16 * (g ^ turn));
-                f[t & 1][1] = *reinterpret_cast<const i32x4 *>(x + t * 2048 + 16 * ((4 + g) ^ turn));
-                xs[t & 1] = (int)scale_of(b.s, wt * 16 * TT + 16 * t + n16, g);
+            constexpr int AHEAD = TT > 1 ? 1 : 0, RING = AHEAD + 1;
+            i32x4 f[RING][2];
+            int xs[RING];
+            auto take = [&](int t) __attribute__((always_inline)) {
+                f[t % RING][0] = *reinterpret_cast<const i32x4 *>(x + t * 2048 + 16 * (g ^ turn));
+                f[t % RING][1] = *reinterpret_cast<const i32x4 *>(x + t * 2048 + 16 * ((4 + g) ^ turn));
+                xs[t % RING] = (int)scale_of(b.s, wt * 16 * TT + 16 * t + n16, g);
             };
-            take(0);
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                if (t + 1 < TT) take(t + 1);
+            for (int t = 0; t < AHEAD; ++t) take(t);
+            each<TT>([&](auto I) __attribute__((always_inline)) {
+                constexpr int t = decltype(I)::value;
+                if constexpr (t + AHEAD < TT) take(t + AHEAD);
 #pragma unroll
                 for (int r = 0; r < RT; ++r)
-                    acc[r][t] = mma_8bit(wf[r], (int)ws[r][0], f[t & 1][0], f[t & 1][1], xs[t & 1], acc[r][t]);
+                    acc[r][t] = mma_8bit(wf[r], (int)ws[r][0], f[t % RING][0], f[t % RING][1], xs[t % RING], acc[r][t]);
                 __builtin_amdgcn_sched_barrier(0);
-            }
+                between(I, std::integral_constant<int, TT>{});
+                __builtin_amdgcn_sched_barrier(0);
+            });
         } else if constexpr (MODE == kSixteen) {
             // lane group g takes K = 8 g .. 8 g + 7 of a block, a block an instruction
             uint32_t wf[RT][2];
@@ -403,36 +413,35 @@ __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) 
 #pragma unroll
                 for (int i = 0; i < 2; ++i) wf[r][i] = *reinterpret_cast<const uint32_t *>(w + r * (256 * CW) + 16 * i + 4 * g);
             // (fragments of the tokens are read AHEAD before they are multiplied)
-            #ifndef AH
-#define AH 3
-#endif
-            constexpr int AHEAD = AH;
+                        constexpr int AHEAD = 3;
             bf16x8 f[AHEAD + 1];
-            auto take = [&](int k) {
+            auto take = [&](int k) __attribute__((always_inline)) {
                 f[k % (AHEAD + 1)] = *reinterpret_cast<const bf16x8 *>(x + k % TT * 2048 + 16 * ((4 * (k / TT) + g) ^ turn));
             };
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k) take(k);
             bf16x8 wv[RT];
-#pragma unroll
-            for (int k = 0; k < 2 * TT; ++k) {
-                if (k + AHEAD < 2 * TT) take(k + AHEAD);
-                if (k % TT == 0)
+            each<2 * TT>([&](auto I) __attribute__((always_inline)) {
+                constexpr int k = decltype(I)::value;
+                if constexpr (k + AHEAD < 2 * TT) take(k + AHEAD);
+                if constexpr (k % TT == 0)
 #pragma unroll
                     for (int r = 0; r < RT; ++r) wv[r] = widen_codes(wf[r][k / TT], ws[r][k / TT]);
 #pragma unroll
                 for (int r = 0; r < RT; ++r)
                     acc[r][k % TT] = Mma<bf16>::run(wv[r], f[k % (AHEAD + 1)], acc[r][k % TT]);
                 __builtin_amdgcn_sched_barrier(0);
-            }
+                between(I, std::integral_constant<int, 2 * TT>{});
+                __builtin_amdgcn_sched_barrier(0);
+            });
         } else {
             // lane group g takes block g, 8 values an instruction
             i32x4 wf[RT];
 #pragma unroll
             for (int r = 0; r < RT; ++r)
                 wf[r] = *reinterpret_cast<const i32x4 *>(w + r * (256 * CW) + 16 * g);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            each<4>([&](auto I) __attribute__((always_inline)) {
+                constexpr int i = decltype(I)::value;
                 bf16x8 wv[RT];
 #pragma unroll
                 for (int r = 0; r < RT; ++r) wv[r] = widen_codes((uint32_t)wf[r][i], ws[r][0]);
@@ -446,27 +455,44 @@ __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) 
                     for (int r = 0; r < RT; ++r) acc[r][t] = Mma<bf16>::run(wv[r], v, acc[r][t]);
                 }
                 __builtin_amdgcn_sched_barrier(0);
-            }
+                between(I, std::integral_constant<int, 4>{});
+                __builtin_amdgcn_sched_barrier(0);
+            });
         }
     };
 
-    auto multiply = [&](const Buffer &b) {
-#pragma unroll
-        for (int u = 0; u < NSUB / WK; ++u) multiply_step(b.step[u * WK + wk]);
+    // the products of one buffer's stage, with the loads of stage `next` into another between them
+    // (each takes its turn at the address unit, in front of which the products would wait; with two
+    // buffers they have to be on their way first: 4096 tokens, 5120 to 2560 in 8 bits 65 -> 59 us, with
+    // two buffers in bfloat16 118 -> 132)
+    auto multiply = [&](const Buffer &b, int next, const Buffer &into) __attribute__((always_inline)) {
+        if constexpr (NBUF == 2) {
+            request(next, into);
+            each<NSUB / WK>([&](auto U) __attribute__((always_inline)) { multiply_step(b.step[decltype(U)::value * WK + wk], [](auto, auto) __attribute__((always_inline)) {}); });
+        } else
+            each<NSUB / WK>([&](auto U) __attribute__((always_inline)) {
+                constexpr int u = decltype(U)::value;
+                multiply_step(b.step[u * WK + wk], [&](auto T_, auto N_) __attribute__((always_inline)) {
+                    request_share(std::integral_constant<int, u * decltype(N_)::value + decltype(T_)::value>{},
+                                  std::integral_constant<int, decltype(N_)::value * (NSUB / WK)>{}, next, into);
+                });
+            });
+    };
+    auto multiply_last = [&](const Buffer &b) __attribute__((always_inline)) {
+        each<NSUB / WK>([&](auto U) __attribute__((always_inline)) { multiply_step(b.step[decltype(U)::value * WK + wk], [](auto, auto) __attribute__((always_inline)) {}); });
     };
 
     // the stage in buffer I of a round of NBUF from `s` on
     int s = 0;
-    auto stage = [&](auto I) {
+    auto stage = [&](auto I) __attribute__((always_inline)) {
         constexpr int i = decltype(I)::value;
-        request(s + i + NBUF - 1, buffer<Buffer, (i + NBUF - 1) % NBUF>());
-        multiply(buffer<Buffer, i>());
+        multiply(buffer<Buffer, i>(), s + i + NBUF - 1, buffer<Buffer, (i + NBUF - 1) % NBUF>());
         wait_and_meet<(NBUF - 2) * NSUB * LOADS>();
     };
-    auto last = [&](auto I) {
-        if (s + decltype(I)::value < stages) multiply(buffer<Buffer, decltype(I)::value>());
+    auto last = [&](auto I) __attribute__((always_inline)) {
+        if (s + decltype(I)::value < stages) multiply_last(buffer<Buffer, decltype(I)::value>());
     };
-    each<NBUF - 1>([&](auto I) { request(decltype(I)::value, buffer<Buffer, decltype(I)::value>()); });
+    each<NBUF - 1>([&](auto I) __attribute__((always_inline)) { request(decltype(I)::value, buffer<Buffer, decltype(I)::value>()); });
     wait_and_meet<(NBUF - 2) * NSUB * LOADS>();
     for (; s + NBUF <= stages; s += NBUF) each<NBUF>(stage);
     wait_and_meet<0>();
@@ -536,39 +562,37 @@ static LinearMode linear_mode(const LinearDims &d) {
 }
 
 // The tiles that are built. One is taken by its estimated time on the CU that gets the most of
-// them: its bytes, its products at the rate that the tile reached on 4096 tokens, 4096 to 18560
-// (TFLOP/s of 8-bit and bfloat16 rows; the whole chip), or its steps at the time of one; and a
-// time a round of blocks. On 105 sizes (1 to 4096 tokens, 512 to 8192 values, 300 to 18560 outputs)
-// the tile so taken was on average 0.6 % (8 bits) and 1.4 % (bfloat16) slower than the best of them, at
-// most 11 and 19 %.
+// them: its bytes, its products at a share of the rate that the tile reached on 4096 tokens, 4096 to
+// 18560 (TFLOP/s of 8-bit and bfloat16 rows; the whole chip), or its stages at the time of one;
+// and a time a round of blocks. On 105 sizes (1 to 4096 tokens, 512 to 8192 values, 300 to 18560
+// outputs) the tile so taken was on average 0.9 % (8 bits) and 0.8 % (bfloat16) slower than the best of
+// them, at most 22 and 18 %.
 struct Tile {
     int tokens, rows, per_cu, steps;      // steps of 128 (bfloat16: 64) values a stage
     double rate8, rate16;
 };
 static constexpr Tile kTiles[] = {
-    {16, 16, 2, 4, 134, 68}, {16, 32, 2, 1, 366, 202}, {32, 32, 2, 4, 408, 213}, {64, 64, 2, 2, 899, 584},
-    {128, 128, 2, 1, 1767, 1003}, {128, 256, 1, 1, 2008, 1270}, {256, 256, 1, 1, 2227, 1309}};
-static const char *const kTileNames[] = {"16x16", "16x32", "32x32", "64x64", "128x128", "128x256", "256x256"};
+    {16, 16, 2, 4, 224, 103}, {16, 32, 2, 1, 369, 191}, {32, 32, 1, 4, 385, 246}, {64, 64, 2, 2, 898, 576},
+    {128, 128, 2, 1, 1793, 1014}, {256, 256, 1, 1, 2507, 1341}, {128, 256, 1, 1, 1760, 0}};
+static const char *const kTileNames[] = {"16x16", "16x32", "32x32", "64x64", "128x128", "256x256", "128x256"};
 
 static int linear_tile_of(const LinearDims &d) {
-    const bool wide = !d.e4m3;            // bfloat16 rows (also for the pace of widened ones)
+    const bool wide = !d.e4m3;
     int best = 0;
     double least = 0;
-    for (int i = 0; i < (int)(sizeof kTiles / sizeof *kTiles); ++i) {
+    for (int i = 0; i < (wide ? 6 : 7); ++i) {
         const Tile &t = kTiles[i];
         const int64_t blocks = (int64_t)((d.T + t.tokens - 1) / t.tokens) * ((d.N + t.rows - 1) / t.rows);
-        const double most = (double)((blocks + 255) / 256);       // of a CU
-        const int per_cu = wide && i == 5 ? 2 : t.per_cu;
-        const double rounds = (double)(((int64_t)most + per_cu - 1) / per_cu);
+        const int64_t most = (blocks + 255) / 256, rounds = (most + t.per_cu - 1) / t.per_cu;     // of a CU
         const double bytes = (double)d.K * ((d.T < t.tokens ? d.T : t.tokens) * (wide ? 2 : 1) + t.rows * 0.53);
         const double flops = 2.0 * t.tokens * t.rows * d.K;
         const double stages = d.K / (wide ? 64.0 : 128.0) / t.steps;
         // microseconds
-        const double by_bytes = most * bytes / (wide ? 6.95e4 : 4.47e4);
-        const double by_products = most * flops * 256e-6 / (wide ? t.rate16 * 0.817 : t.rate8 * 0.477);
-        const double by_stages = rounds * stages * (wide ? 0.202 * (1 + 0.189 * t.steps) : 0.2 * (1 + 0.371 * t.steps));
+        const double by_bytes = most * bytes / (wide ? 6.05e4 : 2.75e4);
+        const double by_products = most * flops * 256e-6 / (wide ? t.rate16 * 0.531 : t.rate8 * 0.944);
+        const double by_stages = rounds * stages * (wide ? 0.269 * (1 + 0.264 * t.steps) : 0.162 * (1 + 0.267 * t.steps));
         double time = by_bytes > by_products ? by_bytes : by_products;
-        time = (time > by_stages ? time : by_stages) + rounds * (wide ? 3.8 : 0.743);
+        time = (time > by_stages ? time : by_stages) + rounds * (wide ? 0.947 : 1.43);
         if (i == 0 || time < least) {
             least = time;
             best = i;
@@ -614,11 +638,10 @@ static void linear_t(const LinearDims &d, const LinearArgs &a, hipStream_t st) {
     case 3: return linear_tile<MODE, 1, 4, 1, 4, 1, 2, 3, WORDS, two, TO>(d, a, st);
     case 4: return linear_tile<MODE, 2, 4, 1, 4, 2, 1, 3, WORDS, two, TO>(d, a, st);
     case 5:
-        if constexpr (MODE == kSixteen) return linear_tile<MODE, 1, 4, 1, 8, 4, 1, 2, WORDS, 2, TO>(d, a, st);
-        else return linear_tile<MODE, 2, 4, 1, 4, 4, 1, 3, WORDS, 1, TO>(d, a, st);
-    default:
         // (scales of a byte a word leave room for two buffers)
         return linear_tile<MODE, 2, 4, 1, 8, 4, 1, WORDS || MODE == kSixteen ? 3 : 2, WORDS, 1, TO>(d, a, st);
+    default:
+        if constexpr (MODE != kSixteen) linear_tile<MODE, 2, 4, 1, 4, 4, 1, 3, WORDS, 1, TO>(d, a, st);
     }
 }
 

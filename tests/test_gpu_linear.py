@@ -71,8 +71,9 @@ def test_whole_numbers(T, K, N, xt):
 
 
 # a size for each tile that is built (per type of the rows), K ending inside a step or not
-TILES = {"few": (4, 2560, 300), "16x16": (12, 4096, 300), "16x32": (16, 512, 9000), "32x32": (64, 8192, 4000), "64x64": (64, 512, 9000),
-         "128x128": (300, 256, 9000), "128x256": (384, 640, 18560), "256x256": (2048, 256, 16000)}
+TILES = {"few": (4, 2560, 300), "16x16": (12, 4096, 300), "16x32": (16, 512, 9000), "32x32": (64, 1024, 2600),
+         "64x64": (32, 256, 9000), "128x128": (200, 256, 9000), "256x256": (1024, 512, 9000),
+         "128x256": (384, 640, 18560)}           # (of 8-bit rows alone)
 
 
 @pytest.mark.parametrize("xt", [BF, E4])
@@ -101,7 +102,7 @@ def test_every_tile(tile, xt, to, odd):
     want = torch.cat([(x[a:a + 512].double() @ w.double().t()) for a in range(0, T, 512)])
     assert float((x.abs().amax(0) * w.abs().amax(0)).sum()) < 2.0 ** 20
     assert torch.equal(out, want.to(to)), took
-    if not odd:
+    if not odd and (xt == E4 or tile != "128x256"):
         assert took == tile
 
 
