@@ -64,61 +64,104 @@ __device__ __forceinline__ float block_sum(float v, float *part) {
     return s;
 }
 
-// One group by one block, VPT vectors of 8 elements a thread; every row on 16
-// bytes (out: 8 for 8-bit rows).
-template <typename TX, typename TR, typename TO, int MODE, int VPT>
-__global__ __launch_bounds__(1024) void norm_kernel(NormArgs a) {
+// 8 elements of a row, the first `n` of them if it ends there; rows start on their element.
+template <typename T> struct Run8 {
+    typedef T vec __attribute__((ext_vector_type(8)));
+    typedef vec any __attribute__((aligned(sizeof(T))));
+    vec v;
+    __device__ __forceinline__ void load(const T *p, int n) {
+        if (n >= 8) v = *reinterpret_cast<const any *>(p);
+        else
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : from_f32<T>(0.0f);
+    }
+    __device__ __forceinline__ void get(float *f) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = to_f32(v[i]);
+    }
+    __device__ __forceinline__ static void store(T *p, const float *f, int n) {
+        vec o;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = from_f32<T>(f[i]);
+        if (n >= 8) *reinterpret_cast<any *>(p) = o;
+        else
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n) p[i] = o[i];
+    }
+};
+
+// The row and first element of group `seg`.
+__device__ __forceinline__ int64_t group_of(const NormArgs &a, unsigned seg, int &at) {
+    if (a.groups == 1) {
+        at = 0;
+        return seg;
+    }
+    const unsigned row = seg / (unsigned)a.groups;
+    at = (int)(seg - row * (unsigned)a.groups) * a.per;
+    return row;
+}
+
+// One group by one block (LANES 0) or by LANES lanes of a block of 256 threads, VPT vectors of 8
+// elements a thread.
+template <typename TX, typename TR, typename TO, int MODE, int VPT, int LANES>
+__global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(NormArgs a) {
     __shared__ float part[16];
-    const int64_t seg = blockIdx.x;
-    const int64_t row = seg / a.groups;
-    const int at = (int)(seg - row * a.groups) * a.per;
+    const int lane = LANES ? (int)threadIdx.x % (LANES ? LANES : 1) : (int)threadIdx.x;   // of the group's
+    const int lanes = LANES ? LANES : (int)blockDim.x;
+    const unsigned seg = LANES ? blockIdx.x * (256u / (LANES ? LANES : 1)) + threadIdx.x / (LANES ? LANES : 1) : blockIdx.x;
+    if (LANES && seg >= a.segments) return;                 // (all of a group's lanes)
+    int at;
+    const int64_t row = group_of(a, seg, at);
     const TX *const x = static_cast<const TX *>(a.x) + row * a.xs + at;
     const TR *const other = static_cast<const TR *>(a.other) + (MODE == kPlain ? 0 : row * a.others + at);
-    RawV<TX, 8> rx[VPT];
-    RawV<TR, 8> ro[VPT];
-    RawV<float, 8> rw[VPT];
+    Run8<TX> rx[VPT];
+    Run8<TR> ro[VPT];
+    Run8<float> rw[VPT];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        const int i = (k * (int)blockDim.x + (int)threadIdx.x) * 8;
-        rx[k].zero();
-        if (i < a.per) {
-            rx[k].load(x + i);
-            if constexpr (MODE != kPlain) ro[k].load(other + i);
-            if (a.weight) rw[k].load(a.weight + at + i);
-        }
+        const int i = (k * lanes + lane) * 8, n = a.per - i;
+        rx[k].load(x + i, n);
+        if constexpr (MODE != kPlain) ro[k].load(other + i, n);
+        if (a.weight) rw[k].load(a.weight + at + i, n);
     }
     float v[VPT][8], sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        const int i = (k * (int)blockDim.x + (int)threadIdx.x) * 8;
+        const int i = (k * lanes + lane) * 8, n = a.per - i;
         rx[k].get(v[k]);
-        if (i < a.per) {
-            if constexpr (MODE != kPlain) {
-                float o[8];
-                ro[k].get(o);
+        if constexpr (MODE != kPlain) {
+            float o[8];
+            ro[k].get(o);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[k][e] = MODE == kAdd ? v[k][e] + o[e] : v[k][e] * silu(o[e]);
-            }
-            if constexpr (MODE == kAdd) {
-                if (a.sum) {
-                    RawV<TR, 8> s;
-                    s.set(v[k]);
-                    s.store(static_cast<TR *>(a.sum) + row * a.sums + at + i);
-                }
-            }
+            for (int e = 0; e < 8; ++e) v[k][e] = MODE == kAdd ? v[k][e] + o[e] : v[k][e] * silu(o[e]);
         }
+        if constexpr (MODE == kAdd)
+            if (a.sum) Run8<TR>::store(static_cast<TR *>(a.sum) + row * a.sums + at + i, v[k], n);
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum = fmaf(v[k][e], v[k][e], sum);
     }
-    sum = block_sum(sum, part);
+    if constexpr (LANES == 16) {
+        sum += dpp<0xb1>(sum);
+        sum += dpp<0x4e>(sum);
+        sum += dpp<0x141>(sum);
+        sum += dpp<0x140>(sum);
+    } else if constexpr (LANES == 64)
+        sum = wave_sum(sum);
+    else
+        sum = block_sum(sum, part);
     const float r = rsqrtf(sum / (float)a.per + a.eps);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        const int i = (k * (int)blockDim.x + (int)threadIdx.x) * 8;
-        float w[8];
-        if (a.weight && i < a.per) rw[k].get(w);
+        const int i = (k * lanes + lane) * 8, n = a.per - i;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[k][e] = a.weight && i < a.per ? v[k][e] * r * w[e] : v[k][e] * r;
+        for (int e = 0; e < 8; ++e) v[k][e] *= r;
+        if (a.weight) {
+            float w[8];
+            rw[k].get(w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[k][e] *= w[e];
+        }
         if constexpr (std::is_same<TO, e4m3>::value) {
             // (32 elements are 4 neighbouring lanes' and end with the group: all in or all out)
             float top = 0.0f;
@@ -137,26 +180,23 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a) {
                 int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[k][4 * j], v[k][4 * j + 1], 0, false);
                 c[j] = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(v[k][4 * j + 2], v[k][4 * j + 3], lo, true);
             }
-            if (i < a.per) {
-                *reinterpret_cast<u32x2 *>(static_cast<uint8_t *>(a.out) + row * a.os + at + i) = c;
+            if (n > 0) {
+                typedef u32x2 any2 __attribute__((aligned(1)));
+                *reinterpret_cast<any2 *>(static_cast<uint8_t *>(a.out) + row * a.os + at + i) = c;
                 if ((threadIdx.x & 3) == 0) a.scale[row * (a.hidden / 32) + (at + i) / 32] = (uint8_t)b;
             }
-        } else if (i < a.per) {
-            RawV<TO, 8> o;
-            o.set(v[k]);
-            o.store(static_cast<TO *>(a.out) + row * a.os + at + i);
-        }
+        } else
+            Run8<TO>::store(static_cast<TO *>(a.out) + row * a.os + at + i, v[k], n);
     }
 }
 
-// The same for rows of any alignment and length: an element a thread and step,
-// read a second time instead of kept.
+// The same for rows that no block can keep: an element a thread and step, read a
+// second time instead.
 template <typename TX, typename TR, typename TO, int MODE>
-__global__ __launch_bounds__(256) void norm_any_kernel(NormArgs a) {
+__global__ __launch_bounds__(256) void norm_long_kernel(NormArgs a) {
     __shared__ float part[4];
-    const int64_t seg = blockIdx.x;
-    const int64_t row = seg / a.groups;
-    const int at = (int)(seg - row * a.groups) * a.per;
+    int at;
+    const int64_t row = group_of(a, blockIdx.x, at);
     const TX *const x = static_cast<const TX *>(a.x) + row * a.xs + at;
     const TR *const other = static_cast<const TR *>(a.other) + (MODE == kPlain ? 0 : row * a.others + at);
     auto value = [&](int i) {
@@ -196,28 +236,34 @@ __global__ __launch_bounds__(256) void norm_any_kernel(NormArgs a) {
 }
 
 template <typename TX, typename TR, typename TO, int MODE>
-static void norm_t(const NormArgs &a, bool wide, hipStream_t st) {
+static void norm_t(const NormArgs &a, hipStream_t st) {
     const dim3 grid((unsigned)a.segments);
     const int vecs = (a.per + 7) / 8;
-    if (!wide || vecs > 4096) {
-        hipLaunchKernelGGL((norm_any_kernel<TX, TR, TO, MODE>), grid, dim3(256), 0, st, a);
+    if (vecs > 4096) {
+        hipLaunchKernelGGL((norm_long_kernel<TX, TR, TO, MODE>), grid, dim3(256), 0, st, a);
+        return;
+    }
+    // (32768 groups of 125: 18.8 us with a block each, 9.5 with 16 lanes)
+    if (vecs <= 64) {
+        const int per = vecs <= 16 ? 16 : 4;                // groups a block
+        const dim3 blocks((unsigned)((a.segments + per - 1) / per));
+        if (vecs <= 16) hipLaunchKernelGGL((norm_kernel<TX, TR, TO, MODE, 1, 16>), blocks, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((norm_kernel<TX, TR, TO, MODE, 1, 64>), blocks, dim3(256), 0, st, a);
         return;
     }
     const int vpt = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : 4;
     const dim3 block((unsigned)(((vecs + vpt - 1) / vpt + 63) / 64 * 64));
-    if (vpt == 1) hipLaunchKernelGGL((norm_kernel<TX, TR, TO, MODE, 1>), grid, block, 0, st, a);
-    else if (vpt == 2) hipLaunchKernelGGL((norm_kernel<TX, TR, TO, MODE, 2>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((norm_kernel<TX, TR, TO, MODE, 4>), grid, block, 0, st, a);
+    if (vpt == 1) hipLaunchKernelGGL((norm_kernel<TX, TR, TO, MODE, 1, 0>), grid, block, 0, st, a);
+    else if (vpt == 2) hipLaunchKernelGGL((norm_kernel<TX, TR, TO, MODE, 2, 0>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((norm_kernel<TX, TR, TO, MODE, 4, 0>), grid, block, 0, st, a);
 }
 template <typename TX, typename TO>
-static void norm_by_mode(const NormArgs &a, NormMode mode, bool residual_bf16, bool wide, hipStream_t st) {
-    if (mode == kPlain) norm_t<TX, TX, TO, kPlain>(a, wide, st);
-    else if (mode == kGate) norm_t<TX, TX, TO, kGate>(a, wide, st);
-    else if (residual_bf16) norm_t<TX, bf16, TO, kAdd>(a, wide, st);
-    else norm_t<TX, float, TO, kAdd>(a, wide, st);
+static void norm_by_mode(const NormArgs &a, NormMode mode, bool residual_bf16, hipStream_t st) {
+    if (mode == kPlain) norm_t<TX, TX, TO, kPlain>(a, st);
+    else if (mode == kGate) norm_t<TX, TX, TO, kGate>(a, st);
+    else if (residual_bf16) norm_t<TX, bf16, TO, kAdd>(a, st);
+    else norm_t<TX, float, TO, kAdd>(a, st);
 }
-
-static size_t bytes_of(Elem e) { return e == Elem::f32 ? 4 : e == Elem::bf16 ? 2 : 1; }
 
 void launch_rms_norm(const NormDims &d, const void *x, const void *gate, const void *residual,
                      const float *weight, void *out, uint8_t *out_scale, void *residual_out,
@@ -228,24 +274,16 @@ void launch_rms_norm(const NormDims &d, const void *x, const void *gate, const v
     const NormArgs a{x, residual ? residual : gate, weight, out, residual_out, out_scale,
                      d.xs, residual ? d.rs : d.gs, d.ros, d.os, d.rows * d.groups,
                      d.groups, d.hidden / d.groups, d.hidden, d.eps};
-    auto on = [](const void *p, int64_t stride, size_t e, size_t n) {
-        return reinterpret_cast<uintptr_t>(p) % n == 0 && (uint64_t)stride * e % n == 0;
-    };
-    const size_t ei = bytes_of(d.in), er = bytes_of(d.residual), eo = bytes_of(d.out);
-    const bool wide = a.per % 8 == 0 && on(x, d.xs, ei, 16) && on(gate, gate ? d.gs : 0, ei, 16) &&
-                      on(residual, residual ? d.rs : 0, er, 16) &&
-                      on(residual_out, residual_out ? d.ros : 0, er, 16) && on(weight, 0, 4, 16) &&
-                      on(out, d.os, eo, eo == 1 ? 8 : 16);
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     const bool rb = d.residual == Elem::bf16;
     if (d.in == Elem::bf16) {
-        if (d.out == Elem::f32) norm_by_mode<bf16, float>(a, mode, rb, wide, st);
-        else if (d.out == Elem::bf16) norm_by_mode<bf16, bf16>(a, mode, rb, wide, st);
-        else norm_by_mode<bf16, e4m3>(a, mode, rb, wide, st);
+        if (d.out == Elem::f32) norm_by_mode<bf16, float>(a, mode, rb, st);
+        else if (d.out == Elem::bf16) norm_by_mode<bf16, bf16>(a, mode, rb, st);
+        else norm_by_mode<bf16, e4m3>(a, mode, rb, st);
     } else {
-        if (d.out == Elem::f32) norm_by_mode<float, float>(a, mode, rb, wide, st);
-        else if (d.out == Elem::bf16) norm_by_mode<float, bf16>(a, mode, rb, wide, st);
-        else norm_by_mode<float, e4m3>(a, mode, rb, wide, st);
+        if (d.out == Elem::f32) norm_by_mode<float, float>(a, mode, rb, st);
+        else if (d.out == Elem::bf16) norm_by_mode<float, bf16>(a, mode, rb, st);
+        else norm_by_mode<float, e4m3>(a, mode, rb, st);
     }
 }
 
