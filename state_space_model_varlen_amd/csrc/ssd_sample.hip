@@ -219,9 +219,9 @@ void launch_probs(const ProbsDims &d, const void *logits, const float *temperatu
 // step, far less than the distance of a uniform number of 24 bits from a
 // border that it does not lie on.
 //
-// Two launches: the weights of every 2048 entries are summed (a wave each), then
-// one block a request finds the 2048 that the draw falls into and goes through
-// their entries. Bound by the rows' bytes, for few requests by the chain draft ->
+// Rows of up to 16 K entries are one block's work. Longer ones take two launches: the
+// weights of every 2048 entries are summed (a wave each), then one block a request
+// finds the 2048 that the draw falls into and goes through their entries. Bound by the rows' bytes, for few requests by the chain draft ->
 // its probabilities -> row.
 
 constexpr int kGrain = 2048, kPickThreads = 256, kPerThread = kGrain / kPickThreads;
@@ -234,18 +234,19 @@ struct Decision {
 __device__ __forceinline__ Decision decide(const VerifyDims &d, const VerifyArgs &a, int r) {
     const int lane = threadIdx.x & 63, most = d.T - 1;
     int n = a.count ? a.count[r] : most;
-    n = n < 0 ? 0 : (n > most ? most : n);
     bool ok = false;
-    if (lane < n) {
+    // (all drafts, whatever the count: it is not waited for)
+    if (lane < most) {
         const int tok = a.tokens[(int64_t)r * most + lane];
+        const float u = a.uniform[(int64_t)r * d.T + lane];
         if (tok >= 0 && tok < d.V) {
             const float p = a.target[((int64_t)r * d.T + lane) * d.ts + tok];
             const float q = a.draft ? a.draft[((int64_t)r * most + lane) * d.ds + tok] : 1.0f;
-            const float u = a.uniform[(int64_t)r * d.T + lane];
             // (an exact product; a draft probability that counts as zero is zero)
             ok = (double)u * (double)(q > 0.0f ? q : 0.0f) < (double)p;
         }
     }
+    n = n < 0 ? 0 : (n > most ? most : n);
     const uint64_t no = ~__ballot(ok);
     const int first = no ? __ffsll((unsigned long long)no) - 1 : 64;
     return Decision{n, first < n ? first : n};
@@ -323,9 +324,9 @@ __global__ __launch_bounds__(256) void verify_sums_kernel(VerifyDims d, VerifyAr
     }
 }
 
-// Inclusive sums over the block's threads, in their order.
-__device__ __forceinline__ double block_scan(double v, double *part) {
-    const int lane = threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+// Inclusive sums over the block's threads, in their order, and the sum of all.
+__device__ __forceinline__ double block_scan(double v, double *part, double &all) {
+    const int lane = threadIdx.x & 63, wave = (int)threadIdx.x >> 6, waves = (int)blockDim.x >> 6;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
         const double o = __shfl_up(v, off, kWave);
@@ -334,21 +335,87 @@ __device__ __forceinline__ double block_scan(double v, double *part) {
     if (lane == 63) part[wave] = v;
     __syncthreads();
     double before = 0.0;
-    for (int i = 0; i < wave; ++i) before += part[i];
+    all = 0.0;
+    for (int i = 0; i < waves; ++i) {
+        if (i < wave) before += part[i];
+        all += part[i];
+    }
     return before + v;
+}
+
+// The first place that passes `want` and the last of positive weight, over the block.
+struct Pick {
+    int found, last;
+    __device__ __forceinline__ void clear() {
+        found = 0x7fffffff;
+        last = -1;
+    }
+    __device__ __forceinline__ int place() const { return found != 0x7fffffff ? found : last; }
+};
+// A thread's N weights from place v0 on, behind weights of `before`.
+template <int N>
+__device__ __forceinline__ void pick_among(const double *w, int v0, double before, double want, Pick *p) {
+    int hit = 0x7fffffff, last = -1;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        before += w[j];
+        if (w[j] > 0.0) {
+            last = v0 + j;
+            if (hit == 0x7fffffff && before > want) hit = v0 + j;
+        }
+    }
+    if (hit != 0x7fffffff) atomicMin(&p->found, hit);
+    if (last >= 0) atomicMax(&p->last, last);
+}
+
+// A thread's N entries of the row: its weights against the draft, and the target's own.
+template <int N>
+__device__ __forceinline__ void weigh_run(const Row &row, int v0, int V, double *w, double *plain) {
+    float p[N], q[N] = {};
+#pragma unroll
+    for (int j = 0; j < N; j += 4) load_entries(row.p, v0 + j, V, p + j);
+    if (row.q)
+#pragma unroll
+        for (int j = 0; j < N; j += 4) load_entries(row.q, v0 + j, V, q + j);
+#pragma unroll
+    for (int j = 0; j < N; ++j) row.weigh(v0 + j, p[j], q[j], w[j], plain[j]);
+}
+
+// Rows of up to 16 K entries: all in one block a request, 16 entries a thread.
+constexpr int kWholePer = 16, kWholeMost = 1024 * kWholePer;
+__global__ __launch_bounds__(1024) void verify_whole_kernel(VerifyDims d, VerifyArgs a) {
+    __shared__ double part[2][16];
+    __shared__ Pick pick;
+    const int r = blockIdx.x, tid = threadIdx.x, v0 = tid * kWholePer;
+    const double uniform = (double)a.uniform[(int64_t)r * d.T + d.T - 1];
+    const Decision k = decide(d, a, r);
+    const Row row(d, a, r, k);
+    if (tid == 0) pick.clear();
+    double w[kWholePer], plain[kWholePer], sw = 0.0, sp = 0.0, tw, tp;
+    weigh_run<kWholePer>(row, v0, d.V, w, plain);
+#pragma unroll
+    for (int j = 0; j < kWholePer; ++j) {
+        sw += w[j];
+        sp += plain[j];
+    }
+    const double iw = block_scan(sw, part[0], tw), ip = block_scan(sp, part[1], tp);
+    if (tw > 0.0) pick_among<kWholePer>(w, v0, iw - sw, tw * uniform, &pick);
+    else pick_among<kWholePer>(plain, v0, ip - sp, tp * uniform, &pick);
+    __syncthreads();
+    if (tid == 0) a.accepted[r] = k.accepted;
+    for (int i = tid; i < d.T; i += (int)blockDim.x)
+        a.out[(int64_t)r * d.T + i] = i < k.accepted ? a.tokens[(int64_t)r * (d.T - 1) + i]
+                                      : i == k.accepted ? pick.place() : -1;
 }
 
 __global__ __launch_bounds__(kPickThreads) void verify_pick_kernel(VerifyDims d, VerifyArgs a, int grains,
                                                                    const double *__restrict__ sums)
 {
     __shared__ double part[3][kPickThreads / 64], start;
-    __shared__ int found[2], last[2];
+    __shared__ Pick pick[2];
     const int r = blockIdx.x, tid = threadIdx.x;
-    if (tid < 2) {
-        found[tid] = 0x7fffffff;
-        last[tid] = -1;
-    }
-    const float uniform = a.uniform[(int64_t)r * d.T + d.T - 1];
+    if (tid < 2) pick[tid].clear();
+    const double uniform = (double)a.uniform[(int64_t)r * d.T + d.T - 1];
     // the first launch's decision
     int n = a.count ? a.count[r] : d.T - 1;
     n = n < 0 ? 0 : (n > d.T - 1 ? d.T - 1 : n);
@@ -357,82 +424,62 @@ __global__ __launch_bounds__(kPickThreads) void verify_pick_kernel(VerifyDims d,
     const double *const s = sums + (int64_t)r * grains * 2;
     // a thread's grains follow one another
     const int per = (grains + kPickThreads - 1) / kPickThreads, g0 = tid * per;
-    double mw = 0.0, mp = 0.0;
-    for (int i = g0; i < g0 + per && i < grains; ++i) {
+    const int g1 = g0 + per < grains ? g0 + per : grains;
+    double mw = 0.0, mp = 0.0, tw, tp;
+    for (int i = g0; i < g1; ++i) {
         mw += s[2 * i];
         mp += s[2 * i + 1];
     }
-    const double iw = block_scan(mw, part[0]), ip = block_scan(mp, part[1]);
-    double tw = 0.0, tp = 0.0;
-#pragma unroll
-    for (int i = 0; i < kPickThreads / 64; ++i) {
-        tw += part[0][i];
-        tp += part[1][i];
-    }
+    const double iw = block_scan(mw, part[0], tw), ip = block_scan(mp, part[1], tp);
     const int which = tw > 0.0 ? 0 : 1;
-    const double want = (which ? tp : tw) * (double)uniform;
+    const double want = (which ? tp : tw) * uniform;
     // the first grain that passes `want`, or the last of positive weight
     double c = which ? ip - mp : iw - mw;
-    int hit = 0x7fffffff, lastpos = -1;
-    for (int i = g0; i < g0 + per && i < grains; ++i) {
+    for (int i = g0; i < g1; ++i) {
         const double w = s[2 * i + which];
-        if (w > 0.0) {
-            lastpos = i;
-            if (hit == 0x7fffffff && c + w > want) hit = i;
-        }
+        pick_among<1>(&w, i, c, want, &pick[0]);
         c += w;
     }
-    if (hit != 0x7fffffff) atomicMin(&found[0], hit);
-    if (lastpos >= 0) atomicMax(&last[0], lastpos);
     __syncthreads();
-    const int grain = found[0] != 0x7fffffff ? found[0] : last[0];
+    const int grain = pick[0].place();
     if (grain < 0) {                         // (the same in every thread)
         if (tid == 0) a.out[(int64_t)r * d.T + k.accepted] = -1;
         return;
     }
-    if (grain >= g0 && grain < g0 + per) {
+    if (grain >= g0 && grain < g1) {
         double b = which ? ip - mp : iw - mw;
         for (int i = g0; i < grain; ++i) b += s[2 * i + which];
         start = b;
     }
-    float pv[kPerThread], qv[kPerThread] = {};
     const int v0 = grain * kGrain + tid * kPerThread;
-#pragma unroll
-    for (int j = 0; j < kPerThread; j += 4) {
-        load_entries(row.p, v0 + j, d.V, pv + j);
-        if (row.q) load_entries(row.q, v0 + j, d.V, qv + j);
-    }
-    double w[kPerThread], mine = 0.0;
-    lastpos = -1;
+    double w[kPerThread], plain[kPerThread], mine = 0.0, all;
+    weigh_run<kPerThread>(row, v0, d.V, w, plain);
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) {
-        double x, p;
-        row.weigh(v0 + j, pv[j], qv[j], x, p);
-        w[j] = which ? p : x;
+        w[j] = which ? plain[j] : w[j];
         mine += w[j];
-        if (w[j] > 0.0) lastpos = v0 + j;
     }
-    const double incl = block_scan(mine, part[2]);          // (start is written by now)
-    c = start + (incl - mine);
-    hit = 0x7fffffff;
-#pragma unroll
-    for (int j = 0; j < kPerThread; ++j) {
-        c += w[j];
-        if (w[j] > 0.0 && c > want && hit == 0x7fffffff) hit = v0 + j;
-    }
-    if (hit != 0x7fffffff) atomicMin(&found[1], hit);
-    if (lastpos >= 0) atomicMax(&last[1], lastpos);
+    const double incl = block_scan(mine, part[2], all);          // (start is written by now)
+    pick_among<kPerThread>(w, v0, start + (incl - mine), want, &pick[1]);
     __syncthreads();
-    if (tid == 0) a.out[(int64_t)r * d.T + k.accepted] = found[1] != 0x7fffffff ? found[1] : last[1];
+    if (tid == 0) a.out[(int64_t)r * d.T + k.accepted] = pick[1].place();
 }
 
 static int grains_of(const VerifyDims &d) { return (d.V + kGrain - 1) / kGrain; }
-size_t verify_workspace(const VerifyDims &d) { return (size_t)d.R * grains_of(d) * 2 * sizeof(double); }
+size_t verify_workspace(const VerifyDims &d)
+{
+    return d.V <= kWholeMost ? 0 : (size_t)d.R * grains_of(d) * 2 * sizeof(double);
+}
 
 void launch_verify(const VerifyDims &d, const VerifyArgs &a, void *workspace, void *stream)
 {
     if (d.R <= 0) return;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    if (d.V <= kWholeMost) {
+        const int threads = ((d.V + kWholePer - 1) / kWholePer + 63) / 64 * 64;
+        hipLaunchKernelGGL(verify_whole_kernel, dim3((unsigned)d.R), dim3((unsigned)threads), 0, st, d, a);
+        return;
+    }
     const int grains = grains_of(d);
     double *const sums = static_cast<double *>(workspace);
     hipLaunchKernelGGL(verify_sums_kernel, dim3((unsigned)((grains + 3) / 4), (unsigned)d.R), dim3(256), 0, st, d, a,

@@ -15,27 +15,72 @@ import torch
 
 from . import _DT, _TORCH, _check, _lib
 from ._step_abi import linear_problem, norm_problem, probs_problem, verify_problem
-from .layer_ops import E4M3, _arr, _on, _rows, _with, _workspace
+from .layer_ops import E4M3, _arr, _on, _rows, _with
 
 _ROW_DT = {**_DT, torch.float8_e4m3fn: E4M3}
 _ROW_TORCH = {**_TORCH, E4M3: torch.float8_e4m3fn}
 
 
-def _call(name, stream, tensors, *args):
-    """Runs the entry point on the GPU that all the tensors lie on."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name}: tensors on different GPUs ({tensors[0].device} and "
-                             f"{t.device})")
+_T, _current, _stream_of = torch.Tensor, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _gpu(t):
+    """The GPU that the call runs on: its first tensor's (-2, which no tensor has: none)."""
+    dev = t.get_device() if isinstance(t, _T) else -1
+    return dev if dev >= 0 else -2
+
+
+def _same_gpu(t, name, dev):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, like the call's first tensor (got {t.device})")
+
+
+# (What is in order is passed with one look at each property, as in layer_ops: a call of a few
+# microseconds takes as long to check as to run. What is not goes there to be told why.)
+
+def _row(t, name, dtype, shape, dev, optional=False):
+    """Pointer and row distance of t, whose rows are its last dimension."""
+    if type(t) is _T and t.dtype is dtype and t.shape == shape and t.get_device() == dev \
+            and t.is_contiguous():
+        return t.data_ptr() or 16, shape[-1]
+    if t is None and optional:
+        return None, 0
+    got = _rows(t, name, dtype, shape, 1)
+    _same_gpu(t, name, dev)
+    return got
+
+
+def _array(t, name, dtype, shape, dev, optional=False):
+    """Pointer of a contiguous array."""
+    if type(t) is _T and t.dtype is dtype and t.shape == shape and t.get_device() == dev \
+            and t.is_contiguous():
+        return t.data_ptr() or 16
+    if t is None and optional:
+        return None
+    got = _arr(t, name, dtype, shape)
+    _same_gpu(t, name, dev)
+    return got
+
+
+def _space(w, dev):
+    """Pointer and size of a workspace."""
+    if w is None:
+        return None, 0
+    n = w.numel() if isinstance(w, _T) else 0
+    return _array(w, "workspace", torch.uint8, (n,), dev), n
+
+
+def _call(name, fn, stream, dev, *args):
+    """Runs the entry point on the GPU that its tensors lie on."""
     if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
-        raise ValueError(f"{name}: the stream is not of {tensors[0].device}")
-    if dev == torch._C._cuda_getDevice():
-        rc = getattr(_lib, name)(*args, _on(stream))
+        raise ValueError(f"{name}: the stream is not of cuda:{dev}")
+    if dev == _current():
+        rc = fn(*args, _stream_of(dev) if stream is None else _on(stream))
     else:
         with torch.cuda.device(dev):
-            rc = getattr(_lib, name)(*args, _on(stream))
-    _check(name, rc)
+            rc = fn(*args, _stream_of(dev) if stream is None else _on(stream))
+    if rc:
+        _check(name, rc)
 
 
 def _alloc(n, device):
@@ -62,7 +107,7 @@ def rms_norm(p: norm_problem, x, weight, out, residual=None, residual_out=None, 
     """out = v / sqrt(mean(v^2) + eps) * weight, v = x, x + residual or x * silu(gate): [rows,
     hidden] each. residual_out keeps the sum (it may be residual itself). weight [hidden] float32
     or None. out_scale [rows,hidden/32] uint8 with 8-bit rows."""
-    q, row = type(p).from_buffer_copy(p), (p.rows, p.hidden)
+    q, row, dev = type(p).from_buffer_copy(p), (p.rows, p.hidden), _gpu(x)
     ti, tr, e4m3 = _TORCH[p.in_dtype], _TORCH[p.residual_dtype], p.out_dtype == E4M3
     if not e4m3 and out_scale is not None:
         raise ValueError("out_scale belongs to 8-bit rows")
@@ -70,14 +115,14 @@ def rms_norm(p: norm_problem, x, weight, out, residual=None, residual_out=None, 
         raise ValueError("residual_out needs residual")
     if gate is not None and residual is not None:
         raise ValueError("gate and residual exclude each other")
-    xp, q.x_stride = _rows(x, "x", ti, row, 1)
-    gp, q.gate_stride = _rows(gate, "gate", ti, row, 1, True)
-    rp, q.residual_stride = _rows(residual, "residual", tr, row, 1, True)
-    sp, q.residual_out_stride = _rows(residual_out, "residual_out", tr, row, 1, True)
-    op, q.out_stride = _rows(out, "out", _ROW_TORCH[p.out_dtype], row, 1)
-    _call("rms_norm", stream, (x, gate, residual, weight, out, out_scale, residual_out),
-          ctypes.byref(q), xp, gp, rp, _arr(weight, "weight", torch.float32, (p.hidden,), True), op,
-          _arr(out_scale, "out_scale", torch.uint8, (p.rows, p.hidden // 32), not e4m3), sp)
+    xp, q.x_stride = _row(x, "x", ti, row, dev)
+    gp, q.gate_stride = _row(gate, "gate", ti, row, dev, True)
+    rp, q.residual_stride = _row(residual, "residual", tr, row, dev, True)
+    sp, q.residual_out_stride = _row(residual_out, "residual_out", tr, row, dev, True)
+    op, q.out_stride = _row(out, "out", _ROW_TORCH[p.out_dtype], row, dev)
+    _call("rms_norm", _lib.rms_norm, stream, dev, ctypes.byref(q), xp, gp, rp,
+          _array(weight, "weight", torch.float32, (p.hidden,), dev, True), op,
+          _array(out_scale, "out_scale", torch.uint8, (p.rows, p.hidden // 32), dev, not e4m3), sp)
 
 
 # ---------------------------------------------------------------------------
@@ -113,10 +158,10 @@ def alloc_linear_weights(p: linear_problem, device="cuda") -> dict:
                 weight_scale=torch.ones(n, k // 32, dtype=torch.uint8, device=device))
 
 
-def _weights(p, weight, weight_scale):
+def _weights(p, weight, weight_scale, dev):
     n, k = p.out_features, p.in_features
-    return (_arr(weight, "weight", torch.uint8, (n, k // 2)),
-            _arr(weight_scale, "weight_scale", torch.uint8, (n, k // 32)))
+    return (_array(weight, "weight", torch.uint8, (n, k // 2), dev),
+            _array(weight_scale, "weight_scale", torch.uint8, (n, k // 32), dev))
 
 
 def linear_w4(p: linear_problem, x, weight, weight_scale, out, x_scale=None, bias=None,
@@ -127,22 +172,24 @@ def linear_w4(p: linear_problem, x, weight, weight_scale, out, x_scale=None, bia
     T, K, N, e4m3 = p.tokens, p.in_features, p.out_features, p.x_dtype == E4M3
     if not e4m3 and x_scale is not None:
         raise ValueError("x_scale belongs to 8-bit rows")
-    xp, xs = _rows(x, "x", _ROW_TORCH[p.x_dtype], (T, K), 1)
-    op, os_ = _rows(out, "out", _TORCH[p.out_dtype], (T, N), 1)
-    _call("linear_w4", stream, (x, weight, weight_scale, out, x_scale, bias, workspace),
+    dev = _gpu(x)
+    xp, xs = _row(x, "x", _ROW_TORCH[p.x_dtype], (T, K), dev)
+    op, os_ = _row(out, "out", _TORCH[p.out_dtype], (T, N), dev)
+    _call("linear_w4", _lib.linear_w4, stream, dev,
           ctypes.byref(_with(p, x_stride=xs, out_stride=os_)), xp,
-          _arr(x_scale, "x_scale", torch.uint8, (T, K // 32), not e4m3),
-          *_weights(p, weight, weight_scale), _arr(bias, "bias", torch.float32, (N,), True), op,
-          *_workspace(workspace))
+          _array(x_scale, "x_scale", torch.uint8, (T, K // 32), dev, not e4m3),
+          *_weights(p, weight, weight_scale, dev),
+          _array(bias, "bias", torch.float32, (N,), dev, True), op, *_space(workspace, dev))
 
 
 def linear_w4_encode(p: linear_problem, w, weight, weight_scale, stream=None):
     """w [N,K] float32 or bfloat16 as 4-bit codes and scales."""
     if not isinstance(w, torch.Tensor) or w.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("w must be a float32 or bfloat16 tensor")
-    _call("linear_w4_encode", stream, (w, weight, weight_scale), ctypes.byref(p), _DT[w.dtype],
-          _arr(w, "w", w.dtype, (p.out_features, p.in_features)),
-          *_weights(p, weight, weight_scale))
+    dev = _gpu(w)
+    _call("linear_w4_encode", _lib.linear_w4_encode, stream, dev, ctypes.byref(p), _DT[w.dtype],
+          _array(w, "w", w.dtype, (p.out_features, p.in_features), dev),
+          *_weights(p, weight, weight_scale, dev))
 
 
 # ---------------------------------------------------------------------------
@@ -168,13 +215,13 @@ def alloc_probs_workspace(p: probs_problem, device="cuda"):
 def token_probs(p: probs_problem, logits, temperature, probs, workspace=None, stream=None):
     """probs [R,T,V] float32 = softmax(logits [R,T,V] / temperature [R]); a temperature of 0: 1 on
     the first of the largest. temperature None: 1. workspace: alloc_probs_workspace(p)."""
-    row = (p.num_reqs, p.tokens_per_req, p.vocab)
-    lp, ls = _rows(logits, "logits", _TORCH[p.in_dtype], row, 1)
-    pp, ps = _rows(probs, "probs", torch.float32, row, 1)
-    _call("token_probs", stream, (logits, temperature, probs, workspace),
+    row, dev = (p.num_reqs, p.tokens_per_req, p.vocab), _gpu(logits)
+    lp, ls = _row(logits, "logits", _TORCH[p.in_dtype], row, dev)
+    pp, ps = _row(probs, "probs", torch.float32, row, dev)
+    _call("token_probs", _lib.token_probs, stream, dev,
           ctypes.byref(_with(p, logits_stride=ls, probs_stride=ps)), lp,
-          _arr(temperature, "temperature", torch.float32, (p.num_reqs,), True), pp,
-          *_workspace(workspace))
+          _array(temperature, "temperature", torch.float32, (p.num_reqs,), dev, True), pp,
+          *_space(workspace, dev))
 
 
 # ---------------------------------------------------------------------------
@@ -203,16 +250,15 @@ def verify_drafts(p: verify_problem, target_probs, draft_probs, draft_tokens, nu
     (None with T = 1), num_drafts [R] int32 (None: T-1 each) and uniform [R,T] in [0, 1).
     workspace: alloc_verify_workspace(p)."""
     R, T, V, i32, f32 = p.num_reqs, p.tokens_per_req, p.vocab, torch.int32, torch.float32
-    tp, ts = _rows(target_probs, "target_probs", f32, (R, T, V), 1)
+    dev = _gpu(target_probs)
+    tp, ts = _row(target_probs, "target_probs", f32, (R, T, V), dev)
+    dp, ds, tok = None, 0, None
     if T > 1:
-        dp, ds = _rows(draft_probs, "draft_probs", f32, (R, T - 1, V), 1, True)
-    else:
-        draft_probs = draft_tokens = dp = None
-        ds = 0
-    _call("verify_drafts", stream,
-          (target_probs, draft_probs, draft_tokens, num_drafts, uniform, num_accepted, tokens,
-           workspace), ctypes.byref(_with(p, target_stride=ts, draft_stride=ds)), tp, dp,
-          _arr(draft_tokens, "draft_tokens", i32, (R, T - 1), T == 1),
-          _arr(num_drafts, "num_drafts", i32, (R,), True), _arr(uniform, "uniform", f32, (R, T)),
-          _arr(num_accepted, "num_accepted", i32, (R,)), _arr(tokens, "tokens", i32, (R, T)),
-          *_workspace(workspace))
+        dp, ds = _row(draft_probs, "draft_probs", f32, (R, T - 1, V), dev, True)
+        tok = _array(draft_tokens, "draft_tokens", i32, (R, T - 1), dev)
+    _call("verify_drafts", _lib.verify_drafts, stream, dev,
+          ctypes.byref(_with(p, target_stride=ts, draft_stride=ds)), tp, dp, tok,
+          _array(num_drafts, "num_drafts", i32, (R,), dev, True),
+          _array(uniform, "uniform", f32, (R, T), dev),
+          _array(num_accepted, "num_accepted", i32, (R,), dev),
+          _array(tokens, "tokens", i32, (R, T), dev), *_space(workspace, dev))

@@ -130,9 +130,9 @@ def test_verify(R, T, V, q):
     check_verify(p, dq, d, n, u)
 
 
-@pytest.mark.parametrize("V", [4095, 4096, 4097, 8193, 20000])
+@pytest.mark.parametrize("V", [1023, 1025, 4096, 8193, 16383, 16384, 16385, 20000, 38913])
 def test_verify_long_rows(V):
-    """More than one segment of a row, ends inside and on one."""
+    """Rows of one block and of many grains, ends inside and on them."""
     p, dq, d, u = drafts_for(V, 4, 3, V)
     check_verify(p, dq, d, None, u)
     check_verify(p, None, d, None, u)
@@ -140,12 +140,19 @@ def test_verify_long_rows(V):
     check_verify(p, dq, d, torch.tensor([0, 1, 2, 0], dtype=I32), u)
 
 
-def test_verify_borders():
-    """Draws that lie on a border of the sums, drafts whose test is an equality."""
-    p = torch.tensor([[[0.25, 0.5, 0.0, 0.25]]]).repeat(9, 1, 1)
+@pytest.mark.parametrize("V", [4, 20000])
+def test_verify_borders_of_sums(V):
+    """Draws that lie on a border of the sums, past it by the least, or at an end."""
+    p = torch.zeros(9, 1, V)
+    at = [0, V // 4, V // 2, V - 1]
+    p[:, 0, at] = torch.tensor([0.25, 0.5, 0.0, 0.25])
     u = torch.tensor([[0.0], [0.2], [0.25], [0.5], [0.75], [0.76], [0.74999], [0.9999], [1.0]])
     _, tok = verify(p, None, None, None, u)
-    assert tok[:, 0].tolist() == [0, 0, 1, 1, 3, 3, 1, 3, 3]
+    assert tok[:, 0].tolist() == [at[i] for i in [0, 0, 1, 1, 3, 3, 1, 3, 3]]
+
+
+def test_verify_borders():
+    """Drafts whose test is an equality."""
     # u q < p is strict; a probability of zero is never accepted, one of the draft's zero always
     p = torch.tensor([[[0.5, 0.5, 0.0], [0.0, 1.0, 0.0]]]).repeat(4, 1, 1)
     q = torch.tensor([[[0.5, 0.25, 0.25]]]).repeat(4, 1, 1)
@@ -173,10 +180,11 @@ def test_verify_odd_probabilities():
     acc, tok = check_verify(p, q, d, None, u)
     assert acc[4] == 0 and tok[4].tolist() == [-1, -1, -1]
     check_verify(p, None, d, None, u)
-    pr = torch.zeros(2, 1, 5000)
-    pr[0, 0, 4999] = 1e-38
-    _, tok = verify(pr, None, None, None, torch.tensor([[0.999], [0.5]]))
-    assert tok[:, 0].tolist() == [4999, -1]
+    for V in (5000, 50000):
+        pr = torch.zeros(2, 1, V)
+        pr[0, 0, V - 1] = 1e-38
+        _, tok = verify(pr, None, None, None, torch.tensor([[0.999], [0.5]]))
+        assert tok[:, 0].tolist() == [V - 1, -1]
 
 
 def test_verify_strides():
@@ -269,3 +277,27 @@ def test_no_requests():
     probs(torch.empty(0, 3, 9))
     ssd.verify_drafts(ssd.make_verify_problem(0, 2, 9), e(0, 2, 9), None, e(0, 1, dtype=I32), None, e(0, 2),
                       e(0, dtype=I32), e(0, 2, dtype=I32))
+
+
+def test_tensors_that_are_turned_down():
+    """Tensors that do not fit are told on the host; a parameter is a tensor too; a stream is taken."""
+    p = ssd.make_probs_problem(1, 1, 64, F32)
+    x = torch.randn(1, 1, 64, device=DEV)
+    out = torch.empty_like(x)
+    with pytest.raises(ValueError, match="GPU"):
+        ssd.token_probs(p, x, torch.ones(1), out)
+    with pytest.raises(ValueError, match="shape"):
+        ssd.token_probs(p, x[..., :32], None, out)
+    with pytest.raises(ValueError, match="float32"):
+        ssd.token_probs(p, x, None, out.half())
+    with pytest.raises(ValueError, match="contiguous"):
+        ssd.token_probs(p, x, None, torch.empty(1, 1, 128, device=DEV)[..., ::2])
+    ssd.token_probs(p, torch.nn.Parameter(x), None, out)
+    check_probs(out, x.cpu())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out.zero_()
+    side.wait_stream(torch.cuda.current_stream())
+    ssd.token_probs(p, x, None, out, stream=side)
+    side.synchronize()
+    check_probs(out, x.cpu())

@@ -177,6 +177,8 @@ def test_verify_pointers():
         assert call_verify(p, (i, None)) == NULL, i
     for i in range(7):
         assert call_verify(p, (i, OFF)) == ALIGN, i
+    assert ssd.verify_drafts_workspace_bytes(p) == 0
+    p = verify(vocab=20000)
     need = ssd.verify_drafts_workspace_bytes(p)
     assert need > 0
     assert call_verify(p, ws=need - 1) == WORK
