@@ -267,6 +267,7 @@ __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) 
     constexpr int LS = (SO + SW + THREADS - 1) / THREADS;
     constexpr int LOADS = LX + LW + LS;
     static_assert(RT == 1 || RT == 2 || RT == 4 || RT == 8, "whole stores");
+    static_assert(LX == 1 || TOK * 8 % THREADS == 0, "loads that are all of the tile's tokens");
     static_assert(NSUB % WK == 0 && LOADS * NSUB * (NBUF - 2) < 64, "waits that can be counted");
     // chunks and words of a step, rounded up to a wave's load; every wave makes the same number of
     // loads, those that have nothing to bring into `spare`
@@ -413,7 +414,7 @@ __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) 
 #pragma unroll
                 for (int i = 0; i < 2; ++i) wf[r][i] = *reinterpret_cast<const uint32_t *>(w + r * (256 * CW) + 16 * i + 4 * g);
             // (fragments of the tokens are read AHEAD before they are multiplied)
-                        constexpr int AHEAD = 3;
+            constexpr int AHEAD = 3;
             bf16x8 f[AHEAD + 1];
             auto take = [&](int k) __attribute__((always_inline)) {
                 f[k % (AHEAD + 1)] = *reinterpret_cast<const bf16x8 *>(x + k % TT * 2048 + 16 * ((4 * (k / TT) + g) ^ turn));
@@ -566,21 +567,25 @@ static LinearMode linear_mode(const LinearDims &d) {
 // 18560 (TFLOP/s of 8-bit and bfloat16 rows; the whole chip), or its stages at the time of one;
 // and a time a round of blocks. On 105 sizes (1 to 4096 tokens, 512 to 8192 values, 300 to 18560
 // outputs) the tile so taken was on average 0.9 % (8 bits) and 0.8 % (bfloat16) slower than the best of
-// them, at most 22 and 18 %.
+// them, at most 22 and 18 %. 192 x 256 was added where tiles of 256 leave CUs without one: 4096 tokens, 5120
+// to 2560 are 220 of them, not 160 (8 bits 56.7 -> 51.1 us, bfloat16 119.9 -> 104.2); 2048 tokens, 2560 to
+// 10576: 67.0 -> 58.1, 128.8 -> 114.8.
 struct Tile {
     int tokens, rows, per_cu, steps;      // steps of 128 (bfloat16: 64) values a stage
     double rate8, rate16;
 };
 static constexpr Tile kTiles[] = {
     {16, 16, 2, 4, 224, 103}, {16, 32, 2, 1, 369, 191}, {32, 32, 1, 4, 385, 246}, {64, 64, 2, 2, 898, 576},
-    {128, 128, 2, 1, 1793, 1014}, {256, 256, 1, 1, 2507, 1341}, {128, 256, 1, 1, 1760, 0}};
-static const char *const kTileNames[] = {"16x16", "16x32", "32x32", "64x64", "128x128", "256x256", "128x256"};
+    {128, 128, 2, 1, 1793, 1014}, {256, 256, 1, 1, 2507, 1341}, {192, 256, 1, 1, 2250, 1200},
+    {128, 256, 1, 1, 1760, 0}};
+static const char *const kTileNames[] = {"16x16",   "16x32",   "32x32",   "64x64",
+                                         "128x128", "256x256", "192x256", "128x256"};
 
 static int linear_tile_of(const LinearDims &d) {
     const bool wide = !d.e4m3;
     int best = 0;
     double least = 0;
-    for (int i = 0; i < (wide ? 6 : 7); ++i) {
+    for (int i = 0; i < (wide ? 7 : 8); ++i) {
         const Tile &t = kTiles[i];
         const int64_t blocks = (int64_t)((d.T + t.tokens - 1) / t.tokens) * ((d.N + t.rows - 1) / t.rows);
         const int64_t most = (blocks + 255) / 256, rounds = (most + t.per_cu - 1) / t.per_cu;     // of a CU
@@ -640,6 +645,7 @@ static void linear_t(const LinearDims &d, const LinearArgs &a, hipStream_t st) {
     case 5:
         // (scales of a byte a word leave room for two buffers)
         return linear_tile<MODE, 2, 4, 1, 8, 4, 1, WORDS || MODE == kSixteen ? 3 : 2, WORDS, 1, TO>(d, a, st);
+    case 6: return linear_tile<MODE, 2, 4, 1, 6, 4, 1, 3, WORDS, 1, TO>(d, a, st);
     default:
         if constexpr (MODE != kSixteen) linear_tile<MODE, 2, 4, 1, 4, 4, 1, 3, WORDS, 1, TO>(d, a, st);
     }

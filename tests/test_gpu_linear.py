@@ -72,7 +72,7 @@ def test_whole_numbers(T, K, N, xt):
 
 # a size for each tile that is built (per type of the rows), K ending inside a step or not
 TILES = {"few": (4, 2560, 300), "16x16": (12, 4096, 300), "16x32": (16, 512, 9000), "32x32": (64, 1024, 2600),
-         "64x64": (32, 256, 9000), "128x128": (200, 256, 9000), "256x256": (1024, 512, 9000),
+         "64x64": (32, 256, 9000), "128x128": (200, 256, 9000), "256x256": (1700, 512, 9000), "192x256": (1150, 512, 9000),
          "128x256": (384, 640, 18560)}           # (of 8-bit rows alone)
 
 
