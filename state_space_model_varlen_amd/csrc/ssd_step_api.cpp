@@ -33,6 +33,9 @@ int launch_status()
     return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 
+// A launch has at most 2^32 - 1 threads in a direction.
+bool launches(int64_t blocks, int64_t threads) { return blocks <= 0xffffffffLL / threads; }
+
 int workspace_ok(const void *workspace, size_t given, size_t need)
 {
     if (need == 0) return SSD_OK;
@@ -51,8 +54,8 @@ int norm_dims(const norm_problem *p, ssd::NormDims *d)
         return SSD_ERR_DTYPE;
     if (!(p->eps >= 0.0f) || !std::isfinite(p->eps)) return SSD_ERR_SHAPE;
     if (p->out_dtype == SSD_E4M3 && p->hidden / p->ngroups % 32 != 0) return SSD_ERR_UNSUPPORTED;
-    // grid limit: a block takes at least one part of a row
-    if ((int64_t)p->rows * p->ngroups > 0x7fffffffLL) return SSD_ERR_UNSUPPORTED;
+    const int per = p->hidden / p->ngroups, lanes = per <= 128 ? 16 : per <= 512 ? 64 : per / 8 + 64;
+    if (!launches((int64_t)p->rows * p->ngroups, lanes < 1024 ? lanes : 1024)) return SSD_ERR_UNSUPPORTED;
     const int64_t h = p->hidden;
     if (!stride_of(p->x_stride, h, &d->xs) || !stride_of(p->gate_stride, h, &d->gs) ||
         !stride_of(p->residual_stride, h, &d->rs) ||
@@ -80,8 +83,9 @@ int linear_dims(const linear_problem *p, ssd::LinearDims *d)
         return SSD_ERR_SHAPE;
     // a tile of up to 256 rows of x or of the weights is addressed by 32-bit byte offsets
     if (d->xs > (1 << 21) || p->in_features > (1 << 21)) return SSD_ERR_UNSUPPORTED;
-    // grid limit: tiles of at least 16 tokens by 16 outputs
-    if (((int64_t)p->tokens / 16 + 1) * ((int64_t)p->out_features / 16 + 1) > 0x7fffffffLL)
+    // (the largest tile: 256 tokens by 256 outputs, 512 threads; a block of few tokens: 16 outputs)
+    if (!launches(((int64_t)p->tokens / 256 + 1) * ((int64_t)p->out_features / 256 + 1), 512) ||
+        !launches((int64_t)p->out_features / 16 + 1, 256))
         return SSD_ERR_UNSUPPORTED;
     d->T = p->tokens;
     d->K = p->in_features;
@@ -99,9 +103,9 @@ int probs_dims(const probs_problem *p, ssd::ProbsDims *d)
     if (!stride_of(p->logits_stride, p->vocab, &d->ls) ||
         !stride_of(p->probs_stride, p->vocab, &d->ps))
         return SSD_ERR_SHAPE;
-    // grid limit: rows times their parts of at least 4096 logits
+    // (whole rows by up to 1024 threads, or parts of at least 4096 logits by 256)
     const int64_t rows = (int64_t)p->num_reqs * p->tokens_per_req;
-    if (p->vocab > (1 << 27) || rows > 0x7fffffffLL || rows * (p->vocab / 4096 + 1) > 0x7fffffffLL)
+    if (p->vocab > (1 << 27) || !launches(rows, 1024) || !launches(rows * (p->vocab / 4096 + 1), 256))
         return SSD_ERR_UNSUPPORTED;
     d->R = p->num_reqs;
     d->T = p->tokens_per_req;
@@ -190,7 +194,7 @@ int linear_w4_encode(const linear_problem *p, int32_t dtype, const void *w, uint
     if (p->in_features <= 0 || p->out_features <= 0) return SSD_ERR_SHAPE;
     if (!float_ok(dtype)) return SSD_ERR_DTYPE;
     if (p->in_features % 32 != 0 ||
-        (int64_t)p->in_features / 32 * p->out_features > 0x7fffffffLL * 32)
+        !launches((int64_t)p->in_features / 32 * p->out_features + 255, 1))
         return SSD_ERR_UNSUPPORTED;
     if (!w || !weight || !weight_scale) return SSD_ERR_NULL;
     if (!aligned(w, 16) || !aligned(weight, 16)) return SSD_ERR_ALIGN;

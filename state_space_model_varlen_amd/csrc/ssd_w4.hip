@@ -571,23 +571,24 @@ static LinearMode linear_mode(const LinearDims &d) {
 // to 2560 are 220 of them, not 160 (8 bits 56.7 -> 51.1 us, bfloat16 119.9 -> 104.2); 2048 tokens, 2560 to
 // 10576: 67.0 -> 58.1, 128.8 -> 114.8.
 struct Tile {
-    int tokens, rows, per_cu, steps;      // steps of 128 (bfloat16: 64) values a stage
+    int tokens, rows, threads, per_cu, steps;      // steps of 128 (bfloat16: 64) values a stage
     double rate8, rate16;
 };
 static constexpr Tile kTiles[] = {
-    {16, 16, 2, 4, 224, 103}, {16, 32, 2, 1, 369, 191}, {32, 32, 1, 4, 385, 246}, {64, 64, 2, 2, 898, 576},
-    {128, 128, 2, 1, 1793, 1014}, {256, 256, 1, 1, 2507, 1341}, {192, 256, 1, 1, 2250, 1200},
-    {128, 256, 1, 1, 1760, 0}};
+    {16, 16, 256, 2, 4, 224, 103},      {16, 32, 128, 2, 1, 369, 191},     {32, 32, 256, 1, 4, 385, 246},
+    {64, 64, 256, 2, 2, 898, 576},      {128, 128, 512, 2, 1, 1793, 1014}, {256, 256, 512, 1, 1, 2507, 1341},
+    {192, 256, 512, 1, 1, 2250, 1200},  {128, 256, 512, 1, 1, 1760, 0}};
 static const char *const kTileNames[] = {"16x16",   "16x32",   "32x32",   "64x64",
                                          "128x128", "256x256", "192x256", "128x256"};
 
 static int linear_tile_of(const LinearDims &d) {
     const bool wide = !d.e4m3;
-    int best = 0;
+    int best = -1;
     double least = 0;
     for (int i = 0; i < (wide ? 7 : 8); ++i) {
         const Tile &t = kTiles[i];
         const int64_t blocks = (int64_t)((d.T + t.tokens - 1) / t.tokens) * ((d.N + t.rows - 1) / t.rows);
+        if (blocks > 0xffffffffLL / t.threads) continue;      // (more than a launch takes; of the largest never)
         const int64_t most = (blocks + 255) / 256, rounds = (most + t.per_cu - 1) / t.per_cu;     // of a CU
         const double bytes = (double)d.K * ((d.T < t.tokens ? d.T : t.tokens) * (wide ? 2 : 1) + t.rows * 0.53);
         const double flops = 2.0 * t.tokens * t.rows * d.K;
@@ -598,7 +599,7 @@ static int linear_tile_of(const LinearDims &d) {
         const double by_stages = rounds * stages * (wide ? 0.269 * (1 + 0.264 * t.steps) : 0.162 * (1 + 0.267 * t.steps));
         double time = by_bytes > by_products ? by_bytes : by_products;
         time = (time > by_stages ? time : by_stages) + rounds * (wide ? 0.947 : 1.43);
-        if (i == 0 || time < least) {
+        if (best < 0 || time < least) {
             least = time;
             best = i;
         }

@@ -173,6 +173,30 @@ def test_non_finite_stay_in_their_rows(T, xt):
     assert np.array_equal(got[clean], want[clean])
 
 
+@pytest.mark.parametrize("to", [BF, F32])
+@pytest.mark.parametrize("xt", [BF, E4])
+@pytest.mark.parametrize("T", [1, 6, 30, 100, 1100])
+def test_scales_of_nan(T, xt, to):
+    """A scale byte of 255 is NaN whatever it scales, zeros too; the rest is untouched."""
+    K, N = 160, 300
+    codes, ws, x, xs, w, xv = make(T, T, K, N, xt, True)
+    codes[9, 16:32] = 0
+    ws[9, 1] = ws[130, 4] = 255
+    rows = torch.ones(T, dtype=torch.bool)
+    if xt == E4 and T > 1:
+        x = x.float()
+        x[2, 64:96] = 0
+        x = x.to(E4)
+        xs[2, 2] = xs[T - 1, 0] = 255
+        rows[2] = rows[T - 1] = False
+    outs = torch.ones(N, dtype=torch.bool)
+    outs[9] = outs[130] = False
+    got = run(codes, ws, x, xs, N, to).cpu()
+    assert bool(got[:, ~outs].isnan().all()) and bool(got[~rows].isnan().all())
+    want = torch.from_numpy(os_.linear(np.nan_to_num(xv), np.nan_to_num(w))[0])
+    assert torch.equal(got[rows][:, outs], want[rows][:, outs].to(to))
+
+
 @pytest.mark.parametrize("xt", [BF, E4])
 def test_ends_of_the_scales(xt):
     """Scale bytes over their whole range, one weight block each: results in float32's range are

@@ -40,6 +40,9 @@ def call_norm(p, *over, residual=OK, gate=None, scale=None, keep=OK):
     (dict(residual_stride=63), SHAPE), (dict(residual_out_stride=-64), SHAPE), (dict(out_stride=1), SHAPE),
     (dict(gate_stride=63), SHAPE), (dict(out_dtype=3, ngroups=4), UNSUP),
     (dict(out_dtype=3, hidden=48), UNSUP), (dict(rows=2 ** 31 - 1, ngroups=2), UNSUP),
+    # more threads than a launch takes
+    (dict(rows=2 ** 28, hidden=1), UNSUP), (dict(rows=2 ** 26, hidden=512), UNSUP),
+    (dict(rows=2 ** 22, hidden=32768), UNSUP),
     (dict(out_dtype=3), NULL),                            # no scales
 ])
 def test_norm_refusals(kw, status):
@@ -74,7 +77,7 @@ def call_linear(p, *over, ws=1 << 40):
     (dict(x_dtype=0), DTYPE), (dict(x_dtype=2), DTYPE), (dict(out_dtype=2), DTYPE), (dict(out_dtype=3), DTYPE),
     (dict(in_features=48), UNSUP), (dict(in_features=33), UNSUP), (dict(x_stride=63), SHAPE),
     (dict(out_stride=47), SHAPE), (dict(x_stride=2 ** 21 + 32), UNSUP), (dict(in_features=2 ** 21 + 32), UNSUP),
-    (dict(tokens=2 ** 31 - 1, out_features=2 ** 20), UNSUP),
+    (dict(tokens=2 ** 31 - 1, out_features=2 ** 20), UNSUP), (dict(out_features=2 ** 28), UNSUP),
 ])
 def test_linear_refusals(kw, status):
     p = linear(**kw)
@@ -98,21 +101,29 @@ def test_linear_pointers():
     assert enc(p, 2, OK, OK, OK) == DTYPE and enc(p, 0, ODD, OK, OK) == ALIGN and enc(p, 0, OK, ODD, OK) == ALIGN
     assert enc(linear(in_features=16), 0, OK, OK, OK) == UNSUP
     assert enc(linear(out_features=0), 0, OK, OK, OK) == SHAPE
+    assert enc(linear(in_features=2 ** 20, out_features=2 ** 17), 0, OK, OK, OK) == UNSUP
     assert LIB.linear_w4_encode(None, 0, OK, OK, OK, None) == NULL
 
 
+def test_tiles_fit_a_launch():
+    """Small tiles of more threads than a launch takes give way to larger ones."""
+    threads = {"16x16": 256, "16x32": 128, "32x32": 256, "64x64": 256}
+    for t, n in ((17, 2 ** 27), (16, 2 ** 28 - 2 ** 10), (2 ** 17, 2 ** 17), (2 ** 21, 2 ** 17), (100, 2 ** 27)):
+        for k in (32, 4096):
+            name = ssd.linear_w4_kernel(linear(tokens=t, in_features=k, out_features=n))
+            rows, cols = map(int, name.split("x"))
+            assert -(-t // rows) * -(-n // cols) * threads.get(name, 512) < 2 ** 32, (t, n, k, name)
+
+
 def test_linear_workspace_is_checked():
-    seen = 0
     for t in (1, 16, 64, 100, 300):
         for k in (64, 1024, 8192):
             p = linear(tokens=t, in_features=k)
             need = ssd.linear_w4_workspace_bytes(p)
             if need:
-                seen += 1
                 assert call_linear(p, ws=need - 1) == WORK
                 assert call_linear(p, (6, None), ws=need) == NULL
                 assert call_linear(p, (6, ODD), ws=need) == ALIGN
-    assert seen >= 0
 
 
 def probs(**kw):
@@ -130,6 +141,7 @@ def call_probs(p, *over, ws=1 << 40):
     (dict(num_reqs=-1), SHAPE), (dict(tokens_per_req=-1), SHAPE), (dict(vocab=0), SHAPE), (dict(in_dtype=2), DTYPE),
     (dict(in_dtype=3), DTYPE), (dict(logits_stride=99), SHAPE), (dict(probs_stride=99), SHAPE),
     (dict(vocab=2 ** 27 + 1), UNSUP), (dict(num_reqs=2 ** 30), UNSUP), (dict(num_reqs=2 ** 17, vocab=2 ** 26), UNSUP),
+    (dict(num_reqs=2 ** 21, vocab=1), UNSUP), (dict(num_reqs=2 ** 16, vocab=2 ** 19), UNSUP),
 ])
 def test_probs_refusals(kw, status):
     assert call_probs(probs(**kw)) == status
