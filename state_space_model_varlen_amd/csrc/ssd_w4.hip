@@ -204,8 +204,13 @@ __global__ __launch_bounds__(256) void linear_few_kernel(LinearDims d, LinearArg
 // rows lie in the order in which the fragments take them, which is such that a
 // lane's results of its RT fragments are 4 RT neighbouring outputs.
 //
-// Scales take a word each: with WORDS the 4 bytes of a stage in one (their
-// arrays' rows are whole words then), else one byte.
+// Scales take a word each: of kWords the 4 bytes of a stage in one (their arrays' rows are whole words
+// then), of kBytes one byte. kQuads (rows are whole 16 bytes) loads them for four stages at once, to
+// one of two places of their own: a row's scales are in a line of their own, which takes its turn
+// whatever is used of it. For 128 x 256, which is bound by these turns: 384 tokens, 4096 to 18560
+// 35.2 -> 33.3 us; the larger tiles have fewer of them and lose by reading the bytes apart (192 x 256,
+// 4096 tokens, 5120 to 2560: 54.2 -> 56.8).
+enum Scales { kBytes, kWords, kQuads };
 typedef __attribute__((address_space(3))) void lds_void;
 
 // Loads of 16, 4 or 1 bytes a lane straight to LDS, the lanes' one behind the other from `to` on (a
@@ -240,6 +245,20 @@ template <int N> __device__ __forceinline__ void wait_and_meet() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// The same where a load came before the newest `N` and is not waited for either if `more` is 0, and
+// such a load. (The compiler does not see the branches: with its own it lost the products' registers.)
+template <int N> __device__ __forceinline__ void wait_and_meet(int more) {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_cmp_eq_u32 %2, 0\n\ts_cbranch_scc1 1f\n\ts_waitcnt vmcnt(%0)\n1:\n\t"
+                 "s_waitcnt vmcnt(%1) lgkmcnt(0)\n\ts_barrier" ::"n"(N), "n"(N + 1), "s"(more) : "memory", "scc");
+    __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void to_lds16_if0(int more, i32x4 r, uint32_t to, uint32_t off, uint32_t at) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_cmp_eq_u32 %4, 0\n\ts_cbranch_scc0 1f\n\t"
+                 "buffer_load_dwordx4 %1, %2, %3 offen lds\n1:" ::"s"(to), "v"(off), "s"(r), "s"(at), "s"(more)
+                 : "memory", "scc");
+}
+
 // Buffer I of a block (objects of their own: the compiler then sees that a read of one does not
 // depend on loads on their way to another).
 template <typename B, int I> __device__ __forceinline__ B &buffer() {
@@ -253,7 +272,7 @@ template <int N, int I = 0, typename F> __device__ __forceinline__ void each(F f
     }
 }
 
-template <int MODE, int WT, int WN, int WK, int TT, int RT, int NSUB, int NBUF, bool WORDS, int PERCU, typename TO>
+template <int MODE, int WT, int WN, int WK, int TT, int RT, int NSUB, int NBUF, Scales SCALES, int PERCU, typename TO>
 __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) void linear_tile_kernel(LinearDims d, LinearArgs a,
                                                                                            int ttiles, int ntiles)
 {
@@ -262,26 +281,39 @@ __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) 
     constexpr int CW = KS / 32;                                                 // chunks of a weight row a stage
     constexpr int LX = (TOK * 8 + THREADS - 1) / THREADS, LW = (ROWS * CW + THREADS - 1) / THREADS;     // loads of a thread
     // words of scales: the tokens' and, from a whole wave's on, the weights'
+    constexpr bool WORDS = SCALES != kBytes, QUADS = SCALES == kQuads;
     constexpr int SX = MODE == kSixteen ? 0 : WORDS ? TOK : TOK * BS, SO = (SX + 63) / 64 * 64;
     constexpr int SW = WORDS && MODE != kSixteen ? ROWS : ROWS * BS;
     constexpr int LS = (SO + SW + THREADS - 1) / THREADS;
-    constexpr int LOADS = LX + LW + LS;
+    constexpr int LOADS = LX + LW + (QUADS ? 0 : LS);
+    static_assert(!QUADS || (MODE != kSixteen && NSUB == 1 && NBUF == 3 && LS == 1), "one load of scales");
     static_assert(RT == 1 || RT == 2 || RT == 4 || RT == 8, "whole stores");
     static_assert(LX == 1 || TOK * 8 % THREADS == 0, "loads that are all of the tile's tokens");
     static_assert(NSUB % WK == 0 && LOADS * NSUB * (NBUF - 2) < 64, "waits that can be counted");
     // chunks and words of a step, rounded up to a wave's load; every wave makes the same number of
     // loads, those that have nothing to bring into `spare`
     constexpr int NX = (TOK * 8 + 63) / 64 * 64, NW = (ROWS * CW + 63) / 64 * 64, NS = (SO + SW + 63) / 64 * 64;
-    struct Step {
+    struct Rows {
         char x[NX * 16], w[NW * 16];
+    };
+    struct RowsAndScales : Rows {
         uint32_t s[NS];
     };
+    struct Fours {
+        uint32_t s[2][NS][4];
+    };
+    using Step = std::conditional_t<QUADS, Rows, RowsAndScales>;
     struct Buffer {
         Step step[NSUB];
     };
     const int tid = threadIdx.x, lane = tid & 63, wave = scalar(tid >> 6), n16 = lane & 15, g = lane >> 4;
-    __shared__ __align__(16) char spare[1024];
-    const uint32_t nowhere = lds_address(spare);
+    constexpr bool EXACT = LX * THREADS == NX && LW * THREADS == NW && LS * THREADS == NS;
+    uint32_t nowhere = 0;
+    if constexpr (!EXACT) {
+        __shared__ __align__(16) char spare[1024];
+        nowhere = lds_address(spare);
+    }
+    auto &fours = buffer<std::conditional_t<QUADS, Fours, uint32_t>, NBUF>();        // (nothing without QUADS)
     const int wt = wave / WN % WT, wn = wave % WN, wk = wave / (WN * WT);
 
     // tiles in groups of token tiles, so that the blocks of one L2 share rows and weights
@@ -334,7 +366,7 @@ __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) 
     // load q of step s on its way; what lies past a row's or the tile's end comes as zeros
     auto load_one = [&](auto Q, int s, const Step &b) __attribute__((always_inline)) {
         constexpr int q = decltype(Q)::value;
-        const uint32_t bx = lds_address(b.x), bw = bx + sizeof(b.x), bs = bw + sizeof(b.w);
+        const uint32_t bx = lds_address(b.x), bw = bx + sizeof(b.x);
         if constexpr (q < LX) {
             const uint32_t xo = xrow + (chunk + 128u * s < (uint32_t)d.K * EX ? 0u : kNothing);
             const int c = q * THREADS + wave * 64;
@@ -348,15 +380,24 @@ __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) 
             const int e = i * THREADS + wave * 64;
             const uint32_t so = srow[i] + (BS * s + sblk[i] < blocks ? 0u : kNothing);
             const i32x4 r = e < SO ? rxs.r : rs.r;                               // (the same in a wave)
-            const uint32_t to = e < NS ? bs + 4 * e : nowhere;
+            const uint32_t to = e < NS ? bw + (uint32_t)sizeof(b.w) + 4 * e : nowhere;
             if constexpr (WORDS && MODE != kSixteen) to_lds4(r, to, so, BS * s);
             else to_lds1(r, to, so, BS * s);
+        }
+    };
+    // the scales of stages s .. s + 3, where s is a multiple of 4
+    auto load_four = [&](int s) __attribute__((always_inline)) {
+        if constexpr (QUADS) {
+            const int e = wave * 64;
+            to_lds16_if0(s & 3, e < SO ? rxs.r : rs.r, e < NS ? lds_address(fours.s[(s >> 2) & 1]) + 16 * e : nowhere,
+                         srow[0] + (BS * s < blocks ? 0u : kNothing), (uint32_t)(BS * s));
         }
     };
     // a share of a stage's loads: those of turn t of `turns`
     auto request_share = [&](auto T_, auto N_, int s, const Buffer &b) __attribute__((always_inline)) {
         constexpr int t = decltype(T_)::value, turns = decltype(N_)::value, all = LOADS * NSUB;
         constexpr int from = all * t / turns, to = all * (t + 1) / turns;
+        if constexpr (t == 0) load_four(s);
         each<to - from>([&](auto I) __attribute__((always_inline)) {
             constexpr int l = from + decltype(I)::value;
             load_one(std::integral_constant<int, l % LOADS>{}, s * NSUB + l / LOADS, b.step[l / LOADS]);
@@ -365,13 +406,15 @@ __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) 
     auto request = [&](int s, const Buffer &b) __attribute__((always_inline)) {
         request_share(std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{}, s, b);
     };
-    // scale of block g of token or row `at`
-    auto scale_of = [&](const uint32_t *p, int at, int blk) __attribute__((always_inline)) -> uint32_t {
-        if constexpr (WORDS && MODE != kSixteen) return reinterpret_cast<const uint8_t *>(p)[4 * at + blk];
-        else return p[at * BS + blk];
+    // scale of block `blk` of token (from 0) or weight row (from SO) `at` in stage s
+    auto scale_of = [&](const Step &b, int s, int from, int at, int blk) __attribute__((always_inline)) -> uint32_t {
+        if constexpr (QUADS)
+            return reinterpret_cast<const uint8_t *>(fours.s[(s >> 2) & 1][from + at])[4 * (s & 3) + blk];
+        else if constexpr (WORDS && MODE != kSixteen) return reinterpret_cast<const uint8_t *>(b.s + from)[4 * at + blk];
+        else return b.s[from + at * BS + blk];
     };
     // (between(turn, turns) is called as the products go)
-    auto multiply_step = [&](const Step &b, auto between) __attribute__((always_inline)) {
+    auto multiply_step = [&](const Step &b, int s, auto between) __attribute__((always_inline)) {
         const char *const x = b.x + (wt * 16 * TT + n16) * 128;
         const char *const w = b.w + (wn * 16 * RT + n16) * (CW * 16);
         const int turn = n16 >> 1;
@@ -380,7 +423,7 @@ __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) 
         for (int r = 0; r < RT; ++r)
 #pragma unroll
             for (int i = 0; i < (MODE == kSixteen ? 2 : 1); ++i)
-                ws[r][i] = scale_of(b.s + SO, wn * 16 * RT + 16 * r + n16, MODE == kSixteen ? i : g);
+                ws[r][i] = scale_of(b, s, SO, wn * 16 * RT + 16 * r + n16, MODE == kSixteen ? i : g);
         if constexpr (MODE == kEight) {
             i32x4 wf[RT];
 #pragma unroll
@@ -392,7 +435,7 @@ __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) 
             auto take = [&](int t) __attribute__((always_inline)) {
                 f[t % RING][0] = *reinterpret_cast<const i32x4 *>(x + t * 2048 + 16 * (g ^ turn));
                 f[t % RING][1] = *reinterpret_cast<const i32x4 *>(x + t * 2048 + 16 * ((4 + g) ^ turn));
-                xs[t % RING] = (int)scale_of(b.s, wt * 16 * TT + 16 * t + n16, g);
+                xs[t % RING] = (int)scale_of(b, s, 0, wt * 16 * TT + 16 * t + n16, g);
             };
 #pragma unroll
             for (int t = 0; t < AHEAD; ++t) take(t);
@@ -448,7 +491,7 @@ __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) 
                 for (int r = 0; r < RT; ++r) wv[r] = widen_codes((uint32_t)wf[r][i], ws[r][0]);
 #pragma unroll
                 for (int t = 0; t < TT; ++t) {
-                    const uint32_t xs = scale_of(b.s, wt * 16 * TT + 16 * t + n16, g);
+                    const uint32_t xs = scale_of(b, s, 0, wt * 16 * TT + 16 * t + n16, g);
                     const bf16x8 v = widen_8bit(*reinterpret_cast<const u32x2 *>(
                                                     x + t * 2048 + 16 * ((2 * g + (i >> 1)) ^ turn) + 8 * (i & 1)),
                                                 __uint_as_float(xs << 23));
@@ -469,18 +512,18 @@ __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) 
     auto multiply = [&](const Buffer &b, int next, const Buffer &into) __attribute__((always_inline)) {
         if constexpr (NBUF == 2) {
             request(next, into);
-            each<NSUB / WK>([&](auto U) __attribute__((always_inline)) { multiply_step(b.step[decltype(U)::value * WK + wk], [](auto, auto) __attribute__((always_inline)) {}); });
+            each<NSUB / WK>([&](auto U) __attribute__((always_inline)) { multiply_step(b.step[decltype(U)::value * WK + wk], next - NBUF + 1, [](auto, auto) __attribute__((always_inline)) {}); });
         } else
             each<NSUB / WK>([&](auto U) __attribute__((always_inline)) {
                 constexpr int u = decltype(U)::value;
-                multiply_step(b.step[u * WK + wk], [&](auto T_, auto N_) __attribute__((always_inline)) {
+                multiply_step(b.step[u * WK + wk], next - NBUF + 1, [&](auto T_, auto N_) __attribute__((always_inline)) {
                     request_share(std::integral_constant<int, u * decltype(N_)::value + decltype(T_)::value>{},
                                   std::integral_constant<int, decltype(N_)::value * (NSUB / WK)>{}, next, into);
                 });
             });
     };
-    auto multiply_last = [&](const Buffer &b) __attribute__((always_inline)) {
-        each<NSUB / WK>([&](auto U) __attribute__((always_inline)) { multiply_step(b.step[decltype(U)::value * WK + wk], [](auto, auto) __attribute__((always_inline)) {}); });
+    auto multiply_last = [&](const Buffer &b, int s) __attribute__((always_inline)) {
+        each<NSUB / WK>([&](auto U) __attribute__((always_inline)) { multiply_step(b.step[decltype(U)::value * WK + wk], s, [](auto, auto) __attribute__((always_inline)) {}); });
     };
 
     // the stage in buffer I of a round of NBUF from `s` on
@@ -488,10 +531,12 @@ __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) 
     auto stage = [&](auto I) __attribute__((always_inline)) {
         constexpr int i = decltype(I)::value;
         multiply(buffer<Buffer, i>(), s + i + NBUF - 1, buffer<Buffer, (i + NBUF - 1) % NBUF>());
-        wait_and_meet<(NBUF - 2) * NSUB * LOADS>();
+        // (all but the loads that have just been asked for)
+        if constexpr (QUADS) wait_and_meet<LOADS>((s + i + NBUF - 1) & 3);
+        else wait_and_meet<(NBUF - 2) * NSUB * LOADS>();
     };
     auto last = [&](auto I) __attribute__((always_inline)) {
-        if (s + decltype(I)::value < stages) multiply_last(buffer<Buffer, decltype(I)::value>());
+        if (s + decltype(I)::value < stages) multiply_last(buffer<Buffer, decltype(I)::value>(), s + decltype(I)::value);
     };
     each<NBUF - 1>([&](auto I) __attribute__((always_inline)) { request(decltype(I)::value, buffer<Buffer, decltype(I)::value>()); });
     wait_and_meet<(NBUF - 2) * NSUB * LOADS>();
@@ -577,7 +622,7 @@ struct Tile {
 static constexpr Tile kTiles[] = {
     {16, 16, 256, 2, 4, 224, 103},      {16, 32, 128, 2, 1, 369, 191},     {32, 32, 256, 1, 4, 385, 246},
     {64, 64, 256, 2, 2, 898, 576},      {128, 128, 512, 2, 1, 1793, 1014}, {256, 256, 512, 1, 1, 2507, 1341},
-    {192, 256, 512, 1, 1, 2250, 1200},  {128, 256, 512, 1, 1, 1760, 0}};
+    {192, 256, 512, 1, 1, 2250, 1200},  {128, 256, 512, 1, 1, 1850, 0}};
 static const char *const kTileNames[] = {"16x16",   "16x32",   "32x32",   "64x64",
                                          "128x128", "256x256", "192x256", "128x256"};
 
@@ -615,10 +660,10 @@ static bool linear_few(const LinearDims &d) {
 }
 const char *linear_kernel_name(const LinearDims &d) { return linear_few(d) ? "few" : kTileNames[linear_tile_of(d)]; }
 
-template <int MODE, int WT, int WN, int WK, int TT, int RT, int NSUB, int NBUF, bool WORDS, int PERCU, typename TO>
+template <int MODE, int WT, int WN, int WK, int TT, int RT, int NSUB, int NBUF, Scales SCALES, int PERCU, typename TO>
 static void linear_tile(const LinearDims &d, const LinearArgs &a, hipStream_t st) {
     const int tt = (d.T + 16 * TT * WT - 1) / (16 * TT * WT), nt = (d.N + 16 * RT * WN - 1) / (16 * RT * WN);
-    hipLaunchKernelGGL((linear_tile_kernel<MODE, WT, WN, WK, TT, RT, NSUB, NBUF, WORDS, PERCU, TO>),
+    hipLaunchKernelGGL((linear_tile_kernel<MODE, WT, WN, WK, TT, RT, NSUB, NBUF, SCALES, PERCU, TO>),
                        dim3((unsigned)(tt * nt)), dim3(64 * WT * WN * WK), 0, st, d, a, tt, nt);
 }
 template <int MODE, bool WORDS, typename TO>
@@ -628,7 +673,7 @@ static void linear_few_t(const LinearDims &d, const LinearArgs &a, hipStream_t s
     hipLaunchKernelGGL((linear_few_kernel<MODE, WORDS, TO>), dim3((unsigned)((d.N + 15) / 16)), dim3(256),
                        d.T * pitch + scales, st, d, a, pitch);
 }
-template <int MODE, bool WORDS, typename TO>
+template <int MODE, Scales W, typename TO>
 static void linear_t(const LinearDims &d, const LinearArgs &a, hipStream_t st) {
     if (linear_few(d)) {
         if (d.K % 256 == 0 && (uintptr_t)a.w_scale % 8 == 0) linear_few_t<MODE, true, TO>(d, a, st);
@@ -636,32 +681,34 @@ static void linear_t(const LinearDims &d, const LinearArgs &a, hipStream_t st) {
         return;
     }
     // (blocks a CU that the buffers leave room for)
-    constexpr int two = WORDS || MODE == kSixteen ? 2 : 1;
+    constexpr int two = W == kWords || MODE == kSixteen ? 2 : 1;
     switch (linear_tile_of(d)) {
-    case 0: return linear_tile<MODE, 1, 1, 4, 1, 1, 4, 3, WORDS, 2, TO>(d, a, st);
-    case 1: return linear_tile<MODE, 1, 2, 1, 1, 1, 1, 8, WORDS, 2, TO>(d, a, st);
-    case 2: return linear_tile<MODE, 1, 1, 4, 2, 2, 4, 3, WORDS, 1, TO>(d, a, st);
-    case 3: return linear_tile<MODE, 1, 4, 1, 4, 1, 2, 3, WORDS, two, TO>(d, a, st);
-    case 4: return linear_tile<MODE, 2, 4, 1, 4, 2, 1, 3, WORDS, two, TO>(d, a, st);
+    case 0: return linear_tile<MODE, 1, 1, 4, 1, 1, 4, 3, W, 2, TO>(d, a, st);
+    case 1: return linear_tile<MODE, 1, 2, 1, 1, 1, 1, 8, W, 2, TO>(d, a, st);
+    case 2: return linear_tile<MODE, 1, 1, 4, 2, 2, 4, 3, W, 1, TO>(d, a, st);
+    case 3: return linear_tile<MODE, 1, 4, 1, 4, 1, 2, 3, W, two, TO>(d, a, st);
+    case 4: return linear_tile<MODE, 2, 4, 1, 4, 2, 1, 3, W, two, TO>(d, a, st);
     case 5:
         // (scales of a byte a word leave room for two buffers)
-        return linear_tile<MODE, 2, 4, 1, 8, 4, 1, WORDS || MODE == kSixteen ? 3 : 2, WORDS, 1, TO>(d, a, st);
-    case 6: return linear_tile<MODE, 2, 4, 1, 6, 4, 1, 3, WORDS, 1, TO>(d, a, st);
+        return linear_tile<MODE, 2, 4, 1, 8, 4, 1, W == kWords || MODE == kSixteen ? 3 : 2, W, 1, TO>(d, a, st);
+    case 6: return linear_tile<MODE, 2, 4, 1, 6, 4, 1, 3, W, 1, TO>(d, a, st);
     default:
-        if constexpr (MODE != kSixteen) linear_tile<MODE, 2, 4, 1, 4, 4, 1, 3, WORDS, 1, TO>(d, a, st);
+        if constexpr (MODE == kEight && W == kWords)
+            if (d.K % 512 == 0 && ((uintptr_t)a.x_scale | (uintptr_t)a.w_scale) % 16 == 0)
+                return linear_tile<MODE, 2, 4, 1, 4, 4, 1, 3, kQuads, 1, TO>(d, a, st);
+        if constexpr (MODE != kSixteen) linear_tile<MODE, 2, 4, 1, 4, 4, 1, 3, W, 1, TO>(d, a, st);
     }
 }
-
 void launch_linear(const LinearDims &d, const LinearArgs &a, void *, void *stream)
 {
     if (d.T <= 0) return;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     const LinearMode m = linear_mode(d);
     const bool words = d.K % 128 == 0 && ((uintptr_t)a.x_scale | (uintptr_t)a.w_scale) % 4 == 0;
-    if (m == kEight) words ? linear_t<kEight, true, bf16>(d, a, st) : linear_t<kEight, false, bf16>(d, a, st);
-    else if (m == kWidened) words ? linear_t<kWidened, true, float>(d, a, st) : linear_t<kWidened, false, float>(d, a, st);
-    else if (d.out_bf16) linear_t<kSixteen, false, bf16>(d, a, st);
-    else linear_t<kSixteen, false, float>(d, a, st);
+    if (m == kEight) words ? linear_t<kEight, kWords, bf16>(d, a, st) : linear_t<kEight, kBytes, bf16>(d, a, st);
+    else if (m == kWidened) words ? linear_t<kWidened, kWords, float>(d, a, st) : linear_t<kWidened, kBytes, float>(d, a, st);
+    else if (d.out_bf16) linear_t<kSixteen, kBytes, bf16>(d, a, st);
+    else linear_t<kSixteen, kBytes, float>(d, a, st);
 }
 
 // ---------------------------------------------------------------------------

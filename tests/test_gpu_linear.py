@@ -84,6 +84,20 @@ def test_every_tile(tile, xt, to, odd):
     T, K, N = TILES[tile]
     if odd:
         T, K, N = max(1, T - 3), K - 96 if K > 512 else K + 32, N - 7
+    took = exact_in_any_order(T, K, N, xt, to)
+    if not odd and (xt == E4 or tile != "128x256"):
+        assert took == tile
+
+
+@pytest.mark.parametrize("K", [512, 1024, 1536, 2560, 4096])
+@pytest.mark.parametrize("shift", [0, 4])
+def test_scales_of_four_stages(K, shift):
+    """The tile that loads scales for four stages of K at once, where their arrays allow it, and not."""
+    assert exact_in_any_order(301, K, 18553, E4, BF, shift) == "128x256"
+
+
+def exact_in_any_order(T, K, N, xt, to, shift=0):
+    """Runs whole numbers and compares bit for bit; scales begin `shift` bytes behind 16. Returns the kernel."""
     p = ssd.make_linear_problem(T, K, N, xt, to)
     took = ssd.linear_w4_kernel(p)
     g = torch.Generator(DEV).manual_seed(K)
@@ -91,6 +105,8 @@ def test_every_tile(tile, xt, to, odd):
     ws = torch.randint(126, 129, (N, K // 32), generator=g, dtype=U8, device=DEV)
     x = torch.randint(-4, 5, (T, K), generator=g, device=DEV).float()
     xs = torch.randint(126, 129, (T, K // 32), generator=g, dtype=U8, device=DEV) if xt == E4 else None
+    if shift:
+        ws, xs = (torch.cat([t.new_zeros(shift), t.flatten()])[shift:].view(t.shape) for t in (ws, xs))
     out = torch.empty(T, N, dtype=to, device=DEV)
     ssd.linear_w4(p, x.to(xt), codes, ws, out, xs, None, ssd.alloc_linear_workspace(p, DEV))
     # the same sums in float32, exact in any order: whole multiples of 2^-4 below 2^20
@@ -102,8 +118,7 @@ def test_every_tile(tile, xt, to, odd):
     want = torch.cat([(x[a:a + 512].double() @ w.double().t()) for a in range(0, T, 512)])
     assert float((x.abs().amax(0) * w.abs().amax(0)).sum()) < 2.0 ** 20
     assert torch.equal(out, want.to(to)), took
-    if not odd and (xt == E4 or tile != "128x256"):
-        assert took == tile
+    return took
 
 
 @pytest.mark.parametrize("xt", [BF, E4])
