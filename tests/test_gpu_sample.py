@@ -72,6 +72,28 @@ def test_masked_and_non_finite(V):
     assert bool((out[0, 2] == 0).all()) and float(out[0, 3, V - 2]) == 1 and bool((out[0, 1, :V // 2] == 0).all())
 
 
+@pytest.mark.parametrize("V", [50, 3000, 9000, 40000])
+def test_ends_of_temperature(V):
+    """Temperatures so high that all but masked logits are equal, and so low that the largest alone counts."""
+    x = torch.randn(6, 2, V, generator=torch.Generator().manual_seed(V))
+    x[:, :, ::3] = -INF
+    x[:, 1, V - 1] = 9.0
+    temp = [1e30, 1e37, 3e38, INF, 1e-30, 1e-40]
+    for ti in (BF, F32):
+        check_probs(probs(x.to(ti), temp), x.to(ti), temp)
+
+
+@pytest.mark.parametrize("ti", [BF, F32])
+@pytest.mark.parametrize("V", [511, 1025, 2047, 2049, 4095, 4097, 8193, 16383, 16385])
+def test_probs_of_every_form(ti, V):
+    g = torch.Generator().manual_seed(V)
+    x = (torch.randn(2, 3, V, generator=g) * 3).to(ti)
+    x[1, 1, : V // 3] = -INF
+    x[0, 2, V - 1] = float("nan")
+    for temp in ([0.6, 1.0], [0.0, 2.0]):
+        check_probs(probs(x, temp), x, temp)
+
+
 @pytest.mark.parametrize("ti", [BF, F32])
 def test_probs_strides(ti):
     R, T, V = 2, 2, 301
