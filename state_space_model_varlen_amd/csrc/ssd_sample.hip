@@ -277,14 +277,34 @@ void launch_probs(const ProbsDims &d, const void *logits, const float *temperatu
 //
 // Rows of up to 16 K entries are one block's work. Longer ones take two launches: the
 // weights of every 2048 entries are summed (a wave each), then one block a request
-// finds the 2048 that the draw falls into and goes through their entries. Bound by the rows' bytes, for few requests by the chain draft ->
-// its probabilities -> row.
+// finds the 2048 that the draw falls into and goes through their entries. Bound by the
+// rows' bytes (128 requests of 131072: 29 us, 4.6 TB/s), for few requests by two launches and
+// the chain draft -> its probabilities -> row -> sums -> entries (one: 13 us).
 
 constexpr int kGrain = 2048, kPickThreads = 256, kPerThread = kGrain / kPickThreads;
 
 struct Decision {
     int count, accepted;     // drafts of the request, and how many of them stand
 };
+
+// Moves of both halves of a double between lanes (lanes without a source, or outside ROWS, get 0).
+template <int CTRL, int ROWS = 15> __device__ __forceinline__ double dpp64(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 15, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 15, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Inclusive sums over the lanes of a wave, in their order. (Moves by the registers' own paths, not
+// through LDS: one request of 6 tokens of 50257 12.8 -> 12.0 us.)
+__device__ __forceinline__ double wave_scan(double v) {
+    v += dpp64<0x111>(v);              // row_shr 1, 2, 4, 8: within 16 lanes
+    v += dpp64<0x112>(v);
+    v += dpp64<0x114>(v);
+    v += dpp64<0x118>(v);
+    v += dpp64<0x142, 0xa>(v);         // lane 15's to the second and lane 47's to the fourth 16
+    v += dpp64<0x143, 0xc>(v);         // lane 31's to the upper 32
+    return v;
+}
 
 // Every wave of the block comes to the same answer: lane i tests draft i.
 __device__ __forceinline__ Decision decide(const VerifyDims &d, const VerifyArgs &a, int r) {
@@ -363,12 +383,9 @@ __global__ __launch_bounds__(256) void verify_sums_kernel(VerifyDims d, VerifyAr
             sw += w;
             sp += pl;
         }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        sw += __shfl_xor(sw, off, kWave);
-        sp += __shfl_xor(sp, off, kWave);
-    }
-    if (lane == 0) {
+    sw = wave_scan(sw);
+    sp = wave_scan(sp);
+    if (lane == 63) {
         sums[((int64_t)r * grains + grain) * 2] = sw;
         sums[((int64_t)r * grains + grain) * 2 + 1] = sp;
     }
@@ -380,24 +397,29 @@ __global__ __launch_bounds__(256) void verify_sums_kernel(VerifyDims d, VerifyAr
     }
 }
 
-// Inclusive sums over the block's threads, in their order, and the sum of all.
-__device__ __forceinline__ double block_scan(double v, double *part, double &all) {
-    const int lane = threadIdx.x & 63, wave = (int)threadIdx.x >> 6, waves = (int)blockDim.x >> 6;
+// Inclusive sums over the block's threads, in their order, of N values each, and the sums of all.
+template <int N> struct BlockScan {
+    double part[N][16];
+    __device__ __forceinline__ void run(double *v, double *all) {
+        const int lane = threadIdx.x & 63, wave = (int)threadIdx.x >> 6, waves = (int)blockDim.x >> 6;
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const double o = __shfl_up(v, off, kWave);
-        if (lane >= off) v += o;
+        for (int k = 0; k < N; ++k) {
+            v[k] = wave_scan(v[k]);
+            if (lane == 63) part[k][wave] = v[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            double before = 0.0;
+            all[k] = 0.0;
+            for (int i = 0; i < waves; ++i) {
+                if (i < wave) before += part[k][i];
+                all[k] += part[k][i];
+            }
+            v[k] += before;
+        }
     }
-    if (lane == 63) part[wave] = v;
-    __syncthreads();
-    double before = 0.0;
-    all = 0.0;
-    for (int i = 0; i < waves; ++i) {
-        if (i < wave) before += part[i];
-        all += part[i];
-    }
-    return before + v;
-}
+};
 
 // The first place that passes `want` and the last of positive weight, over the block.
 struct Pick {
@@ -440,34 +462,37 @@ __device__ __forceinline__ void weigh_run(const Row &row, int v0, int V, double 
 // Rows of up to 16 K entries: all in one block a request, 16 entries a thread.
 constexpr int kWholePer = 16, kWholeMost = 1024 * kWholePer;
 __global__ __launch_bounds__(1024) void verify_whole_kernel(VerifyDims d, VerifyArgs a) {
-    __shared__ double part[2][16];
+    __shared__ BlockScan<2> scan;
     __shared__ Pick pick;
     const int r = blockIdx.x, tid = threadIdx.x, v0 = tid * kWholePer;
     const double uniform = (double)a.uniform[(int64_t)r * d.T + d.T - 1];
     const Decision k = decide(d, a, r);
     const Row row(d, a, r, k);
     if (tid == 0) pick.clear();
-    double w[kWholePer], plain[kWholePer], sw = 0.0, sp = 0.0, tw, tp;
+    double w[kWholePer], plain[kWholePer], sw = 0.0, sp = 0.0, t[2];
     weigh_run<kWholePer>(row, v0, d.V, w, plain);
 #pragma unroll
     for (int j = 0; j < kWholePer; ++j) {
         sw += w[j];
         sp += plain[j];
     }
-    const double iw = block_scan(sw, part[0], tw), ip = block_scan(sp, part[1], tp);
-    if (tw > 0.0) pick_among<kWholePer>(w, v0, iw - sw, tw * uniform, &pick);
-    else pick_among<kWholePer>(plain, v0, ip - sp, tp * uniform, &pick);
+    double i[2] = {sw, sp};
+    scan.run(i, t);
+    if (t[0] > 0.0) pick_among<kWholePer>(w, v0, i[0] - sw, t[0] * uniform, &pick);
+    else pick_among<kWholePer>(plain, v0, i[1] - sp, t[1] * uniform, &pick);
     __syncthreads();
     if (tid == 0) a.accepted[r] = k.accepted;
-    for (int i = tid; i < d.T; i += (int)blockDim.x)
-        a.out[(int64_t)r * d.T + i] = i < k.accepted ? a.tokens[(int64_t)r * (d.T - 1) + i]
-                                      : i == k.accepted ? pick.place() : -1;
+    for (int j = tid; j < d.T; j += (int)blockDim.x)
+        a.out[(int64_t)r * d.T + j] = j < k.accepted ? a.tokens[(int64_t)r * (d.T - 1) + j]
+                                      : j == k.accepted ? pick.place() : -1;
 }
 
 __global__ __launch_bounds__(kPickThreads) void verify_pick_kernel(VerifyDims d, VerifyArgs a, int grains,
                                                                    const double *__restrict__ sums)
 {
-    __shared__ double part[3][kPickThreads / 64], start;
+    __shared__ BlockScan<2> scan;
+    __shared__ BlockScan<1> scan1;
+    __shared__ double start;
     __shared__ Pick pick[2];
     const int r = blockIdx.x, tid = threadIdx.x;
     if (tid < 2) pick[tid].clear();
@@ -481,16 +506,17 @@ __global__ __launch_bounds__(kPickThreads) void verify_pick_kernel(VerifyDims d,
     // a thread's grains follow one another
     const int per = (grains + kPickThreads - 1) / kPickThreads, g0 = tid * per;
     const int g1 = g0 + per < grains ? g0 + per : grains;
-    double mw = 0.0, mp = 0.0, tw, tp;
+    double mw = 0.0, mp = 0.0, t[2];
     for (int i = g0; i < g1; ++i) {
         mw += s[2 * i];
         mp += s[2 * i + 1];
     }
-    const double iw = block_scan(mw, part[0], tw), ip = block_scan(mp, part[1], tp);
-    const int which = tw > 0.0 ? 0 : 1;
-    const double want = (which ? tp : tw) * uniform;
+    double in[2] = {mw, mp};
+    scan.run(in, t);
+    const int which = t[0] > 0.0 ? 0 : 1;
+    const double want = (which ? t[1] : t[0]) * uniform, before = which ? in[1] - mp : in[0] - mw;
     // the first grain that passes `want`, or the last of positive weight
-    double c = which ? ip - mp : iw - mw;
+    double c = before;
     for (int i = g0; i < g1; ++i) {
         const double w = s[2 * i + which];
         pick_among<1>(&w, i, c, want, &pick[0]);
@@ -503,7 +529,7 @@ __global__ __launch_bounds__(kPickThreads) void verify_pick_kernel(VerifyDims d,
         return;
     }
     if (grain >= g0 && grain < g1) {
-        double b = which ? ip - mp : iw - mw;
+        double b = before;
         for (int i = g0; i < grain; ++i) b += s[2 * i + which];
         start = b;
     }
@@ -515,7 +541,8 @@ __global__ __launch_bounds__(kPickThreads) void verify_pick_kernel(VerifyDims d,
         w[j] = which ? plain[j] : w[j];
         mine += w[j];
     }
-    const double incl = block_scan(mine, part[2], all);          // (start is written by now)
+    double incl = mine;
+    scan1.run(&incl, &all);                                      // (start is written by now)
     pick_among<kPerThread>(w, v0, start + (incl - mine), want, &pick[1]);
     __syncthreads();
     if (tid == 0) a.out[(int64_t)r * d.T + k.accepted] = pick[1].place();
