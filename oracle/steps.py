@@ -141,7 +141,8 @@ def probs(logits, temperature=None):
                 out[r, i] = e / e.sum()
             # x - m is rounded once, |d| 2^-24 in the exponent; the exponential, its correction, the
             # reciprocal and the product: 8 more; the sum goes by its terms and its own additions
-            # (at least 64 threads share a row, then 64 over the block and the parts)
+            # (at least 256 threads share a row, a few dozen steps over the block and the parts, and the
+            # terms' exponents are rounded: |d| 2^-24, over a row's probabilities at most ln V 2^-24)
             rel = (np.abs(d) + 8) * EPS
             tol[r, i] = out[r, i] * (rel + (out[r, i] * rel).sum() + (V / 64 + 64) * EPS) + 1e-37
     return out, tol

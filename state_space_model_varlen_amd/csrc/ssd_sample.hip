@@ -11,11 +11,12 @@ namespace ssd {
 // Probabilities.
 
 // A row (short ones) or a part of a row by one block, its logits kept in
-// registers from their only load. A row that one block cannot hold, or that
-// would leave the chip idle, is cut into parts: the first launch leaves each
-// part's largest logit and sum, the second joins them and writes. Bound by the
-// bytes of logits (read twice, the second time mostly from the last-level cache)
-// and probabilities.
+// registers from their only load. A row that one block cannot hold is cut into
+// parts: the first launch leaves each part's largest logit and sum, the second
+// joins them and writes. Bound by the bytes of logits (in parts read twice, the
+// second time from the last-level cache as far as it holds them) and
+// probabilities: 4096 rows of 32000 bfloat16 158 us, 5.0 TB/s; 384 of 131072 74 us,
+// 5.5 TB/s of what is moved, 4.1 of what has to be.
 struct Peak {
     float m;    // the largest logit (-infinity: none)
     float s;    // sum of exp((x - m) / T)
@@ -41,6 +42,12 @@ struct InvTemp {
     }
     // (else the largest float is nearer than `far`, and masked logits are looked for one by one)
     __device__ __forceinline__ bool usual() const { return hi > 1.0e-36f; }
+    // exp(d / T) for a sum: off by the exponent's rounding, d / T 2^-24 of itself, which over a row's
+    // probabilities comes to at most the logarithm of their number times 2^-24 (their entropy's bound)
+    __device__ __forceinline__ float summand(float d) const {
+        d = fmaxf(d, far);
+        return __builtin_amdgcn_exp2f(fmaf(d, hi, d * lo));
+    }
     // exp(d / T) = e (1 + rest ln 2); a d that is NaN or -infinity has e = 0
     __device__ __forceinline__ float split(float d, float &rest) const {
         d = fmaxf(d, far);
@@ -73,11 +80,20 @@ template <typename T, int N> struct Logits {
                 for (int e = 0; e < E; ++e) v[j][e] = i + e < end ? x[i + e] : from_f32<T>(-__builtin_inff());
         }
     }
+    // (unpacked by hand: the compiler rounds a maximum of widened bfloat16 back to bfloat16 and widens it again)
+    __device__ __forceinline__ float at(int j, int e) const {
+        if constexpr (sizeof(T) == 4) return v[j][e];
+        else {
+            typedef uint32_t words __attribute__((ext_vector_type(4)));
+            const uint32_t w = __builtin_bit_cast(words, v[j])[e / 2];
+            return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
+        }
+    }
     template <typename F> __device__ __forceinline__ void each(int from, int threads, F f) const {
 #pragma unroll
         for (int j = 0; j < N; ++j)
 #pragma unroll
-            for (int e = 0; e < E; ++e) f(from + (j * threads + (int)threadIdx.x) * E + e, to_f32(v[j][e]), j, e);
+            for (int e = 0; e < E; ++e) f(from + (j * threads + (int)threadIdx.x) * E + e, at(j, e));
     }
 };
 
@@ -101,10 +117,10 @@ __device__ __forceinline__ Peak block_peak(const Logits<T, N> &l, int from, cons
     Peak k{-__builtin_inff(), 0.0f, 0x7fffffff, 0};
     float own = -__builtin_inff();
     if (usual) {
-        l.each(from, 64 * W, [&](int, float v, int, int) { own = __builtin_elementwise_maximum(own, v); });
+        l.each(from, 64 * W, [&](int, float v) { own = __builtin_elementwise_maximum(own, v); });
         k.m = wave_max(own);
     } else {
-        l.each(from, 64 * W, [&](int i, float v, int, int) {
+        l.each(from, 64 * W, [&](int i, float v) {
             // (places rise: an equal one later does not replace)
             k.at = v > k.m ? i : k.at;
             k.m = v > k.m ? v : k.m;
@@ -120,17 +136,11 @@ __device__ __forceinline__ Peak block_peak(const Logits<T, N> &l, int from, cons
     const float top = k.m == -__builtin_inff() ? 0.0f : k.m;
     float s = 0.0f;
     if (usual) {
-        float rests = 0.0f;
-        l.each(from, 64 * W, [&](int, float v, int, int) {
-            float rest;
-            const float e = inv.split(v - top, rest);
-            s += e;
-            rests = fmaf(e, rest, rests);
-        });
+        l.each(from, 64 * W, [&](int, float v) { s += inv.summand(v - top); });
         // (a logit of NaN or +infinity makes the sum NaN)
-        s = fmaf(kLn2, rests, s) + (own == -__builtin_inff() ? 0.0f : own - own);
+        s += own == -__builtin_inff() ? 0.0f : own - own;
     } else
-        l.each(from, 64 * W, [&](int, float v, int, int) { s += v == -__builtin_inff() ? 0.0f : inv(v - top); });
+        l.each(from, 64 * W, [&](int, float v) { s += v == -__builtin_inff() ? 0.0f : inv(v - top); });
     s = group_sum(s, 64);
     if (lane == 0) sums[wave] = s;
     __syncthreads();
@@ -157,13 +167,13 @@ __device__ __forceinline__ void write_probs(const Logits<T, N> &l, int from, int
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 float rest;
-                const float p1 = inv.split(to_f32(l.v[j][e]) - top, rest) * r;
+                const float p1 = inv.split(l.at(j, e) - top, rest) * r;
                 y[e] = fmaf(p1, rest * kLn2, p1);
             }
         else
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const float v = to_f32(l.v[j][e]);
+                const float v = l.at(j, e);
                 y[e] = greedy ? (i + e == k.at ? 1.0f : 0.0f) : v == -__builtin_inff() ? none : inv(v - top) * r;
             }
         if (i + E <= end)
@@ -181,7 +191,7 @@ __device__ __forceinline__ void write_probs(const Logits<T, N> &l, int from, int
 
 // STEP 0: whole rows; 1: the parts' peaks; 2: parts joined and written.
 template <typename T, int N, int W, int STEP>
-__global__ __launch_bounds__(64 * W) void probs_kernel(int V, int per_req, const T *__restrict__ logits, int64_t ls,
+__global__ __launch_bounds__(64 * W, W == 8 ? 4 : 1) void probs_kernel(int V, int per_req, const T *__restrict__ logits, int64_t ls,
                                                        const float *__restrict__ temperature,
                                                        float *__restrict__ probs, int64_t ps, int parts,
                                                        Peak *__restrict__ peaks)
@@ -220,11 +230,12 @@ __global__ __launch_bounds__(64 * W) void probs_kernel(int V, int per_req, const
     write_probs<T, N, W>(l, from, end, k, greedy, inv, probs + row * ps);
 }
 
-// Rows of up to 8 K logits (bfloat16: 16 K) are taken whole, others in parts of 4 K (8 K).
+// Rows of up to 16 K logits (bfloat16: 32 K) are taken whole, others in parts of 4 K (8 K): 512 rows
+// of 32000 bfloat16 26 us whole and 33 in parts, of 50257 52 and 48; 1024 of 34000 79 and 58.
 template <typename T> static constexpr int probs_span() { return 256 * Logits<T, 4>::E * 4; }
 static int probs_parts(const ProbsDims &d) {
     const int span = d.bf16 ? probs_span<bf16>() : probs_span<float>();
-    return d.V <= 2 * span ? 0 : (d.V + span - 1) / span;
+    return d.V <= 4 * span ? 0 : (d.V + span - 1) / span;
 }
 size_t probs_workspace(const ProbsDims &d) { return (size_t)d.R * d.T * probs_parts(d) * sizeof(Peak); }
 
@@ -253,7 +264,8 @@ static void probs_t(const ProbsDims &d, const void *logits, const float *tempera
         if (d.V <= 256 * E) whole(integral_constant<int, 1>{}, integral_constant<int, 4>{});
         else if (d.V <= 512 * E) whole(integral_constant<int, 2>{}, integral_constant<int, 4>{});
         else if (d.V <= 1024 * E) whole(integral_constant<int, 4>{}, integral_constant<int, 4>{});
-        else whole(integral_constant<int, 4>{}, integral_constant<int, 8>{});
+        else if (d.V <= 2048 * E) whole(integral_constant<int, 4>{}, integral_constant<int, 8>{});
+        else whole(integral_constant<int, 8>{}, integral_constant<int, 8>{});
     }
 }
 

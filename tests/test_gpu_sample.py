@@ -84,7 +84,7 @@ def test_ends_of_temperature(V):
 
 
 @pytest.mark.parametrize("ti", [BF, F32])
-@pytest.mark.parametrize("V", [511, 1025, 2047, 2049, 4095, 4097, 8193, 16383, 16385])
+@pytest.mark.parametrize("V", [511, 1025, 2047, 2049, 4095, 4097, 8193, 16383, 16385, 32767, 32769])
 def test_probs_of_every_form(ti, V):
     g = torch.Generator().manual_seed(V)
     x = (torch.randn(2, 3, V, generator=g) * 3).to(ti)
