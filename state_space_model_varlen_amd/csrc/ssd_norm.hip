@@ -3,8 +3,9 @@
 //
 // out = v rsqrt(mean(v^2) + eps) w: a row (or a group of one) is read once,
 // kept in registers as float while its squares are summed over the block, and
-// written once: bound by its bytes, or for few rows by the latency of one load,
-// one sum over the block and one store.
+// written once: bound by its bytes (4096 rows of 2560 with their float32 sum in
+// place 26.7 us, 4.7 TB/s), or for few rows by the latency of one load, one sum
+// over the block and one store (one row 2.1 us, a call 6.9).
 #include <stdint.h>
 
 #include "ssd_layer_device.h"
@@ -191,7 +192,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(NormArgs a) {
 }
 
 // The same for rows that no block can keep: an element a thread and step, read a
-// second time instead.
+// second time instead (64 rows of 40000 66 us, bound by the chain of a block's loads).
 template <typename TX, typename TR, typename TO, int MODE>
 __global__ __launch_bounds__(256) void norm_long_kernel(NormArgs a) {
     __shared__ float part[4];
