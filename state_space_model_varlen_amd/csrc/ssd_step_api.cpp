@@ -54,6 +54,8 @@ int norm_dims(const norm_problem *p, ssd::NormDims *d)
         return SSD_ERR_DTYPE;
     if (!(p->eps >= 0.0f) || !std::isfinite(p->eps)) return SSD_ERR_SHAPE;
     if (p->out_dtype == SSD_E4M3 && p->hidden / p->ngroups % 32 != 0) return SSD_ERR_UNSUPPORTED;
+    // (elements are counted in 32 bits, a block's threads ahead)
+    if (p->hidden / p->ngroups > 1 << 30) return SSD_ERR_UNSUPPORTED;
     const int per = p->hidden / p->ngroups, lanes = per <= 128 ? 16 : per <= 512 ? 64 : per / 8 + 64;
     if (!launches((int64_t)p->rows * p->ngroups, lanes < 1024 ? lanes : 1024)) return SSD_ERR_UNSUPPORTED;
     const int64_t h = p->hidden;

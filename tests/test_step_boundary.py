@@ -43,6 +43,7 @@ def call_norm(p, *over, residual=OK, gate=None, scale=None, keep=OK):
     # more threads than a launch takes
     (dict(rows=2 ** 28, hidden=1), UNSUP), (dict(rows=2 ** 26, hidden=512), UNSUP),
     (dict(rows=2 ** 22, hidden=32768), UNSUP),
+    (dict(rows=1, hidden=2 ** 31 - 64), UNSUP), (dict(rows=1, hidden=2 ** 30 + 32), UNSUP),   # counts past 31 bits
     (dict(out_dtype=3), NULL),                            # no scales
 ])
 def test_norm_refusals(kw, status):
