@@ -103,6 +103,35 @@ __device__ __forceinline__ int64_t group_of(const NormArgs &a, unsigned seg, int
     return row;
 }
 
+// 8 normed elements from `at` of a row on, the first n of them.
+template <typename TO> __device__ __forceinline__ void write_run(const NormArgs &a, int64_t row, int at, float *v, int n) {
+    if constexpr (std::is_same<TO, e4m3>::value) {
+        // (32 elements are 4 neighbouring lanes' and end with the group: all in or all out)
+        float top = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_size(v[e]));
+        top = fmaxf(top, dpp<0xb1>(top));
+        top = fmaxf(top, dpp<0x4e>(top));
+        const int b = scale_byte(top);
+        const float inv = __uint_as_float((254u - (uint32_t)b) << 23);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = fabsf(v[e]) < __builtin_inff() ? v[e] * inv : __builtin_nanf("");
+        u32x2 c;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * j], v[4 * j + 1], 0, false);
+            c[j] = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * j + 2], v[4 * j + 3], lo, true);
+        }
+        if (n > 0) {
+            typedef u32x2 any2 __attribute__((aligned(1)));
+            *reinterpret_cast<any2 *>(static_cast<uint8_t *>(a.out) + row * a.os + at) = c;
+            if ((threadIdx.x & 3) == 0) a.scale[row * (a.hidden / 32) + at / 32] = (uint8_t)b;
+        }
+    } else
+        Run8<TO>::store(static_cast<TO *>(a.out) + row * a.os + at, v, n);
+}
+
 // One group by one block (LANES 0) or by LANES lanes of a block of 256 threads, VPT vectors of 8
 // elements a thread.
 template <typename TX, typename TR, typename TO, int MODE, int VPT, int LANES>
@@ -163,76 +192,60 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(NormArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[k][e] *= w[e];
         }
-        if constexpr (std::is_same<TO, e4m3>::value) {
-            // (32 elements are 4 neighbouring lanes' and end with the group: all in or all out)
-            float top = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_size(v[k][e]));
-            top = fmaxf(top, dpp<0xb1>(top));
-            top = fmaxf(top, dpp<0x4e>(top));
-            const int b = scale_byte(top);
-            const float inv = __uint_as_float((254u - (uint32_t)b) << 23);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[k][e] = fabsf(v[k][e]) < __builtin_inff() ? v[k][e] * inv : __builtin_nanf("");
-            u32x2 c;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[k][4 * j], v[k][4 * j + 1], 0, false);
-                c[j] = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(v[k][4 * j + 2], v[k][4 * j + 3], lo, true);
-            }
-            if (n > 0) {
-                typedef u32x2 any2 __attribute__((aligned(1)));
-                *reinterpret_cast<any2 *>(static_cast<uint8_t *>(a.out) + row * a.os + at + i) = c;
-                if ((threadIdx.x & 3) == 0) a.scale[row * (a.hidden / 32) + (at + i) / 32] = (uint8_t)b;
-            }
-        } else
-            Run8<TO>::store(static_cast<TO *>(a.out) + row * a.os + at + i, v[k], n);
+        write_run<TO>(a, row, at + i, v[k], n);
     }
 }
 
-// The same for rows that no block can keep: an element a thread and step, read a
-// second time instead (64 rows of 40000 66 us, bound by the chain of a block's loads).
+// The same for rows that no block can keep: read a second time instead (64 rows of 40000 10.1 us,
+// 512 37.5, 4.4 TB/s of what has to be moved).
 template <typename TX, typename TR, typename TO, int MODE>
-__global__ __launch_bounds__(256) void norm_long_kernel(NormArgs a) {
-    __shared__ float part[4];
+__global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
+    __shared__ float part[16];
     int at;
     const int64_t row = group_of(a, blockIdx.x, at);
     const TX *const x = static_cast<const TX *>(a.x) + row * a.xs + at;
     const TR *const other = static_cast<const TR *>(a.other) + (MODE == kPlain ? 0 : row * a.others + at);
-    auto value = [&](int i) {
-        const float v = to_f32(x[i]);
-        if constexpr (MODE == kAdd) return v + to_f32(other[i]);
-        else if constexpr (MODE == kGate) return v * silu(to_f32(other[i]));
-        else return v;
+    constexpr int STEP = 1024 * 8;
+    auto values = [&](int i, float *v) {
+        Run8<TX> rx;
+        rx.load(x + i, a.per - i);
+        rx.get(v);
+        if constexpr (MODE != kPlain) {
+            Run8<TR> ro;
+            float o[8];
+            ro.load(other + i, a.per - i);
+            ro.get(o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = MODE == kAdd ? v[e] + o[e] : v[e] * silu(o[e]);
+        }
     };
     float sum = 0.0f;
-    for (int i = (int)threadIdx.x; i < a.per; i += 256) {
-        const float v = value(i);
-        sum = fmaf(v, v, sum);
+#pragma unroll 4
+    for (int i = (int)threadIdx.x * 8; i < a.per; i += STEP) {
+        float v[8];
+        values(i, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fmaf(v[e], v[e], sum);
     }
     sum = block_sum(sum, part);
     const float r = rsqrtf(sum / (float)a.per + a.eps);
-    for (int i = (int)threadIdx.x; i < a.per; i += 256) {
-        const float v = value(i);
+    for (int i = (int)threadIdx.x * 8; i < a.per; i += STEP) {
+        float v[8];
+        values(i, v);
         if constexpr (MODE == kAdd)
             // (behind the last read of the residual: it may be the same array)
-            if (a.sum) static_cast<TR *>(a.sum)[row * a.sums + at + i] = from_f32<TR>(v);
-        float y = v * r;
-        if (a.weight) y *= a.weight[at + i];
-        if constexpr (std::is_same<TO, e4m3>::value) {
-            // (groups are whole blocks of 32: half a wave is in or out together)
-            float top = finite_size(y);
+            if (a.sum) Run8<TR>::store(static_cast<TR *>(a.sum) + row * a.sums + at + i, v, a.per - i);
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
-            const int b = scale_byte(top);
-            y = fabsf(y) < __builtin_inff() ? y * __uint_as_float((254u - (uint32_t)b) << 23)
-                                            : __builtin_nanf("");
-            static_cast<uint8_t *>(a.out)[row * a.os + at + i] =
-                (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(y, y, 0, false);
-            if ((threadIdx.x & 31) == 0) a.scale[row * (a.hidden / 32) + (at + i) / 32] = (uint8_t)b;
-        } else
-            static_cast<TO *>(a.out)[row * a.os + at + i] = from_f32<TO>(y);
+        for (int e = 0; e < 8; ++e) v[e] *= r;
+        if (a.weight) {
+            Run8<float> rw;
+            float w[8];
+            rw.load(a.weight + at + i, a.per - i);
+            rw.get(w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= w[e];
+        }
+        write_run<TO>(a, row, at + i, v, a.per - i);
     }
 }
 
@@ -241,7 +254,7 @@ static void norm_t(const NormArgs &a, hipStream_t st) {
     const dim3 grid((unsigned)a.segments);
     const int vecs = (a.per + 7) / 8;
     if (vecs > 4096) {
-        hipLaunchKernelGGL((norm_long_kernel<TX, TR, TO, MODE>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((norm_long_kernel<TX, TR, TO, MODE>), grid, dim3(1024), 0, st, a);
         return;
     }
     // (32768 groups of 125: 18.8 us with a block each, 9.5 with 16 lanes)
