@@ -65,3 +65,66 @@ def test_answers(drafts, four_bit):
         best = target[1].argmax(-1).tolist()
         assert got[1] == best[:len(got[1])]
         last = torch.tensor([t[-1] for t in got], dtype=torch.int32, device="cuda")
+
+
+def test_chain_in_a_graph():
+    """Norm, product, probabilities and verification captured together, on a stream of its own, next to
+    the same calls made eagerly on another batch; replayed with new inputs each time."""
+    import state_space_model_varlen_amd as ssd
+    R, T, K, V, dev = 5, 3, 512, 40000, "cuda"
+    rows, bf, u8, i32 = R * T, torch.bfloat16, torch.uint8, torch.int32
+    g = torch.Generator(dev).manual_seed(11)
+    np_ = ssd.make_norm_problem(rows, K, bf, torch.float8_e4m3fn, residual_dtype=torch.float32)
+    lp = ssd.make_linear_problem(rows, K, V, torch.float8_e4m3fn, bf)
+    pp, vp = ssd.make_probs_problem(R, T, V, bf), ssd.make_verify_problem(R, T, V)
+    w = ssd.alloc_linear_weights(lp, dev)
+    ssd.linear_w4_encode(lp, torch.randn(V, K, generator=g, device=dev) * 0.1, **w)
+    temp = torch.tensor([1.0, 0.0, 0.5, 2.0, 1.0], device=dev)
+
+    def batch():
+        b = dict(x=torch.empty(rows, K, dtype=bf, device=dev), res=torch.empty(rows, K, device=dev),
+                 kept=torch.empty(rows, K, device=dev), rows8=torch.empty(rows, K, device=dev).to(torch.float8_e4m3fn),
+                 scale=torch.empty(rows, K // 32, dtype=u8, device=dev), logits=torch.empty(rows, V, dtype=bf, device=dev),
+                 probs=torch.empty(R, T, V, device=dev), drafts=torch.empty(R, T - 1, dtype=i32, device=dev),
+                 uniform=torch.empty(R, T, device=dev), acc=torch.empty(R, dtype=i32, device=dev),
+                 out=torch.empty(R, T, dtype=i32, device=dev), ws=ssd.alloc_probs_workspace(pp, dev),
+                 wv=ssd.alloc_verify_workspace(vp, dev))
+        fill(b)
+        return b
+
+    def fill(b):
+        b["x"].copy_(torch.randn(rows, K, generator=g, device=dev))
+        b["res"].copy_(torch.randn(rows, K, generator=g, device=dev))
+        b["drafts"].copy_(torch.randint(0, V, (R, T - 1), generator=g, device=dev))
+        b["uniform"].copy_(torch.rand(R, T, generator=g, device=dev))
+
+    def run(b):
+        ssd.rms_norm(np_, b["x"], None, b["rows8"], residual=b["res"], residual_out=b["kept"], out_scale=b["scale"])
+        ssd.linear_w4(lp, b["rows8"], w["weight"], w["weight_scale"], b["logits"], b["scale"])
+        ssd.token_probs(pp, b["logits"].view(R, T, V), temp, b["probs"], b["ws"])
+        ssd.verify_drafts(vp, b["probs"], None, b["drafts"], None, b["uniform"], b["acc"], b["out"], b["wv"])
+
+    a, other = batch(), batch()
+    run(a), run(other)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(a)
+    side = torch.cuda.Stream()
+    for _ in range(4):
+        fill(a), fill(other)
+        run(a)
+        want = {k: a[k].clone() for k in ("kept", "rows8", "scale", "logits", "probs", "acc", "out")}
+        for k in want:
+            a[k].view(u8).fill_(0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+        run(other)                              # at the same time, on buffers of its own
+        torch.cuda.synchronize()
+        for k, v in want.items():
+            assert torch.equal(a[k].view(u8), v.view(u8)), k
+        wa, wt = os_.verify(a["probs"].cpu(), None, a["drafts"].cpu(), None, a["uniform"].cpu())
+        assert np.array_equal(a["acc"].cpu().numpy(), wa) and np.array_equal(a["out"].cpu().numpy(), wt)
+        wa, wt = os_.verify(other["probs"].cpu(), None, other["drafts"].cpu(), None, other["uniform"].cpu())
+        assert np.array_equal(other["acc"].cpu().numpy(), wa) and np.array_equal(other["out"].cpu().numpy(), wt)
