@@ -617,7 +617,7 @@ static LinearMode linear_mode(const LinearDims &d) {
 // 18560 (TFLOP/s of 8-bit and bfloat16 rows; the whole chip), or its stages at the time of one;
 // and a time a round of blocks. On 105 sizes (1 to 4096 tokens, 512 to 8192 values, 300 to 18560
 // outputs) the tile so taken was on average 0.9 % (8 bits) and 0.8 % (bfloat16) slower than the best of
-// them, at most 22 and 18 %. 192 x 256 was added where tiles of 256 leave CUs without one: 4096 tokens, 5120
+// them, at most 22 and 18 % (without 192 x 256, which was added later). That one is for sizes whose tiles of 256 leave CUs without one: 4096 tokens, 5120
 // to 2560 are 220 of them, not 160 (8 bits 56.7 -> 51.1 us, bfloat16 119.9 -> 104.2); 2048 tokens, 2560 to
 // 10576: 67.0 -> 58.1, 128.8 -> 114.8.
 struct Tile {
