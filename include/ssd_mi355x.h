@@ -870,26 +870,27 @@ typedef struct {
     int32_t out_features; /* N */
     int32_t x_dtype;      /* SSD_BF16 or SSD_E4M3 */
     int32_t out_dtype;    /* SSD_BF16 or SSD_F32 */
-    int32_t reserved;     /* 0 */
+    int32_t cut_products; /* 1: products of 8-bit rows into SSD_BF16 may be cut; 0: they are exact */
     int64_t x_stride, out_stride;
 } linear_problem;
 
 /*
  *   out[t,n] = sum over k of x[t,k] w[n,k] + bias[n]
  * accumulated in float32, for one token (the weights' bytes bound it) to long
- * prompts (the matrix units do). Products are exact, but for 8-bit rows into
- * SSD_BF16: there the instruction keeps those of 32 values that share a block
- * to 2^-13 of the largest (a few 10^-6 of a result, far below its rounding).
+ * prompts (the matrix units do). Products are exact. With cut_products = 1 those
+ * of 8-bit rows into SSD_BF16 may be cut: of the 32 products of a block of k each
+ * by up to 2^-13 of the largest of x's block times the largest of w's. That is
+ * an error of the largest product's size, not of the result's: where large
+ * products cancel, what is left of the block's others may be nothing.
  *   weight [N,K/2] uint8: two codes a byte, the even k in the low half. A code
  *   is a sign bit and 0, 0.5, 1, 1.5, 2, 3, 4 or 6; the 32 codes of block b of
  *   a row stand for value * 2^(weight_scale[b] - 127)
  *   weight_scale [N,K/32] uint8 (255: NaN)
  *   x [T,K] bfloat16 with x_scale NULL, or SSD_E4M3 with x_scale [T,K/32]
- *   uint8 as rms_norm writes them (255: NaN). The matrix instruction takes
- *   8-bit rows, codes and both scales as they are; for bfloat16 rows, and for
- *   8-bit ones into SSD_F32, values are widened to bfloat16, which is exact
- *   where they lie in its range (scales that linear_w4_encode and rms_norm
- *   write do, values of 2^-126 up)
+ *   uint8 as rms_norm writes them (255: NaN). Values of both are widened to
+ *   bfloat16 before they are multiplied, which is exact from 2^-126 up to its
+ *   largest. Where products may be cut the matrix instruction takes 8-bit rows,
+ *   codes and both scales as they are
  *   bias [N] float32 or NULL; out [T,N]
  * x and its stride must keep every row 16-byte aligned, weight must be 16-byte
  * aligned (SSD_ERR_ALIGN).

@@ -18,7 +18,7 @@ class norm_problem(ctypes.Structure):
 
 class linear_problem(ctypes.Structure):
     _fields_ = [(n, _i32) for n in (
-        "tokens", "in_features", "out_features", "x_dtype", "out_dtype", "reserved")] + [
+        "tokens", "in_features", "out_features", "x_dtype", "out_dtype", "cut_products")] + [
             ("x_stride", _i64), ("out_stride", _i64)]
 
 

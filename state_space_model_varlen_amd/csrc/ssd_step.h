@@ -24,7 +24,7 @@ void launch_rms_norm(const NormDims &d, const void *x, const void *gate, const v
 
 struct LinearDims {
     int T, K, N;
-    bool e4m3, out_bf16;
+    bool e4m3, out_bf16, cut;
     int64_t xs, os;
 };
 struct LinearArgs {

@@ -79,6 +79,7 @@ int linear_dims(const linear_problem *p, ssd::LinearDims *d)
     if (p->tokens < 0 || p->in_features <= 0 || p->out_features <= 0) return SSD_ERR_SHAPE;
     if ((p->x_dtype != SSD_BF16 && p->x_dtype != SSD_E4M3) || !float_ok(p->out_dtype))
         return SSD_ERR_DTYPE;
+    if (p->cut_products != 0 && p->cut_products != 1) return SSD_ERR_UNSUPPORTED;
     if (p->in_features % 32 != 0) return SSD_ERR_UNSUPPORTED;
     if (!stride_of(p->x_stride, p->in_features, &d->xs) ||
         !stride_of(p->out_stride, p->out_features, &d->os))
@@ -94,6 +95,7 @@ int linear_dims(const linear_problem *p, ssd::LinearDims *d)
     d->N = p->out_features;
     d->e4m3 = p->x_dtype == SSD_E4M3;
     d->out_bf16 = p->out_dtype == SSD_BF16;
+    d->cut = p->cut_products != 0;
     return SSD_OK;
 }
 

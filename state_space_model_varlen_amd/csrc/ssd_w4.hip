@@ -5,13 +5,14 @@
 // are 4 neighbouring outputs of one token. K goes in steps of 128: lane l of
 // a wave reads 16 bytes of weight row l % 16, the 32 codes of block l / 16 of
 // the step, as they lie in memory.
-//   8-bit rows: one 16 x 16 x 128 instruction takes codes, 8-bit values and the
-//   exponent bytes of both. It expects of a lane's 32 token values the first 16
-//   from K = 16 (l / 16) and the others from 64 + 16 (l / 16), while a lane's
-//   exponent byte belongs to block l / 16 of either operand.
-//   bfloat16 rows: the codes are widened to bfloat16 with their block's power of
-//   two (exact), and four 16 x 16 x 32 instructions each take 8 of them; the
+//   The codes are widened to bfloat16 with their block's power of two (exact),
+//   8-bit rows too, and four 16 x 16 x 32 instructions each take 8 of them; the
 //   order of K inside the step does not matter as long as both operands keep it.
+//   8-bit rows whose products may be cut (cut_products): one 16 x 16 x 128
+//   instruction takes codes, 8-bit values and the exponent bytes of both. It
+//   expects of a lane's 32 token values the first 16 from K = 16 (l / 16) and the
+//   others from 64 + 16 (l / 16), while a lane's exponent byte belongs to block
+//   l / 16 of either operand.
 #include <stdint.h>
 
 #include "ssd_layer_device.h"
@@ -25,7 +26,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
 enum LinearMode {
-    kEight,      // 8-bit rows, scaled 8-bit instruction
+    kEight,      // 8-bit rows, scaled 8-bit instruction: products cut
     kSixteen,    // bfloat16 rows
     kWidened     // 8-bit rows widened to bfloat16
 };
@@ -607,9 +608,10 @@ __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) 
 size_t linear_workspace(const LinearDims &) { return 0; }
 
 static LinearMode linear_mode(const LinearDims &d) {
-    // float32 results of 8-bit rows come from widened values: the 8-bit instruction cuts the products of
-    // 32 values off at 2^-13 of the largest, 4e-6 of a result's size, which bfloat16 does not see
-    return !d.e4m3 ? kSixteen : d.out_bf16 ? kEight : kWidened;
+    // The 8-bit instruction cuts the 32 products of a block off at 2^-13 of the largest, whatever is left
+    // of them: with one product of 2688 that another cancels, others of up to 0.3 came to nothing. Its
+    // products are a caller's choice, for bfloat16 results; others come from widened values.
+    return !d.e4m3 ? kSixteen : d.cut && d.out_bf16 ? kEight : kWidened;
 }
 
 // The tiles that are built. One is taken by its estimated time on the CU that gets the most of
@@ -711,6 +713,7 @@ void launch_linear(const LinearDims &d, const LinearArgs &a, void *, void *strea
     const LinearMode m = linear_mode(d);
     const bool words = d.K % 128 == 0 && ((uintptr_t)a.x_scale | (uintptr_t)a.w_scale) % 4 == 0;
     if (m == kEight) words ? linear_t<kEight, kWords, bf16>(d, a, st) : linear_t<kEight, kBytes, bf16>(d, a, st);
+    else if (m == kWidened && d.out_bf16) words ? linear_t<kWidened, kWords, bf16>(d, a, st) : linear_t<kWidened, kBytes, bf16>(d, a, st);
     else if (m == kWidened) words ? linear_t<kWidened, kWords, float>(d, a, st) : linear_t<kWidened, kBytes, float>(d, a, st);
     else if (d.out_bf16) linear_t<kSixteen, kBytes, bf16>(d, a, st);
     else linear_t<kSixteen, kBytes, float>(d, a, st);

@@ -129,11 +129,13 @@ def rms_norm(p: norm_problem, x, weight, out, residual=None, residual_out=None, 
 # products with 4-bit weights
 
 def make_linear_problem(tokens: int, in_features: int, out_features: int, x_dtype: torch.dtype,
-                        out_dtype: torch.dtype) -> linear_problem:
-    """x_dtype: bfloat16, or float8_e4m3fn with a scale byte for 32 elements."""
+                        out_dtype: torch.dtype, cut_products: bool = False) -> linear_problem:
+    """x_dtype: bfloat16, or float8_e4m3fn with a scale byte for 32 elements. cut_products: those of
+    8-bit rows into bfloat16 may be cut at 2^-13 of the largest of their 32."""
     p = linear_problem()
     p.tokens, p.in_features, p.out_features = int(tokens), int(in_features), int(out_features)
     p.x_dtype, p.out_dtype = _ROW_DT[x_dtype], _DT[out_dtype]
+    p.cut_products = int(bool(cut_products))
     return p
 
 
