@@ -909,7 +909,8 @@ int linear_w4(const linear_problem *p, const void *x, const uint8_t *x_scale,
  * 16-byte aligned): for every 32 of a row the least power of two for which
  * none exceeds 6 of it (2^-126 to 2^125; 32 zeros have scale byte 1), each
  * element rounded to the nearest value, of two equally near ones to the even
- * code; infinities become 6 and NaN 0 and do not enter the scale. Uses
+ * code; what is past 6 2^125 becomes that (so that every value is a bfloat16);
+ * infinities become 6 and NaN 0 and do not enter the scale. Uses
  * in_features and out_features of p alone.
  */
 int linear_w4_encode(const linear_problem *p, int32_t dtype, const void *w, uint8_t *weight,

@@ -64,14 +64,14 @@ def weights(codes, scale):
 
 
 def encode_weights(row):
-    """Values and scale byte of 32 weights: the least power of two 2^s, s >= -126, with |w| <= 6 2^s
-    for every finite w; each to the nearest value, of two equally near ones the one at an even
-    place."""
+    """Values and scale byte of 32 weights: the least power of two 2^s, -126 <= s <= 125, with
+    |w| <= 6 2^s for every finite w (125 where there is none); each to the nearest value, of two
+    equally near ones the one at an even place."""
     row = np.asarray(row, dtype=np.float64)
     fin = np.isfinite(row)
     top = np.abs(row[fin]).max() if fin.any() else 0.0
     s = -126
-    while top > 6.0 * 2.0 ** s:
+    while top > 6.0 * 2.0 ** s and s < 125:
         s += 1
     got = np.zeros(row.shape)
     for i, v in enumerate(row):

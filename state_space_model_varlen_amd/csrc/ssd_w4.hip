@@ -732,10 +732,10 @@ __global__ __launch_bounds__(256) void encode_kernel(int64_t blocks, const T *__
 #pragma unroll
     for (int i = 0; i < 32; ++i) top = fabsf(v[i]) < __builtin_inff() ? fmaxf(top, fabsf(v[i])) : top;
     // top = 1.m 2^e and 6 = 1.5 2^2: the least s with top <= 6 2^s is e - 2, one more where
-    // 1.m > 1.5
+    // 1.m > 1.5; 6 2^125 = 1.5 2^127 is the largest whose codes all stay in bfloat16's range
     const uint32_t bits = __float_as_uint(top);
     int e = (int)(bits >> 23) - 2 + ((bits & 0x7fffffu) > 0x400000u ? 1 : 0);
-    e = e < 1 ? 1 : e;
+    e = e < 1 ? 1 : e > 252 ? 252 : e;
     const float inv = __uint_as_float((254u - (uint32_t)e) << 23);
     uint32_t word[4] = {0, 0, 0, 0};
 #pragma unroll
