@@ -32,10 +32,11 @@ def rms_norm(x, weight=None, residual=None, gate=None, groups=1, eps=1e-5):
     g = v.reshape(rows, groups, per)
     out = (g / np.sqrt((g ** 2).mean(-1, keepdims=True) + eps)).reshape(rows, h)
     w = np.ones(h) if weight is None else f64(weight)
-    # the sum of squares: one rounding a term of a thread's chain (at least 64 threads share a
-    # group), then at most 64 over the block; quotient, eps, root, two products
+    # the sum of squares: one rounding a term of a thread's chain (of at most 32: longer ones go on
+    # in 64 bits), rounded to float32 once, then 6 over the wave and at most 16 over the block; quotient,
+    # eps, root, two products
     worst = rel.reshape(rows, groups, per).max(-1, keepdims=True).repeat(per, -1).reshape(rows, h)
-    off = rel + worst + ((per / 64 + 64) / 2 + 8) * EPS
+    off = rel + worst + ((min(per, 32) + 1 + 6 + 16) / 2 + 8) * EPS
     return out * w, v, np.abs(out * w) * off + 1e-37
 
 

@@ -197,7 +197,8 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(NormArgs a) {
 }
 
 // The same for rows that no block can keep: read a second time instead (64 rows of 40000 10.1 us,
-// 512 37.5, 4.4 TB/s of what has to be moved).
+// 512 37.5, 4.4 TB/s of what has to be moved). A thread adds up to 2^20 squares, 8 of them in float32
+// and their sums in 64 bits: equal squares would all round one way (2^26 elements of 1.1 were off by 3e-4).
 template <typename TX, typename TR, typename TO, int MODE>
 __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
     __shared__ float part[16];
@@ -219,15 +220,16 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
             for (int e = 0; e < 8; ++e) v[e] = MODE == kAdd ? v[e] + o[e] : v[e] * silu(o[e]);
         }
     };
-    float sum = 0.0f;
+    double squares = 0.0;
 #pragma unroll 4
     for (int i = (int)threadIdx.x * 8; i < a.per; i += STEP) {
-        float v[8];
+        float v[8], eight = 0.0f;
         values(i, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(v[e], v[e], sum);
+        for (int e = 0; e < 8; ++e) eight = fmaf(v[e], v[e], eight);
+        squares += (double)eight;
     }
-    sum = block_sum(sum, part);
+    const float sum = block_sum((float)squares, part);
     const float r = rsqrtf(sum / (float)a.per + a.eps);
     for (int i = (int)threadIdx.x * 8; i < a.per; i += STEP) {
         float v[8];
