@@ -55,9 +55,11 @@ struct InvTemp {
         rest = fmaf(d, lo, fmaf(d, hi, -y));
         return __builtin_amdgcn_exp2f(y);
     }
-    __device__ __forceinline__ float operator()(float d) const {
-        const float y = d * hi;
-        const float rest = fmaf(d, hi, -y) + d * lo;
+    // exp((v - top) / T) of v that is not -infinity, at any T (the halves' difference is a float where
+    // v - top is past the largest, and at temperatures that are not usual their exponential counts)
+    __device__ __forceinline__ float operator()(float v, float top) const {
+        const float d = 0.5f * v - 0.5f * top, y = 2.0f * (d * hi);
+        const float rest = 2.0f * (fmaf(d, hi, -0.5f * y) + d * lo);
         const float e = __builtin_amdgcn_exp2f(y);
         return y > -1000.0f ? fmaf(e, rest * kLn2, e) : e;      // (NaN passes through e)
     }
@@ -140,7 +142,7 @@ __device__ __forceinline__ Peak block_peak(const Logits<T, N> &l, int from, cons
         // (a logit of NaN or +infinity makes the sum NaN)
         s += own == -__builtin_inff() ? 0.0f : own - own;
     } else
-        l.each(from, 64 * W, [&](int, float v) { s += v == -__builtin_inff() ? 0.0f : inv(v - top); });
+        l.each(from, 64 * W, [&](int, float v) { s += v == -__builtin_inff() ? 0.0f : inv(v, top); });
     s = group_sum(s, 64);
     if (lane == 0) sums[wave] = s;
     __syncthreads();
@@ -174,7 +176,7 @@ __device__ __forceinline__ void write_probs(const Logits<T, N> &l, int from, int
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const float v = l.at(j, e);
-                y[e] = greedy ? (i + e == k.at ? 1.0f : 0.0f) : v == -__builtin_inff() ? none : inv(v - top) * r;
+                y[e] = greedy ? (i + e == k.at ? 1.0f : 0.0f) : v == -__builtin_inff() ? none : inv(v, top) * r;
             }
         if (i + E <= end)
 #pragma unroll
@@ -223,7 +225,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 4 : 1) void probs_kernel(int V, in
         float s = 0.0f;
         for (int i = lane; i < parts; i += 64) {
             const Peak o = mine[i];
-            s += o.m == -__builtin_inff() ? o.s : o.s * inv(o.m - k.m);
+            s += o.m == -__builtin_inff() ? o.s : o.s * inv(o.m, k.m);
         }
         k.s = group_sum(s, 64);
     }
