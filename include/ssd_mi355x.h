@@ -895,7 +895,7 @@ typedef struct {
  * x and its stride must keep every row 16-byte aligned, weight must be 16-byte
  * aligned (SSD_ERR_ALIGN).
  *   workspace   linear_w4_workspace_bytes(p) bytes, 16-byte aligned (NULL when
- *               that is 0)
+ *               that is 0, which it is for every problem)
  */
 size_t linear_w4_workspace_bytes(const linear_problem *p);
 /* (for profiles and tests: the kernel that runs p; "" for a problem refused) */

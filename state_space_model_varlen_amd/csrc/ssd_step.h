@@ -33,9 +33,8 @@ struct LinearArgs {
     const float *bias;
     void *out;
 };
-size_t linear_workspace(const LinearDims &d);
 const char *linear_kernel_name(const LinearDims &d);
-void launch_linear(const LinearDims &d, const LinearArgs &a, void *workspace, void *stream);
+void launch_linear(const LinearDims &d, const LinearArgs &a, void *stream);
 void launch_linear_encode(int N, int K, bool bf16, const void *w, uint8_t *codes, uint8_t *scale,
                           void *stream);
 

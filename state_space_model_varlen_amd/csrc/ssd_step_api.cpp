@@ -161,11 +161,8 @@ int rms_norm(const norm_problem *p, const void *x, const void *gate, const void 
     return launch_status();
 }
 
-size_t linear_w4_workspace_bytes(const linear_problem *p)
-{
-    ssd::LinearDims d;
-    return linear_dims(p, &d) ? 0 : ssd::linear_workspace(d);
-}
+// (none is needed: sums that waves share are joined in LDS)
+size_t linear_w4_workspace_bytes(const linear_problem *) { return 0; }
 
 const char *linear_w4_kernel(const linear_problem *p)
 {
@@ -175,19 +172,17 @@ const char *linear_w4_kernel(const linear_problem *p)
 
 int linear_w4(const linear_problem *p, const void *x, const uint8_t *x_scale,
               const uint8_t *weight, const uint8_t *weight_scale, const float *bias, void *out,
-              void *workspace, size_t workspace_bytes, void *stream)
+              void *, size_t, void *stream)
 {
     ssd::LinearDims d;
-    int rc = linear_dims(p, &d);
+    const int rc = linear_dims(p, &d);
     if (rc) return rc;
     if (!x || !weight || !weight_scale || !out || (d.e4m3 && !x_scale)) return SSD_ERR_NULL;
     if (!row_aligned(x, d.xs, size_of(p->x_dtype)) || !aligned(weight, 16) || !aligned(bias, 4) ||
         !aligned(out, size_of(p->out_dtype)))
         return SSD_ERR_ALIGN;
-    rc = workspace_ok(workspace, workspace_bytes, ssd::linear_workspace(d));
-    if (rc) return rc;
     const ssd::LinearArgs a{x, x_scale, weight, weight_scale, bias, out};
-    ssd::launch_linear(d, a, workspace, stream);
+    ssd::launch_linear(d, a, stream);
     return launch_status();
 }
 

@@ -605,8 +605,6 @@ __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) 
     }
 }
 
-size_t linear_workspace(const LinearDims &) { return 0; }
-
 static LinearMode linear_mode(const LinearDims &d) {
     // The 8-bit instruction cuts the 32 products of a block off at 2^-13 of the largest, whatever is left
     // of them: with one product of 2688 that another cancels, others of up to 0.3 came to nothing. Its
@@ -706,7 +704,7 @@ static void linear_t(const LinearDims &d, const LinearArgs &a, hipStream_t st) {
         if constexpr (MODE != kSixteen) linear_tile<MODE, 2, 4, 1, 4, 4, 1, 3, W, 1, TO>(d, a, st);
     }
 }
-void launch_linear(const LinearDims &d, const LinearArgs &a, void *, void *stream)
+void launch_linear(const LinearDims &d, const LinearArgs &a, void *stream)
 {
     if (d.T <= 0) return;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);

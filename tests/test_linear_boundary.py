@@ -19,3 +19,16 @@ def test_products_are_cut_by_choice_alone():
         p.cut_products = bad
         assert LIB.linear_w4(ctypes.byref(p), *[OK] * 7, 0, None) == UNSUP
         assert ssd.linear_w4_kernel(p) == ""
+
+
+@pytest.mark.parametrize("xt", [BF, E4])
+def test_no_workspace_is_needed_or_looked_at(xt):
+    """Every problem's is empty, and what is passed for one decides nothing: a call goes on to what is wrong."""
+    for t in (1, 16, 64, 300, 4096):
+        for k in (64, 1024, 8192):
+            p = ssd.make_linear_problem(t, k, 2560, xt, BF)
+            assert ssd.linear_w4_workspace_bytes(p) == 0 and ssd.linear_w4_kernel(p) != ""
+            assert ssd.alloc_linear_workspace(p, "cpu") is None
+            for ws in (None, OK, ctypes.c_void_p(257)):
+                args = [OK, OK, OK, OK, None, None, ws]               # no result
+                assert LIB.linear_w4(ctypes.byref(p), *args, ctypes.c_size_t(0), None) == 1
