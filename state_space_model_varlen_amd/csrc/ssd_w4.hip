@@ -613,26 +613,37 @@ static LinearMode linear_mode(const LinearDims &d) {
 }
 
 // The tiles that are built. One is taken by its estimated time on the CU that gets the most of
-// them: its bytes, its products at a share of the rate that the tile reached on 4096 tokens, 4096 to
-// 18560 (TFLOP/s of 8-bit and bfloat16 rows; the whole chip), or its stages at the time of one;
-// and a time a round of blocks. On 105 sizes (1 to 4096 tokens, 512 to 8192 values, 300 to 18560
-// outputs) the tile so taken was on average 0.9 % (8 bits) and 0.8 % (bfloat16) slower than the best of
-// them, at most 22 and 18 % (without 192 x 256, which was added later). That one is for sizes whose tiles of 256 leave CUs without one: 4096 tokens, 5120
-// to 2560 are 220 of them, not 160 (8 bits 56.7 -> 51.1 us, bfloat16 119.9 -> 104.2); 2048 tokens, 2560 to
-// 10576: 67.0 -> 58.1, 128.8 -> 114.8.
+// them: its bytes, its products at a share of the rate that the tile reached on long prompts
+// (TFLOP/s; the whole chip), or its stages at the time of one; and a time a round of blocks. On 185
+// sizes (1 to 4096 tokens, 256 to 8192 values, 300 to 50257 outputs) the tile so taken was on average 1.0 %
+// (bfloat16 rows) and 2.3 % (cut products) slower than the best of them, on 280 sizes of widened 8-bit rows
+// 1.9 %, at most 30, 37 and 36 %. (Widened rows by the cut products' figures: 5.2 %, at most 71.)
+// 192 x 256 is for sizes
+// whose tiles of 256 leave CUs without one: 4096 tokens, 5120 to 2560 are 220 of them, not 160 (bfloat16
+// 119.9 -> 104.2 us); 2048 tokens, 2560 to 10576: 128.8 -> 114.8.
 struct Tile {
     int tokens, rows, threads, per_cu, steps;      // steps of 128 (bfloat16: 64) values a stage
-    double rate8, rate16;
+    double rate[3];                                // by LinearMode
 };
 static constexpr Tile kTiles[] = {
-    {16, 16, 256, 2, 4, 224, 103},      {16, 32, 128, 2, 1, 369, 191},     {32, 32, 256, 1, 4, 385, 246},
-    {64, 64, 256, 2, 2, 898, 576},      {128, 128, 512, 2, 1, 1793, 1014}, {256, 256, 512, 1, 1, 2507, 1341},
-    {192, 256, 512, 1, 1, 2250, 1200},  {128, 256, 512, 1, 1, 1850, 0}};
+    {16, 16, 256, 2, 4, {224, 103, 198}},       {16, 32, 128, 2, 1, {369, 191, 349}},
+    {32, 32, 256, 1, 4, {385, 246, 307}},       {64, 64, 256, 2, 2, {898, 576, 547}},
+    {128, 128, 512, 2, 1, {1793, 1014, 1054}},  {256, 256, 512, 1, 1, {2507, 1341, 1247}},
+    {192, 256, 512, 1, 1, {2250, 1200, 1127}},  {128, 256, 512, 1, 1, {1850, 0, 1058}}};
+// Bytes a microsecond of a CU, share of the rate, microseconds of a stage and what a further step of it adds,
+// microseconds of a round.
+struct TileTimes {
+    double bytes, products, stage, step, round;
+};
+static constexpr TileTimes kTileTimes[3] = {
+    {2.75e4, 0.944, 0.162, 0.267, 1.43}, {6.05e4, 0.531, 0.269, 0.264, 0.947}, {1.87e4, 0.501, 0.27, 0.261, 1.15}};
 static const char *const kTileNames[] = {"16x16",   "16x32",   "32x32",   "64x64",
                                          "128x128", "256x256", "192x256", "128x256"};
 
 static int linear_tile_of(const LinearDims &d) {
-    const bool wide = !d.e4m3;
+    const LinearMode mode = linear_mode(d);
+    const TileTimes &c = kTileTimes[mode];
+    const bool wide = mode == kSixteen;
     int best = -1;
     double least = 0;
     for (int i = 0; i < (wide ? 7 : 8); ++i) {
@@ -644,11 +655,11 @@ static int linear_tile_of(const LinearDims &d) {
         const double flops = 2.0 * t.tokens * t.rows * d.K;
         const double stages = d.K / (wide ? 64.0 : 128.0) / t.steps;
         // microseconds
-        const double by_bytes = most * bytes / (wide ? 6.05e4 : 2.75e4);
-        const double by_products = most * flops * 256e-6 / (wide ? t.rate16 * 0.531 : t.rate8 * 0.944);
-        const double by_stages = rounds * stages * (wide ? 0.269 * (1 + 0.264 * t.steps) : 0.162 * (1 + 0.267 * t.steps));
+        const double by_bytes = most * bytes / c.bytes;
+        const double by_products = most * flops * 256e-6 / (t.rate[mode] * c.products);
+        const double by_stages = rounds * stages * c.stage * (1 + c.step * t.steps);
         double time = by_bytes > by_products ? by_bytes : by_products;
-        time = (time > by_stages ? time : by_stages) + rounds * (wide ? 0.947 : 1.43);
+        time = (time > by_stages ? time : by_stages) + rounds * c.round;
         if (best < 0 || time < least) {
             least = time;
             best = i;
@@ -657,11 +668,14 @@ static int linear_tile_of(const LinearDims &d) {
     return best;
 }
 
-// Up to this many tokens' bytes the block of every 16 weight rows reads them all; with more of them
-// than weights the tiles, which share them, are faster.
+// Up to 4 tokens: a block of every 16 weight rows reads them all; with more of them the tiles, which
+// share them, are faster. On 8 sizes of 1 to 8 tokens this limit was on average 3.5 % (bfloat16 rows), 3.0 %
+// (widened) and 3.9 % (cut) slower than the faster of the two ways; a limit of 8 3.9, 6.0 and 10.9 %, of 2
+// 8.1, 4.2 and 2.6 % (8 tokens of 8 bits, 4096 to 18560: 19.8 us here and 14.9 by the tiles; 2560 to 10576:
+// 8.5 and 9.9).
 static bool linear_few(const LinearDims &d) {
     const int64_t bytes = (int64_t)d.T * (d.K + 255) / 256 * 256 * (d.e4m3 ? 1 : 2);
-    return d.T <= (d.e4m3 ? 8 : 4) && bytes <= 48 << 10;
+    return d.T <= 4 && bytes <= 48 << 10;
 }
 const char *linear_kernel_name(const LinearDims &d) { return linear_few(d) ? "few" : kTileNames[linear_tile_of(d)]; }
 
