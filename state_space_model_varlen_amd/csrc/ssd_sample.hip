@@ -289,7 +289,7 @@ void launch_probs(const ProbsDims &d, const void *logits, const float *temperatu
 // step, far less than the distance of a uniform number of 24 bits from a
 // border that it does not lie on.
 //
-// Rows of up to 16 K entries are one block's work. Longer ones take two launches: the
+// Rows of up to 12 K entries are one block's work. Longer ones take two launches: the
 // weights of every 2048 entries are summed (a wave each), then one block a request
 // finds the 2048 that the draw falls into and goes through their entries. Bound by the
 // rows' bytes (128 requests of 131072: 29 us, 4.6 TB/s), for few requests by two launches and
@@ -473,9 +473,11 @@ __device__ __forceinline__ void weigh_run(const Row &row, int v0, int V, double 
     for (int j = 0; j < N; ++j) row.weigh(v0 + j, p[j], q[j], w[j], plain[j]);
 }
 
-// Rows of up to 16 K entries: all in one block a request, 16 entries a thread.
-constexpr int kWholePer = 16, kWholeMost = 1024 * kWholePer;
-__global__ __launch_bounds__(1024) void verify_whole_kernel(VerifyDims d, VerifyArgs a) {
+// Rows of up to 12 K entries: all in one block a request, 16 entries a thread. (One launch and two, in a
+// captured graph: 128 requests of 8000 11.1 and 13.6 us, of 12000 12.7 and 13.7, of 16384 14.3 and 13.7; one
+// request of 12000 11.1 and 12.3, of 16384 12.5 and 12.2; 512 of 8000 14.6 and 16.1, of 12000 25.6 and 19.7.)
+constexpr int kWholePer = 16, kWholeThreads = 768, kWholeMost = kWholeThreads * kWholePer;
+__global__ __launch_bounds__(kWholeThreads) void verify_whole_kernel(VerifyDims d, VerifyArgs a) {
     __shared__ BlockScan<2> scan;
     __shared__ Pick pick;
     const int r = blockIdx.x, tid = threadIdx.x, v0 = tid * kWholePer;
