@@ -267,6 +267,8 @@ static void norm_t(const NormArgs &a, hipStream_t st) {
         else hipLaunchKernelGGL((norm_kernel<TX, TR, TO, MODE, 1, 64>), blocks, dim3(256), 0, st, a);
         return;
     }
+    // (512 rows, 1, 2 and 4 vectors a thread: of 2560 elements 4.1, 4.7 and 6.0 us, of 8192 6.8, 6.6 and 6.9, of
+    // 16384 10.4 by 2 and by 4; 32768 22.8 by 4 and 30.3 read twice)
     const int vpt = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : 4;
     const dim3 block((unsigned)(((vecs + vpt - 1) / vpt + 63) / 64 * 64));
     if (vpt == 1) hipLaunchKernelGGL((norm_kernel<TX, TR, TO, MODE, 1, 0>), grid, block, 0, st, a);

@@ -618,9 +618,8 @@ static LinearMode linear_mode(const LinearDims &d) {
 // sizes (1 to 4096 tokens, 256 to 8192 values, 300 to 50257 outputs) the tile so taken was on average 1.0 %
 // (bfloat16 rows) and 2.3 % (cut products) slower than the best of them, on 280 sizes of widened 8-bit rows
 // 1.9 %, at most 30, 37 and 36 %. (Widened rows by the cut products' figures: 5.2 %, at most 71.)
-// 192 x 256 is for sizes
-// whose tiles of 256 leave CUs without one: 4096 tokens, 5120 to 2560 are 220 of them, not 160 (bfloat16
-// 119.9 -> 104.2 us); 2048 tokens, 2560 to 10576: 128.8 -> 114.8.
+// 192 x 256 is for sizes whose tiles of 256 leave CUs without one: 4096 tokens, 5120 to 2560 are 220 of
+// them, not 160 (bfloat16 119.9 -> 104.2 us); 2048 tokens, 2560 to 10576: 128.8 -> 114.8.
 struct Tile {
     int tokens, rows, threads, per_cu, steps;      // steps of 128 (bfloat16: 64) values a stage
     double rate[3];                                // by LinearMode
