@@ -828,7 +828,10 @@ int attention_decode(const attn_decode_problem *p, const void *q, const void *k_
  * more, every check on the host before the first launch, no result that
  * depends on the order in which blocks run. A workspace holds nothing between
  * calls, and calls that may run at the same time need one each. Arrays of one
- * call must not overlap, except where an entry point says so.
+ * call must not overlap, except where an entry point says so. Refused with
+ * SSD_ERR_UNSUPPORTED: groups of the norm above 2^30 elements; in_features or
+ * x_stride of a product above 2^21; vocabularies above 2^27; a verification of
+ * more than 65535 requests; calls of more threads than a launch takes (2^32).
  */
 
 /* Root-mean-square norm (host struct). */

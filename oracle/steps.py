@@ -103,8 +103,8 @@ def linear(x, w, bias=None):
 def linear_tolerance(y, mag, k, dtype, cut=0.0):
     """Products are exact in float32; of their sum's K + 8 additions each is off by at most a step
     (2^-23, should the matrix unit cut off instead of rounding) of a partial sum, which is never
-    larger than mag; then the result's own rounding. `cut`: cut_products, with 8-bit rows and
-    bfloat16 results."""
+    larger than mag; then the result's own rounding. `cut`: cut_products, where the caller lets
+    products be cut."""
     return (k + 8) * 2 * EPS * mag + cut + STEP[dtype] * (np.abs(y) + cut) + 1e-37
 
 

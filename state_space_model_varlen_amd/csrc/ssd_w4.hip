@@ -90,9 +90,9 @@ __device__ __forceinline__ f32x4 mma_8bit(i32x4 w, int ws, i32x4 x0, i32x4 x1, i
 // values at a time, their weights straight to registers, all of a wave's first
 // UNITS turns on their way before the tokens are waited for, and are joined in
 // LDS. Bound by the weights' bytes (4 tokens, 4096 to 18560: 16.5 us, 2.5 TB/s) and, for small
-// ones, by the chain of loads, products and join (one, 2560 to 10576: 6.3 us). What counts is few loads, as every one of a
-// wave takes its turn at the address unit whatever it brings: two of weights and,
-// where rows of scales are whole words (WORDS), one of scales for 4 K of products.
+// ones, by the chain of loads, products and join (one, 2560 to 10576: 6.3 us). What counts is few loads,
+// whatever each brings: two of weights and, where rows of scales are whole words (WORDS), one of scales
+// for 4 K of products.
 template <int MODE, bool WORDS, typename TO>
 __global__ __launch_bounds__(256) void linear_few_kernel(LinearDims d, LinearArgs a, int pitch)
 {
@@ -201,9 +201,11 @@ __global__ __launch_bounds__(256) void linear_few_kernel(LinearDims d, LinearArg
 // themselves, a stage of K (128 values of 8-bit rows, 64 of bfloat16) in one of
 // NBUF buffers: while a stage is multiplied the next NBUF - 1 are on their way.
 // Bound by the matrix units with what feeds them: 4096 tokens, 2560 to 10576 186 us in
-// bfloat16 (1190 TFLOP/s; 8192 each way 769, 1430) and 104 in 8 bits (2130; 393, 2800).
-// With the loads taken out a 128 x 256 stage of 8 bits goes from 0.95 to 0.6 us, with the
-// products taken out it stays at 0.9: a load's turn at the address unit is what is left.
+// bfloat16 and in widened 8 bits (1190 TFLOP/s; 8192 each way 758 and 749, 1450 and 1470), 100 with
+// cut products (2210; 381, 2880).
+// With cut products and the loads taken out a 128 x 256 stage goes from 0.95 to 0.6 us, with the products
+// taken out it stays at 0.9. Where in a load's way that time goes is not known: the address units
+// are busy for 32 % of this tile's time and 52 % of that of 192 x 256 (TA_BUSY_avr).
 //
 // A token's 128 bytes of a stage are 8 chunks, chunk c in place c ^ token / 2 % 8,
 // so that the 16 tokens that a fragment reads together touch all banks. Weight
@@ -212,9 +214,9 @@ __global__ __launch_bounds__(256) void linear_few_kernel(LinearDims d, LinearArg
 //
 // Scales take a word each: of kWords the 4 bytes of a stage in one (their arrays' rows are whole words
 // then), of kBytes one byte. kQuads (rows are whole 16 bytes) loads them for four stages at once, to
-// one of two places of their own: a row's scales are in a line of their own, which takes its turn
-// whatever is used of it. For 128 x 256, which is bound by these turns: 384 tokens, 4096 to 18560
-// 35.2 -> 33.3 us; the larger tiles have fewer of them and lose by reading the bytes apart (192 x 256,
+// one of two places of their own: a row's scales are in a line of their own, which takes a load
+// whatever is used of it. For 128 x 256 with cut products, which is bound by its loads: 384 tokens, 4096 to
+// 18560 35.2 -> 33.3 us; the larger tiles have fewer of them and lose by reading the bytes apart (192 x 256,
 // 4096 tokens, 5120 to 2560: 54.2 -> 56.8).
 enum Scales { kBytes, kWords, kQuads };
 typedef __attribute__((address_space(3))) void lds_void;
@@ -512,9 +514,8 @@ __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) 
     };
 
     // the products of one buffer's stage, with the loads of stage `next` into another between them
-    // (each takes its turn at the address unit, in front of which the products would wait; with two
-    // buffers they have to be on their way first: 4096 tokens, 5120 to 2560 in 8 bits 65 -> 59 us, with
-    // two buffers in bfloat16 118 -> 132)
+    // (asked for all at once they hold the products up; with two buffers they have to be on their way
+    // first: 4096 tokens, 5120 to 2560 with cut products 65 -> 59 us, with two buffers in bfloat16 118 -> 132)
     auto multiply = [&](const Buffer &b, int next, const Buffer &into) __attribute__((always_inline)) {
         if constexpr (NBUF == 2) {
             request(next, into);
@@ -606,9 +607,9 @@ __global__ __launch_bounds__(64 * WT * WN * WK, (WT * WN * WK * PERCU + 3) / 4) 
 }
 
 static LinearMode linear_mode(const LinearDims &d) {
-    // The 8-bit instruction cuts the 32 products of a block off at 2^-13 of the largest, whatever is left
-    // of them: with one product of 2688 that another cancels, others of up to 0.3 came to nothing. Its
-    // products are a caller's choice, for bfloat16 results; others come from widened values.
+    // The 8-bit instruction cuts the 32 products of a block off at 2^-13 of the largest: where a product of
+    // 2688 was cancelled by another, results of up to 0.6 came out as 0. It is a caller's choice, for
+    // bfloat16 results; others come from widened values.
     return !d.e4m3 ? kSixteen : d.cut && d.out_bf16 ? kEight : kWidened;
 }
 
